@@ -24,6 +24,16 @@ Complex-pole variants (log_poles / residues complex64 (D, N), states
 complex64 (B, D, N)): modal_filter_cpx, fftconv_fwd_cpx, chunk_fwd_cpx,
 modal_decode_cpx.
 
+The serving step around the mixers (submodule serving):
+  add_rmsnorm(x, weight, residual=None, eps=1e-6)        -> (y, residual_out)
+  add_rmsnorm_fp8(x, weight, residual=None, eps=1e-6, group=0)
+                                                         -> (q, scale, residual_out)
+  page_map(old_lens, new_lens, block_table, free_pages, free_head, page_size, T)
+                                       -> (cu, lens, positions, slots, status)
+  kv_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale)      (in place)
+  attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu,
+                 max_q, scale=None)                                   -> out
+
 Every function is also available under the C name (hyena_fftconv_fwd, ...),
 and the submodule hyena_op gives the four core calls the short names
 fftconv, fir, chunk and modal_filter.
@@ -42,6 +52,8 @@ __all__ = [
     "modal_decode", "fir_fwd_window",
     "modal_filter_cpx", "fftconv_fwd_cpx", "chunk_fwd_cpx", "modal_decode_cpx",
     "chunk_fwd_tokmajor", "chunk_tokmajor_workspace_size", "fir_fwd_tokmajor",
+    "add_rmsnorm", "add_rmsnorm_fp8", "page_map", "kv_append_fp8",
+    "attn_paged_fp8", "attn_paged_workspace_size",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_LAUNCH",
     "F32", "BF16", "ALGOS", "EXPORTS",
 ]
@@ -95,6 +107,18 @@ EXPORTS = {
     "hyena_chunk_tokmajor_workspace_size": (_size, [_i64, _i64, _i64, _i64, _int]),
     "hyena_fir_fwd_tokmajor": (_int, [_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _p,
                                       _i64, _p, _p, _p, _p, _i64, _i64, _i64, _int, _p]),
+    "hyena_add_rmsnorm": (_int, [_p, _i64, _p, _i64, _p, ctypes.c_float, _p, _i64, _p, _i64, _i64,
+                                 _i64, _int, _p]),
+    "hyena_add_rmsnorm_fp8": (_int, [_p, _i64, _p, _i64, _p, ctypes.c_float, _p, _p, _i64, _p,
+                                     _i64, _i64, _i64, _int, _p]),
+    "hyena_page_map": (_int, [_p, _p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p,
+                              _i64, _p, _p]),
+    "hyena_kv_append_fp8": (_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64,
+                                   _i64, _i64, _i64, _int, _p]),
+    "hyena_attn_paged_fp8": (_int, [_p, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _p, _i64, _i64,
+                                    _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, ctypes.c_float,
+                                    _p, _int, _p, _size, _p]),
+    "hyena_attn_paged_workspace_size": (_size, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
 }
 
 
@@ -560,6 +584,9 @@ def fir_fwd_tokmajor(xin, taps, skip=None, window_in=None, pos=(0, 1, 2), out=No
     return y, window_out
 
 
+from .serving import (add_rmsnorm, add_rmsnorm_fp8, page_map, kv_append_fp8,  # noqa: E402
+                      attn_paged_fp8, attn_paged_workspace_size)
+
 # The same functions under the names of the C entry points they call
 # (chunk_fwd / chunk_fwd_cpx call the *_algo entry point when algo is not
 # "auto").
@@ -578,6 +605,12 @@ hyena_modal_decode_cpx = modal_decode_cpx
 hyena_chunk_fwd_tokmajor = chunk_fwd_tokmajor
 hyena_chunk_tokmajor_workspace_size = chunk_tokmajor_workspace_size
 hyena_fir_fwd_tokmajor = fir_fwd_tokmajor
+hyena_add_rmsnorm = add_rmsnorm
+hyena_add_rmsnorm_fp8 = add_rmsnorm_fp8
+hyena_page_map = page_map
+hyena_kv_append_fp8 = kv_append_fp8
+hyena_attn_paged_fp8 = attn_paged_fp8
+hyena_attn_paged_workspace_size = attn_paged_workspace_size
 __all__ += [n for n in list(globals()) if n.startswith("hyena_") and callable(globals()[n])]
 
 from . import hyena_op  # noqa: E402,F401  (short names of the four core calls)

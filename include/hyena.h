@@ -105,6 +105,12 @@ typedef enum hyena_chunk_algo {
 #define HYENA_MAX_FFT_LEN (1 << 20)      /* single-pass FFT length, next pow2 >= 2L */
 #define HYENA_MAX_FFT_CHUNK 8192         /* C for HYENA_CHUNK_FFT (FFT length 2C <= 16384) */
 #define HYENA_NOALLOC_SCRATCH_BYTES (64u << 20)  /* device scratch of hyena_fftconv_fwd_noalloc */
+#define HYENA_MAX_NORM_DIM 32768         /* D of hyena_add_rmsnorm(_fp8) */
+#define HYENA_NORM_GROUP 128             /* columns that share a scale in hyena_add_rmsnorm_fp8's grouped form */
+#define HYENA_MIN_PAGE 16                /* tokens per cache page: a power of two in */
+#define HYENA_MAX_PAGE 256               /* [HYENA_MIN_PAGE, HYENA_MAX_PAGE] */
+#define HYENA_MAX_REQUESTS 4096          /* requests per serving step */
+#define HYENA_MAX_HEADS 1024             /* attention heads */
 
 int hyena_abi_version(void);
 const char* hyena_status_string(hyena_status_t status);
@@ -436,6 +442,148 @@ hyena_status_t hyena_chunk_fwd_tokmajor_algo(const void* xin, int32_t pos_x1, in
  * known here.) */
 size_t hyena_chunk_tokmajor_workspace_size(int64_t B, int64_t D, int64_t L, int64_t N,
                                            hyena_dtype_t io);
+
+/* ------------------------------------------------------------------------
+ * The serving step around the mixers: the norm in front of an 8-bit in_proj,
+ * and the paged 8-bit K/V cache of the striped attention blocks (its tables,
+ * the append and the attention that reads it).
+ *
+ * Activations here are token-major rows with strides in ELEMENTS, which need
+ * no alignment beyond their element's; the innermost axis is contiguous.
+ * 8-bit values are e4m3 (4-bit exponent, 3-bit mantissa, largest value 448, no
+ * infinities), one byte each.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * hyena_add_rmsnorm -- residual addition and root-mean-square norm.
+ *   s = x + residual,   y = s / sqrt(mean(s^2) + eps) * weight,
+ *   residual_out = s,
+ * per row of D columns, in fp32; y and residual_out are rounded once each.
+ * The pre / post norms of a block: evo2_flash README, layer_names table.
+ *   x, residual  : T rows of D `io`, row strides x_stride, residual_stride >= 0
+ *                  (0 repeats a row); residual NULL: s = x
+ *   weight       : (D) fp32, or NULL (1)
+ *   y            : T rows of D `io`, row stride y_stride >= D; may be x
+ *   residual_out : T rows of D `io`, or NULL (not kept); may be residual or x
+ *                  (rows of equal stride); needs a residual
+ *   eps          : finite, >= 0
+ * Rows whose squares leave fp32 (|s| ~ 1e18 and more) are scaled first; a NaN
+ * or infinity makes its own row NaN.  D <= HYENA_MAX_NORM_DIM.
+ */
+hyena_status_t hyena_add_rmsnorm(const void* x, int64_t x_stride, const void* residual,
+                                 int64_t residual_stride, const float* weight, float eps, void* y,
+                                 int64_t y_stride, void* residual_out,
+                                 int64_t residual_out_stride, int64_t T, int64_t D,
+                                 hyena_dtype_t io, hipStream_t stream);
+
+/*
+ * hyena_add_rmsnorm_fp8 -- the same with y in e4m3 and scales, the form an
+ * 8-bit in_proj takes (evo2_flash README, layer_names table:
+ * 'blocks.N.projections').
+ *   scale = max|y| / 448 over the run (1 where that is 0 or NaN),
+ *   q = e4m3(y / scale),  y ~ q * scale.
+ *   q       : (T, D) e4m3, contiguous
+ *   q_scale : fp32; group = 0: one run per row, (T); group = HYENA_NORM_GROUP:
+ *             runs of 128 columns (the last one shorter), (T, ceil(D / 128))
+ */
+hyena_status_t hyena_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual,
+                                     int64_t residual_stride, const float* weight, float eps,
+                                     uint8_t* q, float* q_scale, int64_t group,
+                                     void* residual_out, int64_t residual_out_stride, int64_t T,
+                                     int64_t D, hyena_dtype_t io, hipStream_t stream);
+
+/*
+ * hyena_page_map -- the tables of one serving step, from request lengths.
+ * Request r has old_lens[r] cached tokens and brings new_lens[r] (>= 0) more;
+ * its token at position p belongs in page block_table[r][p / page_size].
+ *   lens[r] = old + new;  cu[r] = new tokens of the requests before r
+ *   pages(n) = min(ceil(n / page_size), max_pages)
+ *   pages(old) .. pages(lens) - 1 of request r get the next free pages, in the
+ *   order of the requests: free_pages[*free_head ...]
+ *   new token t = cu[r] + i:  positions[t] = old + i,
+ *   slots[t] = page * page_size + positions[t] mod page_size
+ *   block_table  : (R, max_pages) int32, row stride table_stride >= max_pages;
+ *                  entries of new pages are written, others are kept
+ *   free_pages   : (num_free) int32;  free_head : (1) int32, or NULL (0)
+ *   cu           : (R + 1) int32, written;  lens : (R) int32, written
+ *   positions    : (T) int32, written, or NULL;  slots : (T) int64, written
+ *   status       : (2) int32, written: the free list's new head, and the count
+ *                  of new tokens that found no page (free list or table at its
+ *                  end; their slots are -1)
+ * T is the size of positions and slots: entries past cu[R] get -1 (a fixed T
+ * can be captured in a graph), tokens past T get none.  Outputs must not
+ * overlap the inputs.  Negative lengths count as 0.  R <= HYENA_MAX_REQUESTS.
+ */
+hyena_status_t hyena_page_map(const int32_t* old_lens, const int32_t* new_lens, int64_t R,
+                              int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                              const int32_t* free_pages, int64_t num_free,
+                              const int32_t* free_head, int64_t page_size, int32_t* cu,
+                              int32_t* lens, int32_t* positions, int64_t* slots, int64_t T,
+                              int32_t* status, hipStream_t stream);
+
+/*
+ * hyena_kv_append_fp8 -- new keys and values into the 8-bit cache (the fp8 KV
+ * cache: evo2_flash README, options).
+ *   k_cache : (num_pages, H, page_size, DH) e4m3;  v_cache : (num_pages, H, DH,
+ *   page_size) e4m3;  k_scale, v_scale : (num_pages, H) fp32, all contiguous,
+ *   the caches 16-byte aligned.  A code stands for code * scale of its block (a
+ *   page of a head); scales are powers of two.
+ *   k, v  : (T, H, DH) `io` with token and head strides >= 0
+ *   slots : (T) int64, page * page_size + place; negative or beyond the cache:
+ *           the token is not stored
+ * Per block, with a = the largest finite magnitude of the tokens that the call
+ * writes into it and s1 = 2^ceil(log2(a / 448)) (at least 2^-96): the scale
+ * becomes s1 where the call writes place 0, else max(scale, s1), the codes of
+ * the places before the first written one times old / new scale; new codes are
+ * e4m3(x / scale).  A token with a non-finite key or value gets a NaN key and
+ * zeros for its non-finite values: it makes NaN of the queries that see it and
+ * of no others.
+ * The tokens of one page must stand together in the call, in the order of
+ * their places (as hyena_page_map gives them); two requests must not share a
+ * page that is written.  DH 64 or 128.
+ */
+hyena_status_t hyena_kv_append_fp8(const void* k, int64_t k_tok_stride, int64_t k_head_stride,
+                                   const void* v, int64_t v_tok_stride, int64_t v_head_stride,
+                                   const int64_t* slots, uint8_t* k_cache, uint8_t* v_cache,
+                                   float* k_scale, float* v_scale, int64_t num_pages,
+                                   int64_t page_size, int64_t T, int64_t H, int64_t DH,
+                                   hyena_dtype_t io, hipStream_t stream);
+
+/*
+ * hyena_attn_paged_fp8 -- causal attention of the new tokens over the cache,
+ * single tokens and chunks in one ragged call (attention blocks: evo2_flash
+ * README, layer_names table; Evo2-7B-262K model card, Architecture).
+ * Request r has query tokens cu[r] .. cu[r+1] - 1 of q and lens[r] cached
+ * tokens, the queries' own included; query i stands at position
+ * pos = lens[r] - (cu[r+1] - cu[r]) + i:
+ *   out = sum_{j <= pos} softmax_j(scale * q . k_j) v_j,  0 where pos < 0.
+ *   q    : (T, Hq, DH) `io`, strides >= 0;  out : (T, Hq, DH) `io`, contiguous
+ *   Hq a multiple of Hkv; query head h reads K/V head h / (Hq / Hkv)
+ *   caches and scales : as hyena_kv_append_fp8 writes them, H = Hkv
+ *   block_table : (R, max_pages) int32, row stride table_stride; entries out of
+ *                 [0, num_pages) hide their tokens; lens beyond the table are
+ *                 cut to it
+ *   cu (R + 1), lens (R) : int32
+ *   max_q : no request has more queries (rows past it are not written)
+ * Rows of q past cu[R] are not read, nor written in out.  Softmax statistics
+ * and sums are fp32; for bf16 activations the weights are rounded to bf16 for
+ * the second product, for fp32 both products carry fp32.  Nothing past a
+ * request's length reaches the result, whatever the cache holds there.
+ * Workspace (device, 16-byte aligned, no initial contents) of
+ * hyena_attn_paged_workspace_size bytes; NULL, short or misaligned when one is
+ * needed -> HYENA_ERR_WORKSPACE.
+ */
+hyena_status_t hyena_attn_paged_fp8(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                    const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const float* k_scale, const float* v_scale, int64_t num_pages,
+                                    int64_t page_size, const int32_t* block_table,
+                                    int64_t table_stride, int64_t max_pages, const int32_t* lens,
+                                    const int32_t* cu, int64_t R, int64_t T, int64_t max_q,
+                                    int64_t Hq, int64_t Hkv, int64_t DH, float scale, void* out,
+                                    hyena_dtype_t io, void* workspace, size_t ws_bytes,
+                                    hipStream_t stream);
+size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int64_t max_pages,
+                                       int64_t page_size, int64_t Hq, int64_t Hkv, int64_t DH);
 
 #ifdef __cplusplus
 }
