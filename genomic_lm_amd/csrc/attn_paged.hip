@@ -26,20 +26,31 @@ namespace hyena {
 constexpr float AT_LOG2E = 1.44269504088896340736f;
 constexpr float AT_NEG = -__builtin_inff();
 
+// Two kernels share the calls' requests by their columns (queries times group):
+//   attn_paged_kernel: up to 16 columns, one MFMA tile wide, bound by reading the
+//     cache: four waves on different tiles of the same unit;
+//   attn_wide_kernel: more columns, bound by the matrix cores: four waves on 32
+//     columns each, tiles widened to bf16 once per workgroup in LDS.
+
 // ---------------------------------------------------------------- work split
 // A unit is NT columns of one request on one K/V head; its tokens are cut into
-// pieces of `piece` 64-token tiles, the same for all requests and chosen so
-// that about AT_TARGET pieces exist: every workgroup then has about the same
+// pieces of `tiles` 64-token tiles, the same for all requests and chosen so
+// that about `target` pieces exist: every workgroup then has about the same
 // work however the lengths differ, and a single long sequence fills the chip.
 // A unit of several pieces leaves partial results in the workspace, one slot
 // per piece and head, which attn_join_kernel adds up; a unit of one piece
 // writes its rows directly.
 constexpr int AT_T = 256;                 // threads
 constexpr int AT_TILE = 64;               // cached tokens per tile
-constexpr int AT_NT = 16;                 // columns per unit
+constexpr int AT_MIN_PIECE = 4;           // tiles
+constexpr int AT_NARROW = 16;             // columns up to which a request is narrow
+constexpr int AT_NT = 16;                 // columns per unit, narrow
+constexpr int AT_WNT = 128;               // and wide
 constexpr int AT_TARGET = 2048;           // pieces aimed at
-constexpr int AT_MIN_PIECE = 4;           // tiles: one per wave
-constexpr int AT_SLOTS = 2 * AT_TARGET;   // a unit of x > 1 pieces worth of work is cut into < 2 x
+constexpr int AT_WTARGET = 512;
+// a unit worth x > 1 pieces is cut into fewer than 2 x
+constexpr int AT_SLOTS = 2 * AT_TARGET;
+constexpr int AT_WSLOTS = 2 * AT_WTARGET;
 
 struct AttnWork {
   int tok0, queries, len;    // the request: first query token, queries (up to max_q), cached tokens
@@ -64,22 +75,19 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, 
   len = static_cast<int>(min<int64_t>(max(a.lens[r], 0), cap));
 }
 
-__device__ __forceinline__ int wave_sum_i(int x) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
-// Finds the work of item `item`; false if there is none.  Every thread of the
-// workgroup takes part.  total_slots: slots in use per head.
-__device__ __forceinline__ bool find_work(const AttnArgs& a, int item, AttnShared& sh, AttnWork& w,
-                                          int& total_slots) {
+// Finds the work of item `item` among the requests of more than `lo` and at
+// most `hi` columns; false if there is none.  Every thread of the workgroup
+// takes part.  total_slots: slots in use per head.
+template <int NT, int TARGET>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int hi, int item, AttnShared& sh,
+                                          AttnWork& w, int& total_slots) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = a.Hq / a.Hkv;
   const int run = (a.R + AT_T - 1) / AT_T;
   const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
   auto units_of = [&](int queries) {
-    return static_cast<int>((static_cast<int64_t>(queries) * group + AT_NT - 1) / AT_NT);
+    const int64_t cols = static_cast<int64_t>(queries) * group;
+    return cols > lo && cols <= hi ? static_cast<int>((cols + NT - 1) / NT) : 0;
   };
   auto tiles_of = [](int len) { return (len + AT_TILE - 1) / AT_TILE; };
 
@@ -98,7 +106,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, AttnShare
   work = 0;
 #pragma unroll
   for (int i = 0; i < AT_T / 64; ++i) work += sh.part[i];
-  const unsigned long long even = (work * a.Hkv + AT_TARGET - 1) / AT_TARGET;
+  const unsigned long long even = (work * a.Hkv + TARGET - 1) / TARGET;
   const int tiles = static_cast<int>(even > AT_MIN_PIECE ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_MIN_PIECE);
   auto pieces_of = [&](int len) {
     const int n = tiles_of(len);
@@ -169,20 +177,24 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, AttnShare
 }
 
 // ---------------------------------------------------------------- workspace
-// int4 header, int4 per slot, then m, l (AT_NT each) and O (AT_NT x DH) per slot
+// per kernel: the count of slots in use, a header per slot, then m, l (NT each)
+// and O (NT x DH) per slot
 struct AttnSpace {
-  int* used;                 // slots in use
+  int* used;
   int4* head;                // pieces (0: not a unit's first), first query token, first column, columns
   float* ml;
   float* o;
 };
-__host__ __device__ __forceinline__ AttnSpace attn_space(void* p) {
+__host__ __device__ __forceinline__ AttnSpace attn_space(void* p, int nt, int slots) {
   AttnSpace s;
   s.used = static_cast<int*>(p);
   s.head = reinterpret_cast<int4*>(p) + 1;
-  s.ml = reinterpret_cast<float*>(s.head + AT_SLOTS);
-  s.o = s.ml + AT_SLOTS * 2 * AT_NT;
+  s.ml = reinterpret_cast<float*>(s.head + slots);
+  s.o = s.ml + static_cast<size_t>(slots) * 2 * nt;
   return s;
+}
+constexpr size_t attn_space_bytes(int nt, int slots, int DH) {
+  return 16 + static_cast<size_t>(slots) * (16 + 4 * (2 * nt + nt * DH));
 }
 
 // ---------------------------------------------------------------- operands
@@ -238,7 +250,7 @@ __device__ __forceinline__ uint32_t keep_places(uint32_t w, int at, int n) {
 // + i % 4, so that C's rows 4 g + r of the four sub-tiles are the run's tokens
 // 4 t + r, in order.
 template <typename IO, int DH>
-__global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a) {
+__global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
   constexpr int KH = DH / 64;            // 16-byte loads per K row and lane
   constexpr int KS = DH / 32;            // MFMA steps over the head dimension
@@ -253,10 +265,10 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a) {
   const int head = static_cast<int>(blockIdx.x % a.Hkv);
   const int item = static_cast<int>(blockIdx.x / a.Hkv);
   const int group = a.Hq / a.Hkv;
-  const AttnSpace ws = attn_space(a.workspace);
+  const AttnSpace ws = attn_space(a.workspace, AT_NT, AT_SLOTS);
   AttnWork w;
   int total_slots;
-  const bool have = find_work(a, item, sh, w, total_slots);
+  const bool have = find_work<AT_NT, AT_TARGET>(a, 0, hi, item, sh, w, total_slots);
   if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = total_slots * a.Hkv;
   if (!have) return;
 
@@ -448,11 +460,281 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- wide units
+// S^T and O^T of 32 columns per wave on 32x32x16 MFMAs.  Lane l: i = l % 32 its
+// row of A and column of B and C, hf = l / 32 its half.  Row i of a 32-token
+// half tile is token 16 ((i / 4) % 2) + 4 (i / 8) + i % 4, so that C's rows of
+// half hf are the 16 consecutive tokens 16 hf .. + 15, in order: the operand of
+// the second product, whose k index runs over tokens of one half the same way.
+//
+// A tile is read once per workgroup (16 bytes per thread and step), widened to
+// bf16 and kept in LDS for the four waves, in two buffers: tile t + 1 is in
+// flight from HBM while tile t is multiplied, and written to the other buffer
+// after it.  16-byte pieces of a row are permuted by the row's number so that
+// lanes on consecutive rows read different banks.
+constexpr float AT_SLACK = 8.0f;      // how far (log2) scores may pass the reference before O is rescaled
+
+template <typename IO, int DH>
+__global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo) {
+  constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
+  constexpr int KS = DH / 16;            // MFMA steps over the head dimension
+  constexpr int DT = DH / 32;            // 32-row tiles of O^T
+  constexpr int KC = DH / 8;             // 16-byte pieces of a K row in LDS
+  constexpr int STEPS = DH / 64;         // 16-byte loads per thread of K, and of V
+  __shared__ AttnShared sh;
+  __shared__ __align__(16) u32x4 s_k[2][AT_TILE * KC];
+  __shared__ __align__(16) u32x4 s_v[2][DH * 8];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int i = lane & 31, hf = lane >> 5;
+  const int head = static_cast<int>(blockIdx.x % a.Hkv);
+  const int item = static_cast<int>(blockIdx.x / a.Hkv);
+  const int group = a.Hq / a.Hkv;
+  void* space = a.workspace ? static_cast<char*>(a.workspace) + attn_space_bytes(AT_NT, AT_SLOTS, DH) : nullptr;
+  const AttnSpace ws = attn_space(space, AT_WNT, AT_WSLOTS);
+  AttnWork w;
+  int total_slots;
+  const bool have = find_work<AT_WNT, AT_WTARGET>(a, lo, 0x7FFFFFFF, item, sh, w, total_slots);
+  if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = total_slots * a.Hkv;
+  if (!have) return;
+
+  const int cols = w.queries * group;
+  // the units that see most tokens first
+  const int units = (cols + AT_WNT - 1) / AT_WNT;
+  const int unit = units - 1 - w.unit;
+  const int c0 = unit * AT_WNT;
+  const int wc = c0 + wave * 32;                             // the wave's first column
+  const int col = wc + i;
+  const bool live = col < cols;
+  const int qi = live ? col / group : 0, qh = live ? col % group : 0;
+  const int pos = live ? w.ahead + qi : -1;
+  const int first_pos = w.ahead + wc / group;                // of the wave's first column
+  const int wave_seen = wc < cols ? max(w.ahead + (min(wc + 32, cols) - 1) / group + 1, 0) : 0;
+  const int seen = max(w.ahead + (min(c0 + AT_WNT, cols) - 1) / group + 1, 0);
+  const int t_begin = w.piece * w.tiles;
+  const int t_end = min((seen + AT_TILE - 1) / AT_TILE, t_begin + w.tiles);
+  const int t_wave = min((wave_seen + AT_TILE - 1) / AT_TILE, t_end);
+
+  // queries, with the sign of the scale so that scores only grow with them
+  bf16x8 qf[KS][NS];
+  {
+    const IO* qp = static_cast<const IO*>(a.q) + (w.tok0 + qi) * a.q_tok +
+                   (static_cast<int64_t>(head) * group + qh) * a.q_head;
+    const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      float x[8] = {};
+      if (live) load8(qp + 16 * s + 8 * hf, 8, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= sign;
+      parts<NS>(x, qf[s]);
+    }
+  }
+  const float scale2 = fabsf(a.scale) * AT_LOG2E;
+
+  const int lg = a.page_lg, pmask = (1 << lg) - 1;
+  const int64_t page_bytes = (static_cast<int64_t>(a.Hkv) << lg) * DH;
+  const int64_t head_off = (static_cast<int64_t>(head) << lg) * DH;
+  const int32_t* table = a.block_table + w.r * a.table_stride;
+  auto page_of = [&](int tok) {
+    const int j = tok >> lg;
+    const int p = tok < w.len && j < a.max_pages ? table[j] : -1;
+    return p >= 0 && p < a.num_pages ? p : -1;
+  };
+
+  // ---- staging: step u of a thread is row kr + u KROWS of K (16 dimensions from
+  // 16 kc) and row vd + 64 u of V^T (16 tokens from 16 vc)
+  constexpr int KP = DH / 16;            // 16-code pieces of a K row
+  constexpr int KROWS = AT_T / KP;
+  const int kr = tid / KP, kc = tid % KP;
+  const int vd = tid >> 2, vc = tid & 3;
+  u32x4 rk[STEPS], rv[STEPS];
+  int pk[STEPS], pv;
+  auto pages_of = [&](int tile) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) pk[u] = page_of(tile * AT_TILE + ((kr + u * KROWS) & ~15));
+    pv = page_of(tile * AT_TILE + 16 * vc);
+  };
+  auto fetch = [&](int tile) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int tok = tile * AT_TILE + kr + u * KROWS;
+      rk[u] = *reinterpret_cast<const u32x4*>(a.k_cache + max(pk[u], 0) * page_bytes + head_off +
+                                              (tok & pmask) * DH + 16 * kc);
+      rv[u] = *reinterpret_cast<const u32x4*>(a.v_cache + max(pv, 0) * page_bytes + head_off +
+                                              (static_cast<int64_t>(vd + 64 * u) << lg) +
+                                              ((tile * AT_TILE + 16 * vc) & pmask));
+    }
+    // places of this thread's V run that hold tokens: the rest must not reach
+    // the product (0 * NaN)
+    const int n = pv >= 0 ? w.len - (tile * AT_TILE + 16 * vc) : 0;
+    if (n < 16) {
+#pragma unroll
+      for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rv[u][e] = keep_places(rv[u][e], e, n);
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int row = kr + u * KROWS;                        // token of the tile
+      const int at = (row & 32) | (8 * ((row >> 2) & 3)) | (4 * ((row >> 4) & 1)) | (row & 3);
+      u32x4* kd = s_k[buf] + at * KC;
+      kd[(2 * kc) ^ (at & (KC - 1))] = __builtin_bit_cast(u32x4, widen(rk[u][0], rk[u][1]));
+      kd[(2 * kc + 1) ^ (at & (KC - 1))] = __builtin_bit_cast(u32x4, widen(rk[u][2], rk[u][3]));
+      const int d = vd + 64 * u;
+      u32x4* vdst = s_v[buf] + d * 8;
+      vdst[(2 * vc) ^ (d & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][0], rv[u][1]));
+      vdst[(2 * vc + 1) ^ (d & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][2], rv[u][3]));
+    }
+  };
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+  float m = AT_NEG, l = 0.0f;
+
+  if (t_begin < t_end) {
+    pages_of(t_begin);
+    fetch(t_begin);
+    stage(0);
+    if (t_begin + 1 < t_end) pages_of(t_begin + 1);
+  }
+  __syncthreads();
+  for (int tile = t_begin; tile < t_end; ++tile) {
+    const int buf = (tile - t_begin) & 1;
+    const bool more = tile + 1 < t_end;
+    if (more) {
+      fetch(tile + 1);
+      if (tile + 2 < t_end) pages_of(tile + 2);
+    }
+    if (tile < t_wave) {
+      // scales and places of this lane's two runs
+      float c[2], vl[2], iv[2];
+      int places[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int run = tile * AT_TILE + 32 * h + 16 * hf;
+        const int p = page_of(run);
+        const int64_t si = static_cast<int64_t>(max(p, 0)) * a.Hkv + head;
+        places[h] = p >= 0 ? min(w.len - run, 16) : 0;
+        c[h] = a.k_scale[si] * scale2;
+        const float vs = a.v_scale[si];
+        vl[h] = p >= 0 ? __builtin_amdgcn_logf(vs) : AT_NEG;
+        iv[h] = p >= 0 ? 1.0f / vs : 0.0f;
+      }
+      f32x16 s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[h][r] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int row = 32 * h + i;
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, s_k[buf][row * KC + ((2 * k + hf) ^ (row & (KC - 1)))]);
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) s[h] = mfma(kf, qf[k][n], s[h]);
+        }
+      }
+      const bool masked = __any(places[0] < 16 || places[1] < 16) ||
+                          tile * AT_TILE + AT_TILE - 1 > first_pos;
+      float top = AT_NEG;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (masked) {
+          const int lim = min(places[h], pos - (tile * AT_TILE + 32 * h + 16 * hf) + 1);
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (r >= lim) s[h][r] = AT_NEG;
+        }
+        float t = s[h][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) t = fmaxf(t, s[h][r]);
+        // a masked score times a scale of 0, or times what stands for no page, would be NaN
+        top = fmaxf(top, t == AT_NEG ? AT_NEG : t * c[h]);
+      }
+      top = fmaxf(top, xor32(top, hf));
+      if (__any(top > m + AT_SLACK || (m == AT_NEG && top > m))) {
+        const float m_new = fmaxf(m, top);
+        const float f = m_new == AT_NEG ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] *= f;
+        m = m_new;
+      }
+      const float base = m == AT_NEG ? 0.0f : m;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float off = vl[h] - base;
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = s[h][8 * q + e];
+            p[e] = __builtin_amdgcn_exp2f(masked && x == AT_NEG ? AT_NEG : fmaf(x, c[h], off));
+            sum += p[e];
+          }
+          bf16x8 pf[NS];
+          parts<NS>(p, pf);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const int row = 32 * d + i;
+            const bf16x8 vf = __builtin_bit_cast(bf16x8, s_v[buf][row * 8 + ((4 * h + 2 * hf + q) ^ (row & 7))]);
+#pragma unroll
+            for (int n = NS - 1; n >= 0; --n) o[d] = mfma(vf, pf[n], o[d]);
+          }
+        }
+        l = fmaf(sum, iv[h], l);
+      }
+    }
+    if (more) stage(buf ^ 1);
+    __syncthreads();
+  }
+
+  l += xor32(l, hf);
+  if (!live) return;
+  if (w.pieces == 1) {
+    IO* op = static_cast<IO*>(a.out) +
+             ((static_cast<int64_t>(w.tok0) + qi) * a.Hq + static_cast<int64_t>(head) * group + qh) * DH;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        // rows 8 b + 4 hf .. + 3 of the 32
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Io<IO>::st(op, 32 * d + 8 * b + 4 * hf + r, o[d][4 * b + r] * inv);
+      }
+  } else {
+    const int64_t slot = static_cast<int64_t>(w.slot + w.piece) * a.Hkv + head;
+    if (tid == 0) ws.head[slot] = make_int4(w.piece == 0 ? w.pieces : 0, w.tok0, c0, min(AT_WNT, cols - c0));
+    const int oc = wave * 32 + i;
+    if (hf == 0) {
+      ws.ml[slot * 2 * AT_WNT + oc] = m;
+      ws.ml[slot * 2 * AT_WNT + AT_WNT + oc] = l;
+    }
+    float* op = ws.o + (slot * AT_WNT + oc) * DH;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<f32x4*>(op + 32 * d + 8 * b + 4 * hf) =
+            f32x4{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
+  }
+}
+
 // Joins the pieces of each unit that has several: one workgroup per slot, at
 // work where the slot is its unit's first.
 template <typename IO, int DH>
-__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a) {
-  const AttnSpace ws = attn_space(a.workspace);
+__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, size_t skip, int nt, int slots) {
+  const AttnSpace ws = attn_space(static_cast<char*>(a.workspace) + skip, nt, slots);
   const int64_t slot = blockIdx.x;
   if (slot >= *ws.used) return;
   const int4 h = ws.head[slot];
@@ -461,14 +743,14 @@ __global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a) {
   for (int i = threadIdx.x; i < h.w * DH; i += AT_T) {
     const int c = i / DH, d = i % DH;
     float big = AT_NEG;
-    for (int p = 0; p < h.x; ++p) big = fmaxf(big, ws.ml[(slot + static_cast<int64_t>(p) * a.Hkv) * 2 * AT_NT + c]);
+    for (int p = 0; p < h.x; ++p) big = fmaxf(big, ws.ml[(slot + static_cast<int64_t>(p) * a.Hkv) * 2 * nt + c]);
     float sum = 0.0f, acc = 0.0f;
     for (int p = 0; p < h.x; ++p) {
       const int64_t s = slot + static_cast<int64_t>(p) * a.Hkv;
-      const float mk = ws.ml[s * 2 * AT_NT + c];
+      const float mk = ws.ml[s * 2 * nt + c];
       const float f = mk == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(mk - big);
-      sum = fmaf(f, ws.ml[s * 2 * AT_NT + AT_NT + c], sum);
-      acc = fmaf(f, ws.o[(s * AT_NT + c) * DH + d], acc);
+      sum = fmaf(f, ws.ml[s * 2 * nt + nt + c], sum);
+      acc = fmaf(f, ws.o[(s * nt + c) * DH + d], acc);
     }
     const int cc = h.z + c;
     IO* op = static_cast<IO*>(a.out) +
@@ -478,11 +760,11 @@ __global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-static int64_t most_units(int64_t R, int64_t T, int64_t max_q, int64_t group) {
+static int64_t most_units(int64_t R, int64_t T, int64_t max_cols, int64_t group, int64_t nt) {
   // ceil per request: at most one unit more than its columns' share, and at
-  // most the units of max_q queries
-  const int64_t share = T * group / AT_NT + R;
-  const int64_t each = R * ((max_q * group + AT_NT - 1) / AT_NT);
+  // most the units of max_cols columns
+  const int64_t share = T * group / nt + R;
+  const int64_t each = R * ((max_cols + nt - 1) / nt);
   return share < each ? share : each;
 }
 
@@ -490,36 +772,57 @@ static bool may_split(int64_t max_pages, int page_lg) {
   return (max_pages << page_lg) > AT_MIN_PIECE * AT_TILE;
 }
 
-static int64_t grid_of(int64_t R, int64_t T, int64_t max_q, int64_t max_pages, int page_lg,
-                       int64_t Hq, int64_t Hkv) {
-  const int64_t units = most_units(R, T, max_q, Hq / Hkv);
-  return (units + (may_split(max_pages, page_lg) ? AT_TARGET / Hkv + 1 : 0)) * Hkv;
+struct AttnGrids {
+  bool split;
+  int64_t narrow, wide;      // workgroups; 0: not launched
+  int limit;                 // a request of up to so many columns is narrow
+};
+
+static AttnGrids grids_of(int64_t R, int64_t T, int64_t max_q, int64_t max_pages, int page_lg,
+                          int64_t Hq, int64_t Hkv) {
+  const int64_t group = Hq / Hkv, cols = max_q * group;
+  AttnGrids g{};
+  g.split = may_split(max_pages, page_lg);
+  // a request of its own is wide if it may be: one launch
+  const bool wide = cols > AT_NARROW;
+  g.limit = wide && R == 1 ? 0 : AT_NARROW;
+  if (wide)
+    g.wide = (most_units(R, T, cols, group, AT_WNT) + (g.split ? AT_WTARGET / Hkv + 1 : 0)) * Hkv;
+  if (g.limit)
+    g.narrow = (most_units(R, T, cols < AT_NARROW ? cols : AT_NARROW, group, AT_NT) +
+                (g.split ? AT_TARGET / Hkv + 1 : 0)) * Hkv;
+  return g;
 }
 
 bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t max_pages, int page_lg,
                      int64_t Hq, int64_t Hkv) {
-  return grid_of(R, T, max_q, max_pages, page_lg, Hq, Hkv) < (int64_t(1) << 32) / AT_T;
+  const AttnGrids g = grids_of(R, T, max_q, max_pages, page_lg, Hq, Hkv);
+  constexpr int64_t most = (int64_t(1) << 32) / AT_T;
+  return g.narrow < most && g.wide < most;
 }
 
-size_t attn_paged_workspace(int64_t max_pages, int page_lg, int DH) {
+size_t attn_paged_workspace(int64_t max_q, int64_t max_pages, int page_lg, int64_t Hq, int64_t Hkv,
+                            int DH) {
   if (!may_split(max_pages, page_lg)) return 0;
-  return 16 + static_cast<size_t>(AT_SLOTS) * (16 + 4 * (2 * AT_NT + AT_NT * DH));
+  return attn_space_bytes(AT_NT, AT_SLOTS, DH) +
+         (max_q * (Hq / Hkv) > AT_NARROW ? attn_space_bytes(AT_WNT, AT_WSLOTS, DH) : 0);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a) {
-  const bool split = may_split(a.max_pages, a.page_lg);
-  const unsigned grid = static_cast<unsigned>(
-      grid_of(a.R, a.T, a.max_q, a.max_pages, a.page_lg, a.Hq, a.Hkv));
-  auto go = [&](auto kernel, auto join) {
-    kernel<<<grid, AT_T, 0, a.stream>>>(a);
-    if (split) join<<<AT_SLOTS, AT_T, 0, a.stream>>>(a);
+  const AttnGrids g = grids_of(a.R, a.T, a.max_q, a.max_pages, a.page_lg, a.Hq, a.Hkv);
+  const size_t skip = attn_space_bytes(AT_NT, AT_SLOTS, a.DH);
+  auto go = [&](auto narrow, auto wide, auto join) {
+    if (g.wide) wide<<<static_cast<unsigned>(g.wide), AT_T, 0, a.stream>>>(a, g.limit);
+    if (g.narrow) narrow<<<static_cast<unsigned>(g.narrow), AT_T, 0, a.stream>>>(a, g.limit);
+    if (g.split && g.narrow) join<<<AT_SLOTS, AT_T, 0, a.stream>>>(a, 0, AT_NT, AT_SLOTS);
+    if (g.split && g.wide) join<<<AT_WSLOTS, AT_T, 0, a.stream>>>(a, skip, AT_WNT, AT_WSLOTS);
   };
   if (a.bf16) {
-    if (a.DH == 64) go(attn_paged_kernel<bf16_t, 64>, attn_join_kernel<bf16_t, 64>);
-    else go(attn_paged_kernel<bf16_t, 128>, attn_join_kernel<bf16_t, 128>);
+    if (a.DH == 64) go(attn_paged_kernel<bf16_t, 64>, attn_wide_kernel<bf16_t, 64>, attn_join_kernel<bf16_t, 64>);
+    else go(attn_paged_kernel<bf16_t, 128>, attn_wide_kernel<bf16_t, 128>, attn_join_kernel<bf16_t, 128>);
   } else {
-    if (a.DH == 64) go(attn_paged_kernel<float, 64>, attn_join_kernel<float, 64>);
-    else go(attn_paged_kernel<float, 128>, attn_join_kernel<float, 128>);
+    if (a.DH == 64) go(attn_paged_kernel<float, 64>, attn_wide_kernel<float, 64>, attn_join_kernel<float, 64>);
+    else go(attn_paged_kernel<float, 128>, attn_wide_kernel<float, 128>, attn_join_kernel<float, 128>);
   }
   return hipGetLastError();
 }

@@ -98,7 +98,8 @@ struct AttnArgs {
 // the table is too short for a request's tokens to be split).
 bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t max_pages, int page_lg,
                      int64_t Hq, int64_t Hkv);
-size_t attn_paged_workspace(int64_t max_pages, int page_lg, int DH);
+size_t attn_paged_workspace(int64_t max_q, int64_t max_pages, int page_lg, int64_t Hq, int64_t Hkv,
+                            int DH);
 hipError_t launch_attn_paged(const AttnArgs& a);
 
 }  // namespace hyena

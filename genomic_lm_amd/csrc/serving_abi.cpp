@@ -195,7 +195,7 @@ hyena_status_t hyena_attn_paged_fp8(const void* q, int64_t q_tok_stride, int64_t
   if (q_tok_stride > most / T || q_head_stride > most / Hq || !fits(T, Hq * DH * 4) ||
       !fits(table_stride, 4 * R))
     return HYENA_ERR_UNSUPPORTED;
-  const size_t need = hyena::attn_paged_workspace(max_pages, lg, static_cast<int>(DH));
+  const size_t need = hyena::attn_paged_workspace(max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
   if (need > 0 && (!workspace || ws_bytes < need || !aligned_to(workspace, 16)))
     return HYENA_ERR_WORKSPACE;
   hyena::AttnArgs n{q, q_tok_stride, q_head_stride, k_cache, v_cache, k_scale, v_scale, num_pages,
@@ -211,7 +211,7 @@ size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int6
   const int lg = page_lg(page_size);
   if (check_attn(R, T, max_q, max_pages, lg, Hq, Hkv, DH) != HYENA_OK) return 0;
   if (R == 0 || T == 0 || max_q == 0 || Hq == 0) return 0;
-  return hyena::attn_paged_workspace(max_pages, lg, static_cast<int>(DH));
+  return hyena::attn_paged_workspace(max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
 }
 
 }  // extern "C"
