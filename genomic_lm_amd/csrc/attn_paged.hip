@@ -51,6 +51,7 @@ constexpr int AT_WTARGET = 512;
 // a unit worth x > 1 pieces is cut into fewer than 2 x
 constexpr int AT_SLOTS = 2 * AT_TARGET;
 constexpr int AT_WSLOTS = 2 * AT_WTARGET;
+constexpr int AT_JOIN = 512;              // workgroups of the joining launch
 
 struct AttnWork {
   int tok0, queries, len;    // the request: first query token, queries (up to max_q), cached tokens
@@ -59,12 +60,13 @@ struct AttnWork {
   int piece, pieces;         // this workgroup's piece of the unit's
   int tiles;                 // tiles per piece
   int slot;                  // workspace slot of piece 0 of the unit (per head)
+  int split;                 // number of the unit among those of several pieces (per head)
 };
 
 struct AttnShared {
   unsigned long long part[AT_T / 64];
-  int items[AT_T / 64], slots[AT_T / 64];
-  int found[4];              // request, item within it, first slot, set
+  int items[AT_T / 64], slots[AT_T / 64], splits[AT_T / 64];
+  int found[5];              // request, item within it, first slot, first split unit, set
 };
 
 __device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, int& queries, int& len) {
@@ -75,121 +77,184 @@ __device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, 
   len = static_cast<int>(min<int64_t>(max(a.lens[r], 0), cap));
 }
 
+// Inclusive sums over the wave.
+__device__ __forceinline__ void wave_scan3(int& x, int& y, int& z) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int a = __shfl_up(x, o), b = __shfl_up(y, o), c = __shfl_up(z, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+      z += c;
+    }
+  }
+}
+
 // Finds the work of item `item` among the requests of more than `lo` and at
 // most `hi` columns; false if there is none.  Every thread of the workgroup
-// takes part.  total_slots: slots in use per head.
+// takes part.  splits: units of several pieces per head.  Each workgroup walks
+// all requests itself (two sums and a scan over them): a launch of its own for
+// that costs more at every R up to the limit.  Up to 64 requests each wave
+// does it alone, without a barrier; one request needs no scan.
 template <int NT, int TARGET>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int hi, int item, AttnShared& sh,
-                                          AttnWork& w, int& total_slots) {
+                                          AttnWork& w, int& splits) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = a.Hq / a.Hkv;
-  const int run = (a.R + AT_T - 1) / AT_T;
-  const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
   auto units_of = [&](int queries) {
     const int64_t cols = static_cast<int64_t>(queries) * group;
     return cols > lo && cols <= hi ? static_cast<int>((cols + NT - 1) / NT) : 0;
   };
   auto tiles_of = [](int len) { return (len + AT_TILE - 1) / AT_TILE; };
-
-  // all tiles of all units
-  unsigned long long work = 0;
-  for (int r = r0; r < r1; ++r) {
-    int t, q, n;
-    request_of(a, r, t, q, n);
-    work += static_cast<unsigned long long>(units_of(q)) * tiles_of(n);
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o);
-  if (lane == 0) sh.part[wave] = work;
-  if (tid == 0) sh.found[3] = 0;
-  __syncthreads();
-  work = 0;
-#pragma unroll
-  for (int i = 0; i < AT_T / 64; ++i) work += sh.part[i];
-  const unsigned long long even = (work * a.Hkv + TARGET - 1) / TARGET;
-  const int tiles = static_cast<int>(even > AT_MIN_PIECE ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_MIN_PIECE);
+  auto piece_tiles = [&](unsigned long long work) {
+    const unsigned long long even = (work * a.Hkv + TARGET - 1) / TARGET;
+    return static_cast<int>(even > AT_MIN_PIECE ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_MIN_PIECE);
+  };
+  int tiles = 0, at = 0;
   auto pieces_of = [&](int len) {
     const int n = tiles_of(len);
     return n > tiles ? (n - 1) / tiles + 1 : 1;
   };
 
-  // items and slots before this thread's requests
-  int items = 0, slots = 0;
-  for (int r = r0; r < r1; ++r) {
+  if (a.R == 1) {
     int t, q, n;
-    request_of(a, r, t, q, n);
-    const int u = units_of(q), p = pieces_of(n);
-    items += u * p;
-    if (p > 1) slots += u * p;
-  }
-  int before = items, sbefore = slots;
+    request_of(a, 0, t, q, n);
+    const int u = units_of(q);
+    tiles = piece_tiles(static_cast<unsigned long long>(u) * tiles_of(n));
+    const int p = pieces_of(n);
+    splits = p > 1 ? u : 0;
+    if (item >= u * p) return false;
+    w.r = w.slot = w.split = 0;
+    at = item;
+  } else if (a.R <= 64) {
+    int t, q = 0, n = 0;
+    if (lane < a.R) request_of(a, lane, t, q, n);
+    const int u = units_of(q);
+    unsigned long long work = static_cast<unsigned long long>(u) * tiles_of(n);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int x = __shfl_up(before, o), y = __shfl_up(sbefore, o);
-    if (lane >= o) {
-      before += x;
-      sbefore += y;
+    for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o);
+    tiles = piece_tiles(work);
+    const int p = pieces_of(n), items = u * p, slots = p > 1 ? items : 0, split = p > 1 ? u : 0;
+    int items_in = items, slots_in = slots, split_in = split;
+    wave_scan3(items_in, slots_in, split_in);
+    splits = __shfl(split_in, 63);
+    const unsigned long long here = __ballot(item < items_in);
+    if (!here) return false;
+    w.r = __ffsll(static_cast<long long>(here)) - 1;
+    at = item - __shfl(items_in - items, w.r);
+    w.slot = __shfl(slots_in - slots, w.r);
+    w.split = __shfl(split_in - split, w.r);
+  } else {
+    const int run = (a.R + AT_T - 1) / AT_T;
+    const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
+    unsigned long long work = 0;
+    for (int r = r0; r < r1; ++r) {
+      int t, q, n;
+      request_of(a, r, t, q, n);
+      work += static_cast<unsigned long long>(units_of(q)) * tiles_of(n);
     }
-  }
-  if (lane == 63) {
-    sh.items[wave] = before;
-    sh.slots[wave] = sbefore;
-  }
-  before -= items;
-  sbefore -= slots;
-  __syncthreads();
-  total_slots = 0;
 #pragma unroll
-  for (int i = 0; i < AT_T / 64; ++i) {
-    if (i < wave) {
-      before += sh.items[i];
-      sbefore += sh.slots[i];
-    }
-    total_slots += sh.slots[i];
-  }
-  if (item >= before && item < before + items) {
+    for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o);
+    if (lane == 0) sh.part[wave] = work;
+    if (tid == 0) sh.found[4] = 0;
+    __syncthreads();
+    work = 0;
+#pragma unroll
+    for (int i = 0; i < AT_T / 64; ++i) work += sh.part[i];
+    tiles = piece_tiles(work);
+    int items = 0, slots = 0, split = 0;
     for (int r = r0; r < r1; ++r) {
       int t, q, n;
       request_of(a, r, t, q, n);
       const int u = units_of(q), p = pieces_of(n);
-      if (item < before + u * p) {
-        sh.found[0] = r;
-        sh.found[1] = item - before;
-        sh.found[2] = sbefore;
-        sh.found[3] = 1;
-        break;
+      items += u * p;
+      if (p > 1) {
+        slots += u * p;
+        split += u;
       }
-      before += u * p;
-      if (p > 1) sbefore += u * p;
     }
+    int before = items, sbefore = slots, ubefore = split;
+    wave_scan3(before, sbefore, ubefore);
+    if (lane == 63) {
+      sh.items[wave] = before;
+      sh.slots[wave] = sbefore;
+      sh.splits[wave] = ubefore;
+    }
+    before -= items;
+    sbefore -= slots;
+    ubefore -= split;
+    __syncthreads();
+    splits = 0;
+#pragma unroll
+    for (int i = 0; i < AT_T / 64; ++i) {
+      if (i < wave) {
+        before += sh.items[i];
+        sbefore += sh.slots[i];
+        ubefore += sh.splits[i];
+      }
+      splits += sh.splits[i];
+    }
+    if (item >= before && item < before + items) {
+      for (int r = r0; r < r1; ++r) {
+        int t, q, n;
+        request_of(a, r, t, q, n);
+        const int u = units_of(q), p = pieces_of(n);
+        if (item < before + u * p) {
+          sh.found[0] = r;
+          sh.found[1] = item - before;
+          sh.found[2] = sbefore;
+          sh.found[3] = ubefore;
+          sh.found[4] = 1;
+          break;
+        }
+        before += u * p;
+        if (p > 1) {
+          sbefore += u * p;
+          ubefore += u;
+        }
+      }
+    }
+    __syncthreads();
+    if (!sh.found[4]) return false;
+    w.r = sh.found[0];
+    at = sh.found[1];
+    w.slot = sh.found[2];
+    w.split = sh.found[3];
   }
-  __syncthreads();
-  if (!sh.found[3]) return false;
-  w.r = sh.found[0];
+  // the same in every lane from here on
+  w.r = __builtin_amdgcn_readfirstlane(w.r);
+  at = __builtin_amdgcn_readfirstlane(at);
   request_of(a, w.r, w.tok0, w.queries, w.len);
   w.ahead = w.len - (min(a.cu[w.r + 1], a.T) - w.tok0);
+  w.tiles = __builtin_amdgcn_readfirstlane(tiles);
   w.pieces = pieces_of(w.len);
-  w.unit = sh.found[1] / w.pieces;
-  w.piece = sh.found[1] % w.pieces;
-  w.tiles = tiles;
-  w.slot = sh.found[2] + w.unit * w.pieces;
+  w.unit = at / w.pieces;
+  w.piece = at % w.pieces;
+  w.slot = __builtin_amdgcn_readfirstlane(w.slot) + w.unit * w.pieces;
+  w.split = __builtin_amdgcn_readfirstlane(w.split) + w.unit;
   return true;
 }
 
 // ---------------------------------------------------------------- workspace
-// per kernel: the count of slots in use, a header per slot, then m, l (NT each)
-// and O (NT x DH) per slot
+// per kernel: the count of units of several pieces, a header for each, then m,
+// l (NT each) and O (NT x DH) per slot
+struct AttnUnit {
+  int pieces, slot;          // and its first slot; piece p lies p * heads slots on
+  int tok0, col0, cols;      // the request's first query token; the unit's first column, its columns
+  int pad[3];
+};
 struct AttnSpace {
-  int* used;
-  int4* head;                // pieces (0: not a unit's first), first query token, first column, columns
+  int* used;                 // units of several pieces
+  AttnUnit* head;
   float* ml;
   float* o;
 };
 __host__ __device__ __forceinline__ AttnSpace attn_space(void* p, int nt, int slots) {
   AttnSpace s;
   s.used = static_cast<int*>(p);
-  s.head = reinterpret_cast<int4*>(p) + 1;
-  s.ml = reinterpret_cast<float*>(s.head + slots);
+  s.head = reinterpret_cast<AttnUnit*>(static_cast<char*>(p) + 16);
+  s.ml = reinterpret_cast<float*>(s.head + slots / 2);      // a split unit has at least two slots
   s.o = s.ml + static_cast<size_t>(slots) * 2 * nt;
   return s;
 }
@@ -267,9 +332,9 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
   const int group = a.Hq / a.Hkv;
   const AttnSpace ws = attn_space(a.workspace, AT_NT, AT_SLOTS);
   AttnWork w;
-  int total_slots;
-  const bool have = find_work<AT_NT, AT_TARGET>(a, 0, hi, item, sh, w, total_slots);
-  if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = total_slots * a.Hkv;
+  int splits;
+  const bool have = find_work<AT_NT, AT_TARGET>(a, 0, hi, item, sh, w, splits);
+  if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = splits * a.Hkv;
   if (!have) return;
 
   const int cols = w.queries * group, c0 = w.unit * AT_NT;
@@ -312,7 +377,7 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
 
   u32x4 kr[4][KH], vr[DT];
   float ks, vs;
-  int pk, pv;
+  int pk, pv, pv_next;
   auto load_k = [&](int tile) {
     const uint8_t* p = a.k_cache + max(pk, 0) * page_bytes + head_off + 16 * g;
 #pragma unroll
@@ -330,16 +395,30 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
       vr[d] = *reinterpret_cast<const u32x4*>(p + (static_cast<int64_t>(16 * d + i) << lg));
   };
 
-  for (int tile = w.piece * w.tiles + wave; tile < t_end; tile += AT_T / 64) {
+  // K of the wave's next tile is requested once S no longer needs the current
+  // one's registers, V after O; page numbers one tile earlier still
+  auto pages = [&](int tile) {
     pk = page_of(tile * AT_TILE + 16 * (i >> 2));
-    pv = page_of(tile * AT_TILE + 16 * g);
-    load_k(tile);
-    load_v(tile);
-    const int64_t si = static_cast<int64_t>(max(pv, 0)) * a.Hkv + head;
+    pv_next = page_of(tile * AT_TILE + 16 * g);
+  };
+  auto scales = [&]() {
+    const int64_t si = static_cast<int64_t>(max(pv_next, 0)) * a.Hkv + head;
     ks = a.k_scale[si];
-    vs = pv >= 0 ? a.v_scale[si] : 0.0f;
+    vs = pv_next >= 0 ? a.v_scale[si] : 0.0f;
+  };
+  constexpr int STEP = AT_T / 64;
+  int tile = w.piece * w.tiles + wave;
+  if (tile < t_end) {
+    pages(tile);
+    load_k(tile);
+    scales();
+    pv = pv_next;
+    load_v(tile);
+    pages(tile + STEP);
+  }
+  for (; tile < t_end; tile += STEP) {
     const float c = ks * a.scale * AT_LOG2E;
-
+    const float v_scale = vs;
     f32x4 s[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -351,6 +430,10 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
 #pragma unroll
         for (int n = NS - 1; n >= 0; --n) s[t] = mfma16(kf, qf[k][n], s[t]);
       }
+    }
+    if (tile + STEP < t_end) {
+      load_k(tile + STEP);
+      scales();
     }
     float x[4][4];
     float top = AT_NEG;
@@ -399,7 +482,7 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
       for (int e = 0; e < 8; ++e) {
         p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - base);
         l += p[e];
-        p[e] *= vs;
+        p[e] *= v_scale;
       }
       parts<NS>(p, pf[h]);
     }
@@ -411,6 +494,11 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
 #pragma unroll
         for (int n = NS - 1; n >= 0; --n) o[d] = mfma16(vf, pf[h][n], o[d]);
       }
+    }
+    if (tile + STEP < t_end) {
+      pv = pv_next;
+      load_v(tile + STEP);
+      pages(tile + 2 * STEP);
     }
   }
 
@@ -448,8 +536,9 @@ __global__ __launch_bounds__(AT_T) void attn_paged_kernel(AttnArgs a, int hi) {
     for (int e = 0; e < PER; ++e) Io<IO>::st(op, e, acc[e] * inv);
   } else {
     const int64_t slot = static_cast<int64_t>(w.slot + w.piece) * a.Hkv + head;
-    if (tid == 0)
-      ws.head[slot] = make_int4(w.piece == 0 ? w.pieces : 0, w.tok0, c0, min(AT_NT, cols - c0));
+    if (tid == 0 && w.piece == 0)
+      ws.head[static_cast<int64_t>(w.split) * a.Hkv + head] =
+          AttnUnit{w.pieces, static_cast<int>(slot), w.tok0, c0, min(AT_NT, cols - c0), {0, 0, 0}};
     if ((tid & 15) == 0) {
       ws.ml[slot * 2 * AT_NT + oc] = big;
       ws.ml[slot * 2 * AT_NT + AT_NT + oc] = sum;
@@ -493,9 +582,9 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo) 
   void* space = a.workspace ? static_cast<char*>(a.workspace) + attn_space_bytes(AT_NT, AT_SLOTS, DH) : nullptr;
   const AttnSpace ws = attn_space(space, AT_WNT, AT_WSLOTS);
   AttnWork w;
-  int total_slots;
-  const bool have = find_work<AT_WNT, AT_WTARGET>(a, lo, 0x7FFFFFFF, item, sh, w, total_slots);
-  if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = total_slots * a.Hkv;
+  int splits;
+  const bool have = find_work<AT_WNT, AT_WTARGET>(a, lo, 0x7FFFFFFF, item, sh, w, splits);
+  if (blockIdx.x == 0 && tid == 0 && a.workspace) *ws.used = splits * a.Hkv;
   if (!have) return;
 
   const int cols = w.queries * group;
@@ -714,7 +803,9 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo) 
       }
   } else {
     const int64_t slot = static_cast<int64_t>(w.slot + w.piece) * a.Hkv + head;
-    if (tid == 0) ws.head[slot] = make_int4(w.piece == 0 ? w.pieces : 0, w.tok0, c0, min(AT_WNT, cols - c0));
+    if (tid == 0 && w.piece == 0)
+      ws.head[static_cast<int64_t>(w.split) * a.Hkv + head] =
+          AttnUnit{w.pieces, static_cast<int>(slot), w.tok0, c0, min(AT_WNT, cols - c0), {0, 0, 0}};
     const int oc = wave * 32 + i;
     if (hf == 0) {
       ws.ml[slot * 2 * AT_WNT + oc] = m;
@@ -730,32 +821,79 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo) 
   }
 }
 
-// Joins the pieces of each unit that has several: one workgroup per slot, at
-// work where the slot is its unit's first.
-template <typename IO, int DH>
-__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, size_t skip, int nt, int slots) {
-  const AttnSpace ws = attn_space(static_cast<char*>(a.workspace) + skip, nt, slots);
-  const int64_t slot = blockIdx.x;
-  if (slot >= *ws.used) return;
-  const int4 h = ws.head[slot];
-  if (h.x == 0) return;
-  const int head = static_cast<int>(slot % a.Hkv), group = a.Hq / a.Hkv;
-  for (int i = threadIdx.x; i < h.w * DH; i += AT_T) {
-    const int c = i / DH, d = i % DH;
-    float big = AT_NEG;
-    for (int p = 0; p < h.x; ++p) big = fmaxf(big, ws.ml[(slot + static_cast<int64_t>(p) * a.Hkv) * 2 * nt + c]);
-    float sum = 0.0f, acc = 0.0f;
-    for (int p = 0; p < h.x; ++p) {
-      const int64_t s = slot + static_cast<int64_t>(p) * a.Hkv;
-      const float mk = ws.ml[s * 2 * nt + c];
-      const float f = mk == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(mk - big);
-      sum = fmaf(f, ws.ml[s * 2 * nt + nt + c], sum);
-      acc = fmaf(f, ws.o[(s * nt + c) * DH + d], acc);
+// ---------------------------------------------------------------- joining pieces
+// out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p over a unit's pieces.  A
+// workgroup takes 16 columns of a unit: DH / 4 lanes per column, four values
+// each; with fewer columns than it has lanes for, the lanes left over take
+// every other (fourth, eighth) piece and are added through LDS.  The grid is
+// fixed and walks the units, whose number only the device knows.
+template <typename IO, int DH, int NT>
+__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, size_t skip, int slots) {
+  constexpr int LPC = DH / 4;              // lanes per column
+  constexpr int SETS = AT_T / LPC;         // columns the workgroup holds at once
+  __shared__ float s_m[SETS], s_l[SETS];
+  __shared__ __align__(16) f32x4 s_o[SETS][LPC];
+  const AttnSpace ws = attn_space(static_cast<char*>(a.workspace) + skip, NT, slots);
+  const int64_t tasks = static_cast<int64_t>(*ws.used) * (NT / 16);
+  const int group = a.Hq / a.Hkv;
+  const int set = threadIdx.x / LPC, d = (threadIdx.x % LPC) * 4;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int64_t unit = task / (NT / 16);
+    const int first = static_cast<int>(task % (NT / 16)) * 16;
+    const AttnUnit u = ws.head[unit];
+    const int head = static_cast<int>(unit % a.Hkv);
+    const int cols = min(u.cols - first, 16);
+    if (cols <= 0) continue;
+    int lg = 0;                            // log2 of the columns side by side
+    while ((1 << lg) < cols && (1 << lg) < SETS) ++lg;
+    const int side = 1 << lg, ways = SETS >> lg;
+    const int way = set >> lg;
+    for (int c0 = 0; c0 < cols; c0 += side) {
+      const int c = c0 + (set & (side - 1));
+      float m = AT_NEG, l = 0.0f;
+      f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+      if (c < cols) {
+#pragma unroll 4
+        for (int p = way; p < u.pieces; p += ways) {
+          const int64_t s = u.slot + static_cast<int64_t>(p) * a.Hkv;
+          const float pm = ws.ml[s * 2 * NT + first + c], pl = ws.ml[s * 2 * NT + NT + first + c];
+          const f32x4 po = *reinterpret_cast<const f32x4*>(ws.o + (s * NT + first + c) * DH + d);
+          const float big = fmaxf(m, pm);
+          const float fo = m == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(m - big);
+          const float fp = pm == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(pm - big);
+          l = l * fo + pl * fp;
+          o = o * fo + po * fp;
+          m = big;
+        }
+      }
+      if (ways > 1) {
+        if (d == 0) {
+          s_m[set] = m;
+          s_l[set] = l;
+        }
+        s_o[set][d >> 2] = o;
+        __syncthreads();
+        float big = AT_NEG;
+        for (int k = 0; k < ways; ++k) big = fmaxf(big, s_m[(k << lg) + (set & (side - 1))]);
+        l = 0.0f;
+        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < ways; ++k) {
+          const int from = (k << lg) + (set & (side - 1));
+          const float f = s_m[from] == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(s_m[from] - big);
+          l += f * s_l[from];
+          o += f * s_o[from][d >> 2];
+        }
+        __syncthreads();
+      }
+      if (way == 0 && c < cols) {
+        const int cc = u.col0 + first + c;
+        IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(u.tok0) + cc / group) * a.Hq +
+                                            static_cast<int64_t>(head) * group + cc % group) * DH + d;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Io<IO>::st(op, e, o[e] * inv);
+      }
     }
-    const int cc = h.z + c;
-    IO* op = static_cast<IO*>(a.out) +
-             ((static_cast<int64_t>(h.y) + cc / group) * a.Hq + static_cast<int64_t>(head) * group + cc % group) * DH;
-    Io<IO>::st(op, d, sum == 0.0f ? 0.0f : acc / sum);
   }
 }
 
@@ -811,18 +949,22 @@ size_t attn_paged_workspace(int64_t max_q, int64_t max_pages, int page_lg, int64
 hipError_t launch_attn_paged(const AttnArgs& a) {
   const AttnGrids g = grids_of(a.R, a.T, a.max_q, a.max_pages, a.page_lg, a.Hq, a.Hkv);
   const size_t skip = attn_space_bytes(AT_NT, AT_SLOTS, a.DH);
-  auto go = [&](auto narrow, auto wide, auto join) {
+  auto go = [&](auto narrow, auto wide, auto join, auto wide_join) {
     if (g.wide) wide<<<static_cast<unsigned>(g.wide), AT_T, 0, a.stream>>>(a, g.limit);
     if (g.narrow) narrow<<<static_cast<unsigned>(g.narrow), AT_T, 0, a.stream>>>(a, g.limit);
-    if (g.split && g.narrow) join<<<AT_SLOTS, AT_T, 0, a.stream>>>(a, 0, AT_NT, AT_SLOTS);
-    if (g.split && g.wide) join<<<AT_WSLOTS, AT_T, 0, a.stream>>>(a, skip, AT_WNT, AT_WSLOTS);
+    if (g.split && g.narrow) join<<<AT_JOIN, AT_T, 0, a.stream>>>(a, 0, AT_SLOTS);
+    if (g.split && g.wide) wide_join<<<AT_JOIN, AT_T, 0, a.stream>>>(a, skip, AT_WSLOTS);
   };
   if (a.bf16) {
-    if (a.DH == 64) go(attn_paged_kernel<bf16_t, 64>, attn_wide_kernel<bf16_t, 64>, attn_join_kernel<bf16_t, 64>);
-    else go(attn_paged_kernel<bf16_t, 128>, attn_wide_kernel<bf16_t, 128>, attn_join_kernel<bf16_t, 128>);
+    if (a.DH == 64) go(attn_paged_kernel<bf16_t, 64>, attn_wide_kernel<bf16_t, 64>,
+       attn_join_kernel<bf16_t, 64, AT_NT>, attn_join_kernel<bf16_t, 64, AT_WNT>);
+    else go(attn_paged_kernel<bf16_t, 128>, attn_wide_kernel<bf16_t, 128>,
+       attn_join_kernel<bf16_t, 128, AT_NT>, attn_join_kernel<bf16_t, 128, AT_WNT>);
   } else {
-    if (a.DH == 64) go(attn_paged_kernel<float, 64>, attn_wide_kernel<float, 64>, attn_join_kernel<float, 64>);
-    else go(attn_paged_kernel<float, 128>, attn_wide_kernel<float, 128>, attn_join_kernel<float, 128>);
+    if (a.DH == 64) go(attn_paged_kernel<float, 64>, attn_wide_kernel<float, 64>,
+       attn_join_kernel<float, 64, AT_NT>, attn_join_kernel<float, 64, AT_WNT>);
+    else go(attn_paged_kernel<float, 128>, attn_wide_kernel<float, 128>,
+       attn_join_kernel<float, 128, AT_NT>, attn_join_kernel<float, 128, AT_WNT>);
   }
   return hipGetLastError();
 }
