@@ -91,6 +91,25 @@ __device__ __forceinline__ void store8(IO* p, int64_t n, const float (&x)[8]) {
 // integer maximum carries a NaN where a float maximum would drop it.
 __device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// Largest x over the 16 lanes of a row of the wave, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
+  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, true)));
+  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xF, 0xF, true)));
+  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xF, 0xF, true)));
+  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x140, 0xF, 0xF, true)));
+  return x;
+}
+// and over the wave.
+__device__ __forceinline__ uint32_t max64(uint32_t x) {
+  x = max16(x);
+  const int l = static_cast<int>(threadIdx.x);
+  uint32_t o = __float_as_uint(xor16(__uint_as_float(x), l));
+  x = x > o ? x : o;
+  o = __float_as_uint(xor32(__uint_as_float(x), (l >> 5) & 1));
+  return x > o ? x : o;
+}
+
 // The smallest power of two s with top / s <= 448 = 1.75 * 2^8, at least
 // FP8_MIN_SCALE; top a finite magnitude's bits.  Exact: exponent and mantissa
 // are compared as integers.

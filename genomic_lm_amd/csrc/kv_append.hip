@@ -30,6 +30,7 @@ namespace hyena {
 
 constexpr int KA_T = 256;
 constexpr int KA_SHORT = 4;      // runs of up to this many tokens go to one wave
+constexpr int KA_GAP = 64;       // (one per lane: a wave looks so far back and ahead)
 
 struct KvPtr {
   const void* src;               // (T, heads, DH) rows, strides in elements
@@ -38,23 +39,11 @@ struct KvPtr {
   float* scale;
 };
 
-// Largest finite magnitude and the presence of a non-finite one, per element.
-__device__ __forceinline__ void see(const float (&x)[8], uint32_t& top, bool& bad) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t m = mag_bits(x[e]);
-    if (m >= 0x7F800000u) bad = true;
-    else top = m > top ? m : top;
-  }
-}
-
-__device__ __forceinline__ uint32_t wave_max_u(uint32_t x) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t y = static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), o));
-    x = x > y ? x : y;
-  }
-  return x;
+// Largest finite magnitude, and whether a non-finite one was seen.
+__device__ __forceinline__ void see(float x, uint32_t& top, bool& bad) {
+  const uint32_t m = mag_bits(x);
+  if (m >= 0x7F800000u) bad = true;
+  else top = m > top ? m : top;
 }
 
 // The codes of the first n0 tokens of a block times f, by `team` lanes.
@@ -75,23 +64,227 @@ __device__ __forceinline__ void move_old(uint8_t* blk, int n0, int P, float f, i
   }
 }
 
-// One workgroup takes `per` consecutive tokens of one head: the runs of
-// consecutive places of one page that start there.  Short runs go to a wave
-// each, longer ones to the workgroup.
+// One workgroup takes `per` consecutive tokens of one head: the runs that open
+// there.  A run is the tokens of one page, which stand together in the call,
+// fewer than KA_GAP tokens without a slot between two of them.  Short runs go
+// to a wave each, longer ones to the workgroup.
 template <typename IO, int DH>
-__global__ __launch_bounds__(KA_T) void kv_append_kernel(KvPtr kp, KvPtr vp,
+struct Append {
+  static constexpr int LPT = DH / 8;               // lanes per token, eight dimensions each
+  static constexpr int TPW = 64 / LPT;             // tokens a wave holds at once
+  static constexpr int TPG = KA_T / LPT;           // tokens the workgroup holds at once
+  static constexpr int STEPS = 64 / TPG;           // steps of a 64-token piece
+  static constexpr int VROW = 64 + 4;              // padded row of the transposed tile
+  static constexpr unsigned long long LANES = (1ull << LPT) - 1;
+
+  struct Run {
+    int64_t t;                                     // first token
+    int64_t blk;                                   // block of the cache
+    int n0, n;                                     // first place, tokens from the first to the last
+    bool straight;                                 // place n0 + j for token j
+    const int64_t* slots;                          // of the run's tokens
+    int64_t page0, pages;                          // first slot of the page, slots of the cache
+    uint8_t *kb, *vb;                              // the block's codes
+
+    // the place of token j, -1 if it has none
+    __device__ __forceinline__ int place(int j) const {
+      if (straight) return n0 + j;
+      const int64_t s = slots[j];
+      return s >= 0 && s < pages ? static_cast<int>(s - page0) : -1;
+    }
+  };
+
+  // the wave's run of at most KA_SHORT tokens: one token per LPT lanes
+  static __device__ __forceinline__ void by_wave(const KvPtr& kp, const KvPtr& vp, const IO* ks,
+                                                 const IO* vs, const Run& u, int P) {
+    const int lane = threadIdx.x & 63, j = lane / LPT, c = (lane % LPT) * 8;
+    float ok = 0.0f, ov = 0.0f;
+    if (u.n0) {
+      ok = kp.scale[u.blk];
+      ov = vp.scale[u.blk];
+    }
+    float k[8] = {}, v[8] = {};
+    const int at = j < u.n ? u.place(j) : -1;
+    if (at >= 0) {
+      load8(ks + (u.t + j) * kp.tok + c, 8, k);
+      load8(vs + (u.t + j) * vp.tok + c, 8, v);
+    }
+    uint32_t tk = 0, tv = 0;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      see(k[e], tk, bad);
+      see(v[e], tv, bad);
+    }
+    const bool poison = ((__ballot(bad) >> (j * LPT)) & LANES) != 0;
+    float sk = block_scale(max64(tk)), sv = block_scale(max64(tv));
+    if (u.n0) {
+      if (sk > ok) move_old<DH, false>(u.kb, u.n0, P, ok / sk, lane, 64); else sk = ok;
+      if (sv > ov) move_old<DH, true>(u.vb, u.n0, P, ov / sv, lane, 64); else sv = ov;
+      // the moved words before the new bytes that share them
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
+    }
+    if (lane == 0) {
+      kp.scale[u.blk] = sk;
+      vp.scale[u.blk] = sv;
+    }
+    if (at < 0) return;
+    const float ik = 1.0f / sk, iv = 1.0f / sv;          // powers of two: exact
+    uint32_t w[2];
+    w[0] = fp8x4(k[0] * ik, k[1] * ik, k[2] * ik, k[3] * ik);
+    w[1] = fp8x4(k[4] * ik, k[5] * ik, k[6] * ik, k[7] * ik);
+    if (poison) w[0] = w[1] = FP8_NAN * 0x01010101u;
+    __builtin_memcpy(u.kb + at * DH + c, w, 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = mag_bits(v[e]) >= 0x7F800000u ? 0.0f : v[e] * iv;
+    w[0] = fp8x4(v[0], v[1], v[2], v[3]);
+    w[1] = fp8x4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      u.vb[static_cast<int64_t>(c + e) * P + at] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+  }
+
+  // The workgroup's run: largest magnitudes first, then codes, in pieces of 64
+  // tokens (one piece unless P > 64, kept in registers between the two).
+  // Thread: tokens STEPS j0 .. + STEPS - 1 of the piece, so that its codes of
+  // one dimension of V are neighbours in the transposed row.
+  static __device__ __forceinline__ void by_group(const KvPtr& kp, const KvPtr& vp, const IO* ks,
+                                                  const IO* vs, const Run& u, int P, uint8_t* vt,
+                                                  uint32_t (*sh_top)[KA_T / 64]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int j0 = (tid / LPT) * STEPS, c = (tid % LPT) * 8;
+    float ok = 0.0f, ov = 0.0f;
+    if (u.n0) {
+      ok = kp.scale[u.blk];
+      ov = vp.scale[u.blk];
+    }
+    Vec8<IO> k[STEPS], v[STEPS];
+    uint32_t tk = 0, tv = 0;
+    uint32_t poison = 0;                   // bit q: token q holds a non-finite value
+    auto piece = [&](int p0) {
+      // past the run's end: its last token again, which has a slot
+      int j = min(p0 + j0, u.n - 1);
+      const IO* kr = ks + (u.t + j) * kp.tok + c;
+      const IO* vr = vs + (u.t + j) * vp.tok + c;
+#pragma unroll
+      for (int q = 0; q < STEPS; ++q) {
+        k[q].load(kr);
+        v[q].load(vr);
+        if (j + 1 < u.n) {
+          ++j;
+          kr += kp.tok;
+          vr += vp.tok;
+        }
+      }
+      poison = 0;
+#pragma unroll
+      for (int q = 0; q < STEPS; ++q) {
+        if (u.place(min(p0 + j0 + q, u.n - 1)) < 0) continue;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          see(k[q].get(e), tk, bad);
+          see(v[q].get(e), tv, bad);
+        }
+        if (bad) poison |= 1u << q;
+      }
+      if (__any(poison)) {
+        // of the token: every lane that holds a part of it
+#pragma unroll
+        for (int o = 1; o < LPT; o <<= 1) poison |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(poison), o));
+      }
+    };
+    const int pieces = (u.n + 63) >> 6;
+    for (int p = 0; p < pieces; ++p) piece(p * 64);
+    tk = max64(tk);
+    tv = max64(tv);
+    if (lane == 0) {
+      sh_top[0][wave] = tk;
+      sh_top[1][wave] = tv;
+    }
+    __syncthreads();                       // (also: the old scales are read)
+#pragma unroll
+    for (int w = 0; w < KA_T / 64; ++w) {
+      tk = max(tk, sh_top[0][w]);
+      tv = max(tv, sh_top[1][w]);
+    }
+    float sk = block_scale(tk), sv = block_scale(tv);
+    if (u.n0) {
+      const bool mk = sk > ok, mv = sv > ov;
+      if (mk) move_old<DH, false>(u.kb, u.n0, P, ok / sk, tid, KA_T); else sk = ok;
+      if (mv) move_old<DH, true>(u.vb, u.n0, P, ov / sv, tid, KA_T); else sv = ov;
+      if (mk || mv) __syncthreads();       // the moved words before the new bytes that share them
+    }
+    if (tid == 0) {
+      kp.scale[u.blk] = sk;
+      vp.scale[u.blk] = sv;
+    }
+    const float ik = 1.0f / sk, iv = 1.0f / sv;
+    for (int p = 0; p < pieces; ++p) {
+      const int p0 = p * 64;
+      if (pieces > 1) piece(p0);
+#pragma unroll
+      for (int q = 0; q < STEPS; ++q) {
+        const int j = p0 + j0 + q;
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[h] = fp8x4(k[q].get(4 * h) * ik, k[q].get(4 * h + 1) * ik, k[q].get(4 * h + 2) * ik,
+                       k[q].get(4 * h + 3) * ik);
+        if ((poison >> q) & 1) w[0] = w[1] = FP8_NAN * 0x01010101u;
+        const int at = j < u.n ? u.place(j) : -1;
+        if (at >= 0) __builtin_memcpy(u.kb + at * DH + c, w, 8);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < STEPS; ++q) f[q] = v[q].get(e) * iv;
+        if (poison) {
+#pragma unroll
+          for (int q = 0; q < STEPS; ++q)
+            if (mag_bits(v[q].get(e)) >= 0x7F800000u) f[q] = 0.0f;
+        }
+        uint8_t* to = vt + (c + e) * VROW + j0;
+        const uint32_t w = fp8x4(f[0], f[1], f[2], f[3]);
+        if constexpr (STEPS == 4) *reinterpret_cast<uint32_t*>(to) = w;
+        else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(w);
+      }
+      __syncthreads();
+      // rows of V: 64 places of one dimension, from place n0 + p0
+      const int m = u.n - p0 < 64 ? u.n - p0 : 64;
+      if (u.straight && m == 64 && ((u.n0 + p0) & 15) == 0) {
+        uint8_t* out = u.vb + u.n0 + p0;
+#pragma unroll
+        for (int i = tid; i < DH * 4; i += KA_T) {
+          const int d = i >> 2, o = (i & 3) * 16;
+          const uint32_t* from = reinterpret_cast<const uint32_t*>(vt + d * VROW + o);
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(d) * P + o) =
+              make_uint4(from[0], from[1], from[2], from[3]);
+        }
+      } else {
+        for (int i = tid; i < DH * m; i += KA_T) {
+          const int d = i / m, o = i % m, at = u.place(p0 + o);
+          if (at >= 0) u.vb[static_cast<int64_t>(d) * P + at] = vt[d * VROW + o];
+        }
+      }
+      __syncthreads();
+    }
+  }
+};
+
+// Four waves per SIMD for bf16 (128 VGPRs): 81 us against 86 us at three and 104
+// us at five (spills) for 13605 tokens of 32 heads of 128; fp32 would spill.
+template <typename IO, int DH>
+__global__ __launch_bounds__(KA_T, sizeof(IO) == 2 ? 4 : 2) void kv_append_kernel(KvPtr kp, KvPtr vp,
                                                          const int64_t* __restrict__ slots,
                                                          int64_t num_pages, int lg, int T, int H,
                                                          int per) {
-  constexpr int LPT = DH / 8;               // lanes per token
-  constexpr int TPW = 64 / LPT;             // tokens a wave holds at once
-  constexpr int TPG = KA_T / LPT;           // tokens the workgroup holds at once
-  constexpr int STEPS = 64 / TPG;           // steps of a 64-token piece
-  constexpr int VROW = 64 + 8;              // padded row of the transposed tile
-  __shared__ __align__(16) uint8_t vt[DH * VROW];
+  using A = Append<IO, DH>;
+  __shared__ __align__(16) uint8_t vt[DH * A::VROW];
   __shared__ uint32_t sh_top[2][KA_T / 64];
   const int P = 1 << lg, pmask = P - 1;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int head = static_cast<int>(blockIdx.x % H);
   const int64_t first = static_cast<int64_t>(blockIdx.x / H) * per;
   const int64_t limit = num_pages << lg;
@@ -102,173 +295,61 @@ __global__ __launch_bounds__(KA_T) void kv_append_kernel(KvPtr kp, KvPtr vp,
     const int64_t s = t >= 0 && t < T ? slots[t] : -1;
     return s >= 0 && s < limit ? s : -1;
   };
-  // does token t open a run: a valid slot that does not continue the one before it
-  auto opens = [&](int64_t t) {
-    const int64_t s = slot_of(t);
-    if (s < 0) return false;
-    return (s & pmask) == 0 || slot_of(t - 1) != s - 1;
-  };
-  // tokens of the run that t opens (every lane of the wave takes part)
-  auto run_of = [&](int64_t t, int64_t s) {
-    const int room = P - static_cast<int>(s & pmask);
-    int n = 0;
-    while (n < room) {
-      const int i = n + lane;
-      const bool in = i < room && slot_of(t + i) == s + i;
-      const unsigned long long miss = ~__ballot(in);
-      if (miss) return n + __ffsll(static_cast<long long>(miss)) - 1;
-      n += 64;
-    }
-    return room;
-  };
-
-  // which of the tokens open a run (per <= 64; the same in every wave)
-  unsigned long long todo = __ballot(lane < per && opens(first + lane));
+  // the slots of 64 tokens from the workgroup's first on and of the 64 before
+  // it, the same in every wave: a token opens a run unless the nearest token
+  // with a slot before it is in its page and less than KA_GAP tokens away
+  const int64_t mine = slot_of(first + lane), old = slot_of(first - 1 - lane);
+  const unsigned long long valid = __ballot(mine >= 0), prior = __ballot(old >= 0);
+  const int64_t up = __shfl_up(mine, 1);
+  const unsigned long long below = valid & ((1ull << lane) - 1);
+  const int near = below ? 63 - __clzll(static_cast<long long>(below)) : 0;
+  const int back = prior ? __ffsll(static_cast<long long>(prior)) - 1 : 0;
+  const int64_t in_window = __shfl(mine, near), in_prior = __shfl(old, back);
+  const int64_t last = below ? in_window : prior ? in_prior : -1;
+  const int away = below ? lane - near : lane + 1 + back;
+  const bool joins = mine >= 0 && last >= 0 && (last >> lg) == (mine >> lg) && away < KA_GAP;
+  const unsigned long long opens = valid & ~__ballot(joins);
+  const unsigned long long next = __ballot(lane > 0 && mine >= 0 && mine == up + 1 && up >= 0);
+  unsigned long long todo = opens & (per < 64 ? (1ull << per) - 1 : ~0ull);
   int turn = 0;
   while (todo) {
     const int i = __ffsll(static_cast<long long>(todo)) - 1;
     todo &= todo - 1;
-    const int64_t t = first + i;
-    const int64_t s = slot_of(t);
+    typename A::Run u;
+    u.t = first + i;
+    const int64_t s = __shfl(mine, i);
     const int64_t page = s >> lg;
-    const int n0 = static_cast<int>(s & pmask);
-    const int64_t blk = page * H + head;
-    const int64_t base = blk * static_cast<int64_t>(P) * DH;
-    const int n = run_of(t, s);
-    uint8_t* kb = kp.cache + base;
-    uint8_t* vb = vp.cache + base;
-
-    if (n <= KA_SHORT && n <= TPW) {
-      if ((turn++ & (KA_T / 64 - 1)) != wave) continue;
-      const int j = lane / LPT, c = (lane % LPT) * 8;
-      float k[8] = {}, v[8] = {};
-      if (j < n) {
-        load8(ks + (t + j) * kp.tok + c, 8, k);
-        load8(vs + (t + j) * vp.tok + c, 8, v);
+    u.n0 = static_cast<int>(s & pmask);
+    // to the last token with a slot before the next run
+    const unsigned long long above = i == 63 ? 0 : ~0ull << (i + 1);
+    const unsigned long long stop = opens & above;
+    const unsigned long long mem = valid & above & (stop ? (stop & -stop) - 1 : ~0ull);
+    u.n = mem ? 64 - __clzll(static_cast<long long>(mem)) - i : 1;
+    u.straight = ((above & ((u.n == 64 - i) ? ~0ull : (1ull << (i + u.n)) - 1)) & ~next) == 0;
+    if (!stop) {
+      // no other run in the window: look on, KA_GAP - 1 tokens past the last one
+      for (;;) {
+        const int64_t v = lane < KA_GAP - 1 ? slot_of(u.t + u.n + lane) : -1;
+        const unsigned long long has = __ballot(v >= 0), other = __ballot(v >= 0 && (v >> lg) != page);
+        const unsigned long long in = other ? has & ((other & -other) - 1) : has;
+        if (!in) break;
+        const int m = 64 - __clzll(static_cast<long long>(in));
+        const unsigned long long run = __ballot(v == s + u.n + lane);
+        u.straight &= (~run & (m == 64 ? ~0ull : (1ull << m) - 1)) == 0;
+        u.n += m;
+        if (other) break;
       }
-      uint32_t tk = 0, tv = 0;
-      bool bad = false;
-      see(k, tk, bad);
-      see(v, tv, bad);
-      const unsigned long long bads = __ballot(bad);
-      const bool poison = ((bads >> (j * LPT)) & ((1ull << LPT) - 1)) != 0;
-      float sk = block_scale(wave_max_u(tk)), sv = block_scale(wave_max_u(tv));
-      if (n0) {
-        const float ok = kp.scale[blk], ov = vp.scale[blk];
-        if (sk > ok) move_old<DH, false>(kb, n0, P, ok / sk, lane, 64); else sk = ok;
-        if (sv > ov) move_old<DH, true>(vb, n0, P, ov / sv, lane, 64); else sv = ov;
-        // the moved words before the new bytes that share them
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");
-      }
-      if (lane == 0) {
-        kp.scale[blk] = sk;
-        vp.scale[blk] = sv;
-      }
-      if (j < n) {
-        const float ik = 1.0f / sk, iv = 1.0f / sv;      // powers of two: exact
-        uint32_t w[2];
-        w[0] = fp8x4(k[0] * ik, k[1] * ik, k[2] * ik, k[3] * ik);
-        w[1] = fp8x4(k[4] * ik, k[5] * ik, k[6] * ik, k[7] * ik);
-        if (poison) w[0] = w[1] = FP8_NAN * 0x01010101u;
-        __builtin_memcpy(kb + (n0 + j) * DH + c, w, 8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (mag_bits(v[e]) >= 0x7F800000u) v[e] = 0.0f;
-        w[0] = fp8x4(v[0] * iv, v[1] * iv, v[2] * iv, v[3] * iv);
-        w[1] = fp8x4(v[4] * iv, v[5] * iv, v[6] * iv, v[7] * iv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          vb[static_cast<int64_t>(c + e) * P + n0 + j] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-      }
-      continue;
     }
-
-    // ---- the workgroup's run: largest magnitudes first, then codes, in
-    // pieces of 64 tokens (one piece unless P > 64)
-    const int j0 = tid / LPT, c = (tid % LPT) * 8;
-    float k[STEPS][8], v[STEPS][8];
-    uint32_t tk = 0, tv = 0;
-    bool bad[STEPS];
-    auto piece = [&](int p0) {
-#pragma unroll
-      for (int q = 0; q < STEPS; ++q) {
-        const int j = p0 + q * TPG + j0;
-        const int64_t m = j < n ? 8 : 0;
-        load8(ks + (t + (j < n ? j : 0)) * kp.tok + c, m, k[q]);
-        load8(vs + (t + (j < n ? j : 0)) * vp.tok + c, m, v[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < STEPS; ++q) {
-        bad[q] = false;
-        see(k[q], tk, bad[q]);
-        see(v[q], tv, bad[q]);
-      }
-    };
-    const int pieces = (n + 63) >> 6;
-    for (int p = 0; p < pieces; ++p) piece(p * 64);
-    tk = wave_max_u(tk);
-    tv = wave_max_u(tv);
-    if (lane == 0) {
-      sh_top[0][wave] = tk;
-      sh_top[1][wave] = tv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < KA_T / 64; ++w) {
-      tk = max(tk, sh_top[0][w]);
-      tv = max(tv, sh_top[1][w]);
-    }
-    float sk = block_scale(tk), sv = block_scale(tv);
-    if (n0) {
-      const float ok = kp.scale[blk], ov = vp.scale[blk];
-      if (sk > ok) move_old<DH, false>(kb, n0, P, ok / sk, tid, KA_T); else sk = ok;
-      if (sv > ov) move_old<DH, true>(vb, n0, P, ov / sv, tid, KA_T); else sv = ov;
-    }
-    __syncthreads();                       // old scales read, old codes moved
-    if (tid == 0) {
-      kp.scale[blk] = sk;
-      vp.scale[blk] = sv;
-    }
-    const float ik = 1.0f / sk, iv = 1.0f / sv;
-    for (int p = 0; p < pieces; ++p) {
-      const int p0 = p * 64;
-      if (pieces > 1) piece(p0);
-#pragma unroll
-      for (int q = 0; q < STEPS; ++q) {
-        const int j = p0 + q * TPG + j0;
-        const unsigned long long bads = __ballot(bad[q]);
-        const bool poison = ((bads >> ((lane / LPT) * LPT)) & ((1ull << LPT) - 1)) != 0;
-        uint32_t w[2];
-        w[0] = fp8x4(k[q][0] * ik, k[q][1] * ik, k[q][2] * ik, k[q][3] * ik);
-        w[1] = fp8x4(k[q][4] * ik, k[q][5] * ik, k[q][6] * ik, k[q][7] * ik);
-        if (poison) w[0] = w[1] = FP8_NAN * 0x01010101u;
-        if (j < n) __builtin_memcpy(kb + static_cast<int64_t>(n0 + j) * DH + c, w, 8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (mag_bits(v[q][e]) >= 0x7F800000u) v[q][e] = 0.0f;
-        w[0] = fp8x4(v[q][0] * iv, v[q][1] * iv, v[q][2] * iv, v[q][3] * iv);
-        w[1] = fp8x4(v[q][4] * iv, v[q][5] * iv, v[q][6] * iv, v[q][7] * iv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          vt[(c + e) * VROW + (j - p0)] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-      }
-      __syncthreads();
-      // rows of V: 64 places of one dimension, from place n0 + p0
-      const int m = n - p0 < 64 ? n - p0 : 64;
-      uint8_t* out = vb + n0 + p0;
-      if (m == 64 && ((n0 + p0) & 7) == 0) {
-        for (int i = tid; i < DH * 8; i += KA_T) {
-          const int d = i >> 3, o = (i & 7) * 8;
-          *reinterpret_cast<uint64_t*>(out + static_cast<int64_t>(d) * P + o) =
-              *reinterpret_cast<const uint64_t*>(vt + d * VROW + o);
-        }
-      } else {
-        for (int i = tid; i < DH * m; i += KA_T) {
-          const int d = i / m, o = i % m;
-          out[static_cast<int64_t>(d) * P + o] = vt[d * VROW + o];
-        }
-      }
-      __syncthreads();
+    u.slots = slots + u.t;
+    u.page0 = page << lg;
+    u.pages = limit;
+    u.blk = page * H + head;
+    u.kb = kp.cache + u.blk * static_cast<int64_t>(P) * DH;
+    u.vb = vp.cache + u.blk * static_cast<int64_t>(P) * DH;
+    if (u.n <= KA_SHORT) {
+      if ((turn++ & (KA_T / 64 - 1)) == wave) A::by_wave(kp, vp, ks, vs, u, P);
+    } else {
+      A::by_group(kp, vp, ks, vs, u, P, vt, sh_top);
     }
   }
 }

@@ -19,24 +19,6 @@
 
 namespace hyena {
 
-// Largest x over the 16 lanes of a row of the wave, in each of them.
-__device__ __forceinline__ uint32_t max16(uint32_t x) {
-  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xF, 0xF, true)));
-  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xF, 0xF, true)));
-  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xF, 0xF, true)));
-  x = up(x, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x140, 0xF, 0xF, true)));
-  return x;
-}
-__device__ __forceinline__ uint32_t max64(uint32_t x) {
-  x = max16(x);
-  const int l = static_cast<int>(threadIdx.x);
-  uint32_t o = __float_as_uint(xor16(__uint_as_float(x), l));
-  x = x > o ? x : o;
-  o = __float_as_uint(xor32(__uint_as_float(x), (l >> 5) & 1));
-  return x > o ? x : o;
-}
-
 // Sum (or maximum of magnitude bits) over the W waves of a row.
 template <int W>
 __device__ __forceinline__ float row_sum(float x, float* sh, int wave) {
