@@ -44,7 +44,8 @@ def flags() -> list[str]:
 # on the matrix cores, its 32 AGPRs would come on top of the 128 registers
 # that four waves per SIMD leave each wave.
 EXTRA_FLAGS = {
-    "attn_paged.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "attn_narrow.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "attn_wide.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "chunk_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fftconv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fir_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],

@@ -1,0 +1,502 @@
+// attn_narrow.hip -- attention over the paged cache for requests of up to 16
+// columns (attn_paged.hpp): single tokens, or a few with shared heads.  Bound by
+// reading the cache, 2 DH bytes per cached token and K/V head.
+//
+// All tiles of all units (a unit: one request on one K/V head) form one list,
+// and every wave takes the same number of consecutive ones: however the lengths
+// differ, all waves of one resident grid read equally much, from the first
+// cycle to the last.  A wave goes through its units one after another, the next
+// tile always in flight, across the border of two units as within one.  A unit
+// that lies within one wave's share is written by it; the others leave partial
+// results (m, l, O) in the workspace, at most two per wave, which
+// attn_narrow_join_kernel adds up.
+#include "attn_paged.hpp"
+
+namespace hyena {
+
+constexpr int AN_GROUPS = 512;                    // workgroups: two per CU, all resident
+constexpr int AN_WAVES = AN_GROUPS * (AT_T / 64);
+constexpr int AN_WHOLE = 4;                       // tables of up to so many tiles: a unit per wave, no join
+
+// Partial results: wave w's first unit, begun by an earlier wave, in slot 2 w,
+// its last one, continued by the next, in 2 w + 1; nt columns each.
+struct NarrowSpace {
+  int4* head;      // per wave: pieces of the unit that begins in it and ends elsewhere (0: none),
+                   // its first query token, K/V head, columns
+  float* ml;
+  float* o;
+};
+__device__ __forceinline__ NarrowSpace narrow_space(void* p, int nt) {
+  NarrowSpace s;
+  s.head = static_cast<int4*>(p);
+  s.ml = reinterpret_cast<float*>(s.head + AN_WAVES);
+  s.o = s.ml + static_cast<size_t>(2 * AN_WAVES) * 2 * nt;
+  return s;
+}
+
+// A tile in the list, and its request; the same in every lane.
+struct Place {
+  int r, head, tile, tiles;
+  int tok0, queries, len;
+  int ahead;                 // position of the request's first query
+};
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Tiles of a request per K/V head: 0 if it is not narrow or has no query, and
+// one (of masked tokens) if it has queries and nothing cached: their rows are
+// written too.
+__device__ __forceinline__ int unit_tiles(int queries, int len, int group, int limit) {
+  const int64_t cols = static_cast<int64_t>(queries) * group;
+  return cols > 0 && cols <= limit ? max((len + AT_TILE - 1) / AT_TILE, 1) : 0;
+}
+
+__device__ __forceinline__ void set_request(const AttnArgs& a, int limit, int r, Place& p) {
+  int t, q, n;
+  request_of(a, r, t, q, n);
+  p.r = r;
+  p.tok0 = uni(t);
+  p.queries = uni(q);
+  p.len = uni(n);
+  p.ahead = p.len - (min(a.cu[r + 1], a.T) - p.tok0);
+  p.tiles = uni(unit_tiles(p.queries, p.len, a.Hq / a.Hkv, limit));
+}
+
+// The tile after p; there is one.
+__device__ __forceinline__ void advance(const AttnArgs& a, int limit, Place& p) {
+  if (++p.tile < p.tiles) return;
+  p.tile = 0;
+  if (++p.head < a.Hkv) return;
+  p.head = 0;
+  do set_request(a, limit, p.r + 1, p); while (p.tiles == 0 && p.r + 1 < a.R);
+}
+
+struct NarrowShared {
+  unsigned long long before[AT_T], part[AT_T / 64];
+};
+
+// The share of wave `w`: its first tile `p`, its number in the list `at`, and
+// the tiles per wave; returns the wave's number of tiles.  Every thread of the
+// workgroup takes part.
+__device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, int w, NarrowShared& sh,
+                                                Place& p, long long& at, long long& per) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int group = a.Hq / a.Hkv;
+  auto weight = [&](int r) {
+    int t, q, n;
+    request_of(a, r, t, q, n);
+    return static_cast<long long>(unit_tiles(q, n, group, limit)) * a.Hkv;
+  };
+  auto share = [&](long long total) {
+    per = (total + AN_WAVES - 1) / AN_WAVES;
+    at = per * w;
+    return min(per, total - at);
+  };
+  auto into = [&](int r, long long rest) {
+    set_request(a, limit, r, p);
+    p.head = uni(static_cast<int>(rest / p.tiles));
+    p.tile = uni(static_cast<int>(rest % p.tiles));
+  };
+  auto shfl = [](long long x, int from) { return __shfl(x, from); };
+
+  if (a.R == 1) {
+    const long long n = share(weight(0));
+    if (n > 0) into(0, at);
+    return n;
+  }
+  if (a.R <= 64) {
+    const long long mine = lane < a.R ? weight(lane) : 0;
+    long long end = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const long long x = __shfl_up(end, o);
+      if (lane >= o) end += x;
+    }
+    const long long n = share(shfl(end, 63));
+    if (n <= 0) return n;
+    const int r = __ffsll(static_cast<long long>(__ballot(at < end))) - 1;
+    into(uni(r), at - shfl(end - mine, r));
+    return n;
+  }
+  const int run = (a.R + AT_T - 1) / AT_T;
+  const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += weight(r);
+  long long end = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const long long x = __shfl_up(end, o);
+    if (lane >= o) end += x;
+  }
+  if (lane == 63) sh.part[wave] = end;
+  __syncthreads();
+  long long total = 0, base = 0;
+#pragma unroll
+  for (int i = 0; i < AT_T / 64; ++i) {
+    if (i < wave) base += sh.part[i];
+    total += sh.part[i];
+  }
+  sh.before[tid] = base + end - mine;
+  __syncthreads();
+  const long long n = share(total);
+  if (n <= 0) return n;
+  // the last thread whose requests begin at or before `at`
+  int t = 0;
+#pragma unroll
+  for (int i = 0; i < AT_T / 64; ++i) {
+    const unsigned long long le = __ballot(static_cast<long long>(sh.before[64 * i + lane]) <= at);
+    if (le) t = 64 * i + 63 - __clzll(static_cast<long long>(le));
+  }
+  t = uni(t);
+  long long rest = at - static_cast<long long>(sh.before[t]);
+  int r = t * run;
+  for (;;) {
+    const long long x = weight(r);
+    if (rest < x) break;
+    rest -= x;
+    ++r;                                  // ends: the thread's requests hold the tile
+  }
+  into(uni(r), rest);
+  return n;
+}
+
+// Lane l: i = l % 16 is its row of A (token of K, dimension of V^T) and its
+// column of B and C, g = l / 16 its 16-token run of the tile.  Row i of K's
+// sub-tile t is token 16 (i / 4) + 4 t + i % 4, so that C's rows 4 g + r of the
+// four sub-tiles are the run's tokens 4 t + r, in order: the operand of the
+// second product.
+//
+// Two waves per SIMD with 16 KiB of the next tile in flight each: 128 KiB per
+// CU, against ~25 bytes a cycle that a CU's share of HBM delivers in ~2000
+// cycles of latency.
+template <typename IO, int DH, bool WHOLE>
+__global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int limit, void* space, int nt) {
+  constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
+  constexpr int KH = DH / 64;            // 16-byte loads per K row and lane
+  constexpr int KS = DH / 32;            // MFMA steps over the head dimension
+  constexpr int DT = DH / 16;            // 16-row tiles of O^T
+  __shared__ NarrowShared sh;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int i = lane & 15, g = lane >> 4;
+  const int wave = uni(static_cast<int>(blockIdx.x) * (AT_T / 64) + (tid >> 6));
+  const int group = a.Hq / a.Hkv;
+  const NarrowSpace ws = narrow_space(space, nt);
+  Place cur;
+  long long at = 0, per = 1, left;
+  if constexpr (WHOLE) {
+    if (wave >= static_cast<int64_t>(a.R) * a.Hkv) return;
+    set_request(a, limit, wave / a.Hkv, cur);
+    cur.head = wave % a.Hkv;
+    cur.tile = 0;
+    left = cur.tiles;
+  } else {
+    left = find_share(a, limit, wave, sh, cur, at, per);
+  }
+  int4 header{0, 0, 0, 0};
+  if (left > 0) {
+    const int lg = a.page_lg, pmask = (1 << lg) - 1;
+    const int64_t page_bytes = (static_cast<int64_t>(a.Hkv) << lg) * DH;
+    const float scale2 = a.scale * AT_LOG2E;
+
+    u32x4 kr[4][KH], vr[DT];
+    float ks, vs;
+    bf16x8 qf[KS][NS];
+    int ck, cv;                            // pages of the tile to load next: of K's run, of this lane's run
+    auto pages = [&](const Place& p) {
+      const int32_t* table = a.block_table + p.r * a.table_stride;
+      ck = table_page(a, table, p.tile * AT_TILE + 16 * (i >> 2), p.len);
+      cv = table_page(a, table, p.tile * AT_TILE + 16 * g, p.len);
+    };
+    auto load_k = [&](const Place& p) {
+      const uint8_t* at0 = a.k_cache + max(ck, 0) * page_bytes + ((static_cast<int64_t>(p.head) << lg) * DH) + 16 * g;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int tok = p.tile * AT_TILE + 16 * (i >> 2) + 4 * t + (i & 3);
+#pragma unroll
+        for (int h = 0; h < KH; ++h)
+          kr[t][h] = *reinterpret_cast<const u32x4*>(at0 + (tok & pmask) * DH + 64 * h);
+      }
+      const int64_t si = static_cast<int64_t>(max(cv, 0)) * a.Hkv + p.head;
+      ks = a.k_scale[si];
+      vs = a.v_scale[si];
+    };
+    auto load_v = [&](const Place& p, int page) {
+      const uint8_t* at0 = a.v_cache + max(page, 0) * page_bytes + ((static_cast<int64_t>(p.head) << lg) * DH) +
+                           ((p.tile * AT_TILE + 16 * g) & pmask);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        vr[d] = *reinterpret_cast<const u32x4*>(at0 + (static_cast<int64_t>(16 * d + i) << lg));
+    };
+    auto load_q = [&](const Place& p) {
+      const int cols = p.queries * group;
+      const IO* qp = static_cast<const IO*>(a.q) + (p.tok0 + i / group) * a.q_tok +
+                     (static_cast<int64_t>(p.head) * group + i % group) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float x[8] = {};
+        if (i < cols) load8(qp + 64 * (s >> 1) + 16 * g + 8 * (s & 1), 8, x);
+        parts<NS>(x, qf[s]);
+      }
+    };
+
+    f32x4 o[DT];
+    float m, l;
+    auto clear = [&]() {
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      m = AT_NEG;
+      l = 0.0f;
+    };
+
+    Place next = cur, later;
+    int from = cur.tile;                   // the unit's first tile in this share
+    pages(cur);
+    load_q(cur);
+    load_k(cur);
+    int pv = cv;
+    load_v(cur, pv);
+    if (left > 1) {
+      advance(a, limit, next);
+      pages(next);
+    }
+    clear();
+    for (;;) {
+      // cur is loaded or in flight; next's pages are known
+      const float c = ks * scale2;
+      const bool more = left > 1;
+      f32x4 s[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const u32x4 raw = kr[t][k >> 1];
+          const bf16x8 kf = (k & 1) ? widen(raw[2], raw[3]) : widen(raw[0], raw[1]);
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) s[t] = mfma16(kf, qf[k][n], s[t]);
+        }
+      }
+      const float v_scale = pv >= 0 ? vs : 0.0f;
+      const int run0 = cur.tile * AT_TILE + 16 * g;
+      const int places = pv >= 0 ? min(max(cur.len - run0, 0), 16) : 0;
+      if (more) load_k(next);
+
+      const int pos = cur.ahead + i / group;               // last token this column sees
+      float x[4][4];
+      float top = AT_NEG;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[t][r] = s[t][r] * c;
+      // masks where a run is not whole or some column does not see all of it
+      if (__any(places < 16) || cur.tile * AT_TILE + AT_TILE - 1 > cur.ahead) {
+        const int lim = min(places, pos - run0 + 1);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * t + r >= lim) x[t][r] = AT_NEG;
+        // 0 * NaN: whatever lies past the end must not reach the product
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vr[d][e] = keep_places(vr[d][e], e, places);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, x[t][r]);
+      top = fmaxf(top, xor16(top, lane));
+      top = fmaxf(top, xor32(top, lane >> 5));
+      const float m_new = fmaxf(m, top);
+      const float base = m_new == AT_NEG ? 0.0f : m_new;    // nothing seen yet: 2^-inf = 0
+      if (__any(m_new > m)) {
+        const float f = __builtin_amdgcn_exp2f(m - base);
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+      m = m_new;
+      bf16x8 pf[2][NS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - base);
+          l += p[e];
+          p[e] *= v_scale;
+        }
+        parts<NS>(p, pf[h]);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bf16x8 vf = widen(vr[d][2 * h], vr[d][2 * h + 1]);
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) o[d] = mfma16(vf, pf[h][n], o[d]);
+        }
+      }
+      if (more) {
+        pv = cv;
+        load_v(next, pv);
+        later = next;
+        if (left > 2) {
+          advance(a, limit, later);
+          pages(later);
+        }
+      }
+
+      const bool ends = cur.tile + 1 == cur.tiles;
+      if (ends || !more) {
+        // leave the unit: its columns are on lanes i of every g
+        l += xor16(l, lane);
+        l += xor32(l, lane >> 5);
+        const int cols = cur.queries * group;
+        if (i < cols) {
+          if (from == 0 && ends) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(cur.tok0) + i / group) * a.Hq +
+                                                static_cast<int64_t>(cur.head) * group + i % group) * DH;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) Io<IO>::st(op, 16 * d + 4 * g + r, o[d][r] * inv);
+          } else {
+            const int64_t slot = 2 * static_cast<int64_t>(wave) + (from == 0 ? 1 : 0);
+            if (g == 0) {
+              ws.ml[(slot * 2) * nt + i] = m;
+              ws.ml[(slot * 2 + 1) * nt + i] = l;
+            }
+            float* op = ws.o + (slot * nt + i) * DH;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(op + 16 * d + 4 * g) = o[d];
+          }
+        }
+        if (from == 0 && !ends) {
+          // begun here, continued by the waves up to the one with its last tile
+          const long long last = at + per - 1 + (cur.tiles - 1 - cur.tile);
+          header = make_int4(static_cast<int>(last / per) - wave + 1, cur.tok0, cur.head, cols);
+        }
+        if (!more) break;
+        clear();
+        from = 0;
+        load_q(next);
+      }
+      cur = next;
+      next = later;
+      --left;
+    }
+  }
+  if (!WHOLE && lane == 0) ws.head[wave] = header;
+}
+
+// Joins the pieces of the unit that begins in wave blockIdx.x and ends in a
+// later one:  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p.  Lanes: DH / 4
+// per column, four values each; the sets of lanes that the unit's columns
+// leave over take every other (fourth, ...) piece and are added through LDS.
+// Workgroups y share the columns of a unit.
+template <typename IO, int DH>
+__global__ __launch_bounds__(AT_T) void attn_narrow_join_kernel(AttnArgs a, void* space, int nt) {
+  constexpr int LPC = DH / 4;
+  constexpr int SETS = AT_T / LPC;
+  __shared__ float s_m[SETS], s_l[SETS];
+  __shared__ __align__(16) f32x4 s_o[SETS][LPC];
+  const NarrowSpace ws = narrow_space(space, nt);
+  const int w = blockIdx.x;
+  const int4 h = ws.head[w];               // pieces, first query token, head, columns
+  if (h.x == 0) return;
+  const int group = a.Hq / a.Hkv;
+  const int set = threadIdx.x / LPC, d = (threadIdx.x % LPC) * 4;
+  const int mine = (h.w - static_cast<int>(blockIdx.y) + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+  int lg = 0;                              // log2 of the columns side by side
+  while ((1 << lg) < mine && (1 << lg) < SETS) ++lg;
+  const int side = 1 << lg, ways = SETS >> lg, way = set >> lg;
+  for (int c0 = 0; c0 < mine; c0 += side) {
+    const int k = c0 + (set & (side - 1));
+    const int c = static_cast<int>(blockIdx.y) + k * static_cast<int>(gridDim.y);
+    float m = AT_NEG, l = 0.0f;
+    f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    if (k < mine) {
+#pragma unroll 8
+      for (int p = way; p < h.x; p += ways) {
+        const int64_t slot = 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0);
+        const float pm = ws.ml[(slot * 2) * nt + c], pl = ws.ml[(slot * 2 + 1) * nt + c];
+        const f32x4 po = *reinterpret_cast<const f32x4*>(ws.o + (slot * nt + c) * DH + d);
+        const float big = fmaxf(m, pm);
+        const float fo = m == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(m - big);
+        const float fp = pm == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(pm - big);
+        l = l * fo + pl * fp;
+        o = o * fo + po * fp;
+        m = big;
+      }
+    }
+    if (ways > 1) {
+      if (d == 0) {
+        s_m[set] = m;
+        s_l[set] = l;
+      }
+      s_o[set][d >> 2] = o;
+      __syncthreads();
+      float big = AT_NEG;
+      for (int y = 0; y < ways; ++y) big = fmaxf(big, s_m[(y << lg) + (set & (side - 1))]);
+      l = 0.0f;
+      o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int y = 0; y < ways; ++y) {
+        const int z = (y << lg) + (set & (side - 1));
+        const float f = s_m[z] == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(s_m[z] - big);
+        l += f * s_l[z];
+        o += f * s_o[z][d >> 2];
+      }
+      __syncthreads();
+    }
+    if (way == 0 && k < mine) {
+      IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(h.y) + c / group) * a.Hq +
+                                          static_cast<int64_t>(h.z) * group + c % group) * DH + d;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Io<IO>::st(op, e, o[e] * inv);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+static bool whole(int64_t max_pages, int page_lg) {
+  return (max_pages << page_lg) <= AN_WHOLE * AT_TILE;
+}
+
+size_t attn_narrow_workspace(int64_t max_pages, int page_lg, int64_t cols, int DH) {
+  if (whole(max_pages, page_lg)) return 0;
+  const int64_t nt = cols < AT_NARROW ? cols : AT_NARROW;
+  return static_cast<size_t>(AN_WAVES) * (sizeof(int4) + 2 * 4 * (2 * nt + nt * DH));
+}
+
+hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* workspace) {
+  const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
+  const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
+  auto go = [&](auto one, auto many, auto join) {
+    if (whole(a.max_pages, a.page_lg)) {
+      const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
+      one<<<static_cast<unsigned>((units + 3) / 4), AT_T, 0, a.stream>>>(a, limit, nullptr, nt);
+      return;
+    }
+    many<<<AN_GROUPS, AT_T, 0, a.stream>>>(a, limit, workspace, nt);
+    join<<<dim3(AN_WAVES, nt < 4 ? nt : 4), AT_T, 0, a.stream>>>(a, workspace, nt);
+  };
+  if (a.bf16) {
+    if (a.DH == 64)
+      go(attn_narrow_kernel<bf16_t, 64, true>, attn_narrow_kernel<bf16_t, 64, false>, attn_narrow_join_kernel<bf16_t, 64>);
+    else
+      go(attn_narrow_kernel<bf16_t, 128, true>, attn_narrow_kernel<bf16_t, 128, false>, attn_narrow_join_kernel<bf16_t, 128>);
+  } else {
+    if (a.DH == 64)
+      go(attn_narrow_kernel<float, 64, true>, attn_narrow_kernel<float, 64, false>, attn_narrow_join_kernel<float, 64>);
+    else
+      go(attn_narrow_kernel<float, 128, true>, attn_narrow_kernel<float, 128, false>, attn_narrow_join_kernel<float, 128>);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace hyena

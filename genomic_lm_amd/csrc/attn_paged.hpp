@@ -1,0 +1,103 @@
+// attn_paged.hpp -- attention over the paged 8-bit K/V cache (kv_append.hip):
+// what the two kernels share (attn_narrow.hip, attn_wide.hip).
+//
+// The striped attention blocks (evo2_flash README, layer_names table and
+// options table: attention beside the Hyena mixers, K/V cache in 8 bits).
+// Request r owns query tokens cu[r] .. cu[r+1] and lens[r] cached tokens, its
+// queries being the last of them; query head h reads K/V head h / G.  With c =
+// scale * k_scale * log2 e per block and query i at position
+// pos = lens - (queries) + i,
+//     s_j = c q.k_j (j <= pos),  m = max s,  l = sum 2^(s_j - m),
+//     o = sum 2^(s_j - m) v_scale v_j / l,   0 where no token is seen.
+//
+// The columns of the matrix products are (query, query head of the group)
+// pairs of one K/V head, so the heads that share a K/V head read it once.
+// S^T = K Q^T puts tokens on the rows: a lane then holds 16 consecutive
+// tokens of one column, the softmax of a column is its registers and one or
+// two lane exchanges, and the result is already the operand of O^T = V^T P^T.
+// V is stored transposed for that product.  e4m3 values are exact in bf16, so
+// codes are widened in registers and the block scales are applied to S and P.
+#pragma once
+
+#include "fp8.hpp"
+#include "mfma_common.hpp"
+#include "serving.hpp"
+
+namespace hyena {
+
+constexpr float AT_LOG2E = 1.44269504088896340736f;
+constexpr float AT_NEG = -__builtin_inff();
+constexpr int AT_T = 256;                 // threads
+constexpr int AT_TILE = 64;               // cached tokens per tile
+constexpr int AT_NARROW = 16;             // columns up to which a request is narrow
+
+__device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, int& queries, int& len) {
+  const int c0 = a.cu[r], c1 = min(a.cu[r + 1], a.T);
+  tok0 = max(c0, 0);
+  queries = min(max(c1 - tok0, 0), a.max_q);
+  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_lg;
+  len = static_cast<int>(min<int64_t>(max(a.lens[r], 0), cap));
+}
+
+// ---------------------------------------------------------------- operands
+// Eight codes to bf16 (exact).
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
+  bf16x8 r;
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+  r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+  return r;
+}
+
+// Eight floats as NS bf16 parts: one rounding (NS = 1: bf16 queries are exact,
+// and P's 2^-9 per weight is below the output's own rounding), or three that
+// carry fp32 (NS = 3, fp32 activations).
+template <int NS>
+__device__ __forceinline__ void parts(const float (&x)[8], bf16x8 (&p)[NS]) {
+  if constexpr (NS == 1) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = cvt2(x[2 * e], x[2 * e + 1]);
+    p[0] = __builtin_bit_cast(bf16x8, w);
+  } else {
+    u32x4 w0, w1, w2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t a, b, c;
+      split3_pair(x[2 * e], x[2 * e + 1], a, b, c);
+      w0[e] = a;
+      w1[e] = b;
+      w2[e] = c;
+    }
+    p[0] = __builtin_bit_cast(bf16x8, w0);
+    p[1] = __builtin_bit_cast(bf16x8, w1);
+    p[2] = __builtin_bit_cast(bf16x8, w2);
+  }
+}
+
+// Codes of places >= n of the four in word `at` (places 4 at .. 4 at + 3) to 0.
+__device__ __forceinline__ uint32_t keep_places(uint32_t w, int at, int n) {
+  const int k = n - 4 * at;
+  return k >= 4 ? w : k <= 0 ? 0u : w & ((1u << (8 * k)) - 1);
+}
+
+// The page of a token.
+__device__ __forceinline__ int table_page(const AttnArgs& a, const int32_t* table, int tok, int len) {
+  const int j = tok >> a.page_lg;
+  // -1 past the end or where the table holds no page
+  const int p = tok < len && j < a.max_pages ? table[j] : -1;
+  return p >= 0 && p < a.num_pages ? p : -1;
+}
+
+// Requests of up to `limit` columns (attn_narrow.hip) and of more than `limit`
+// (attn_wide.hip), each with its launches, workspace and largest grid.
+hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* workspace);
+hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* workspace);
+size_t attn_narrow_workspace(int64_t max_pages, int page_lg, int64_t cols, int DH);
+size_t attn_wide_workspace(int64_t max_pages, int page_lg, int DH);
+int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv);
+
+}  // namespace hyena

@@ -94,12 +94,10 @@ struct AttnArgs {
   void* workspace;
   hipStream_t stream;
 };
-// Whether the launch grid of the shape exists, and the workspace it needs (0:
-// the table is too short for a request's tokens to be split).
-bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t max_pages, int page_lg,
-                     int64_t Hq, int64_t Hkv);
-size_t attn_paged_workspace(int64_t max_q, int64_t max_pages, int page_lg, int64_t Hq, int64_t Hkv,
-                            int DH);
+// Whether the launch grids of the shape exist, and the workspace it needs.
+bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv);
+size_t attn_paged_workspace(int64_t R, int64_t max_q, int64_t max_pages, int page_lg, int64_t Hq,
+                            int64_t Hkv, int DH);
 hipError_t launch_attn_paged(const AttnArgs& a);
 
 }  // namespace hyena

@@ -163,7 +163,7 @@ static hyena_status_t check_attn(int64_t R, int64_t T, int64_t max_q, int64_t ma
     return HYENA_ERR_INVALID_ARG;
   if (lg < 0 || (DH != 64 && DH != 128) || R > HYENA_MAX_REQUESTS || Hq > HYENA_MAX_HEADS ||
       T > kMaxInt || max_q > kMaxInt || max_pages > ((kMaxInt - 1024) >> lg) ||
-      (Hq > 0 && !hyena::attn_paged_fits(R, T, max_q, max_pages, lg, Hq, Hkv)))
+      (Hq > 0 && !hyena::attn_paged_fits(R, T, max_q, Hq, Hkv)))
     return HYENA_ERR_UNSUPPORTED;
   return HYENA_OK;
 }
@@ -195,14 +195,14 @@ hyena_status_t hyena_attn_paged_fp8(const void* q, int64_t q_tok_stride, int64_t
   if (q_tok_stride > most / T || q_head_stride > most / Hq || !fits(T, Hq * DH * 4) ||
       !fits(table_stride, 4 * R))
     return HYENA_ERR_UNSUPPORTED;
-  const size_t need = hyena::attn_paged_workspace(max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
+  const size_t need = hyena::attn_paged_workspace(R, max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
   if (need > 0 && (!workspace || ws_bytes < need || !aligned_to(workspace, 16)))
     return HYENA_ERR_WORKSPACE;
   hyena::AttnArgs n{q, q_tok_stride, q_head_stride, k_cache, v_cache, k_scale, v_scale, num_pages,
                     lg, block_table, table_stride, static_cast<int>(max_pages), lens, cu,
                     static_cast<int>(R), static_cast<int>(T), static_cast<int>(max_q),
                     static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(DH), scale, out,
-                    io == HYENA_BF16, need > 0 ? workspace : nullptr, stream};
+                    io == HYENA_BF16, workspace, stream};
   return from_hip(hyena::launch_attn_paged(n));
 }
 
@@ -211,7 +211,7 @@ size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int6
   const int lg = page_lg(page_size);
   if (check_attn(R, T, max_q, max_pages, lg, Hq, Hkv, DH) != HYENA_OK) return 0;
   if (R == 0 || T == 0 || max_q == 0 || Hq == 0) return 0;
-  return hyena::attn_paged_workspace(max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
+  return hyena::attn_paged_workspace(R, max_q, max_pages, lg, Hq, Hkv, static_cast<int>(DH));
 }
 
 }  // extern "C"

@@ -14,6 +14,7 @@ new_cache() allocates them.  A step of a model maps its new tokens to slots once
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -64,6 +65,13 @@ def _vec(name, t, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _like(x, dtype=None):
+    """An uninitialised contiguous tensor of x's shape (the shortest path to one)."""
+    if x.is_contiguous():
+        return torch.empty_like(x, dtype=dtype)
+    return torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+
+
 def _norm_args(x, weight, residual, residual_out):
     xp, xs = _rows("x", x)
     D, dev = x.shape[-1], x.get_device()
@@ -73,7 +81,7 @@ def _norm_args(x, weight, residual, residual_out):
     if residual is not None:
         rp, rs = _rows("residual", residual, x)
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            residual_out = _like(x)
         rop, ros = _rows("residual_out", residual_out, x)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
@@ -89,7 +97,7 @@ def add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out=None, resi
     x, residual_out may be residual or x."""
     head, tail, residual_out = _norm_args(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _like(x)
     yp, ys = _rows("out", out, x)
     _check("hyena_add_rmsnorm", lib().hyena_add_rmsnorm(*head, eps, yp, ys, *tail))
     return out, residual_out
@@ -107,9 +115,9 @@ def add_rmsnorm_fp8(x, weight=None, residual=None, eps: float = 1e-6, group: int
     shape, dev = x.shape, x.get_device()
     sshape = shape[:-1] if group == 0 else (*shape[:-1], (shape[-1] + group - 1) // group)
     if q is None:
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        q = _like(x, torch.float8_e4m3fn)
     if scale is None:
-        scale = torch.empty(sshape, dtype=torch.float32, device=x.device)
+        scale = x.new_empty(sshape, dtype=torch.float32)
     qp = _vec("q", q, q.dtype if getattr(q, "dtype", None) in _FP8 else torch.float8_e4m3fn, shape, dev)
     sp = _vec("scale", scale, torch.float32, sshape, dev)
     _check("hyena_add_rmsnorm_fp8", lib().hyena_add_rmsnorm_fp8(*head, eps, qp, sp, group, *tail))
@@ -140,23 +148,20 @@ def page_map(old_lens, new_lens, block_table, free_pages, free_head, page_size: 
     (T) int32, slots (T) int64 and status (2) int32: the free list's new head and
     the number of new tokens without a page."""
     tp, step, R, width = _table(block_table)
-    dev, device = block_table.get_device(), block_table.device
+    dev = block_table.get_device()
     i32 = torch.int32
     op = _vec("old_lens", old_lens, i32, (R,), dev)
     np_ = _vec("new_lens", new_lens, i32, (R,), dev)
     fp = _vec("free_pages", free_pages, i32, None, dev)
     hp = None if free_head is None else _vec("free_head", free_head, i32, (1,), dev)
     T = int(T)
-    if cu is None:
-        cu = torch.empty(R + 1, dtype=i32, device=device)
-    if lens is None:
-        lens = torch.empty(R, dtype=i32, device=device)
-    if positions is None:
-        positions = torch.empty(T, dtype=i32, device=device)
+    if cu is None or lens is None or positions is None or status is None:
+        # one allocation for the outputs that were not given
+        a, b, c, d = block_table.new_empty(2 * R + T + 3).split_with_sizes((R + 1, R, T, 2))
+        cu, lens = a if cu is None else cu, b if lens is None else lens
+        positions, status = c if positions is None else positions, d if status is None else status
     if slots is None:
-        slots = torch.empty(T, dtype=torch.int64, device=device)
-    if status is None:
-        status = torch.empty(2, dtype=i32, device=device)
+        slots = block_table.new_empty(T, dtype=torch.int64)
     cp, lp = _vec("cu", cu, i32, (R + 1,), dev), _vec("lens", lens, i32, (R,), dev)
     pp, slp = _vec("positions", positions, i32, (T,), dev), _vec("slots", slots, torch.int64, (T,), dev)
     stp = _vec("status", status, i32, (2,), dev)
@@ -216,6 +221,7 @@ def kv_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale) -> None:
         *kp, *vp, sp, kc, vc, ks, vs, N, P, T, H, DH, _io(k), _stream(k)))
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_paged_workspace_size(R: int, T: int, max_q: int, max_pages: int, page_size: int, Hq: int,
                               Hkv: int, DH: int) -> int:
     return int(lib().hyena_attn_paged_workspace_size(R, T, max_q, max_pages, page_size, Hq, Hkv, DH))
@@ -238,14 +244,15 @@ def attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu,
     lp = _vec("lens", lens, torch.int32, (R,), dev)
     cp = _vec("cu", cu, torch.int32, (R + 1,), dev)
     if out is None:
-        out = torch.empty((T, Hq, DH), dtype=q.dtype, device=q.device)
+        out = _like(q)
         op = out.data_ptr()
     else:
         op = _vec("out", out, q.dtype, q.shape, dev)
     max_q = int(max_q)
-    need = lib().hyena_attn_paged_workspace_size(R, T, max_q, width, P, Hq, Hkv, DH) if Hkv else 0
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        need = attn_paged_workspace_size(R, T, max_q, width, P, Hq, Hkv, DH)
+        if need:
+            workspace = q.new_empty(need, dtype=torch.uint8)
     wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(),
                                                   workspace.numel() * workspace.element_size())
     _check("hyena_attn_paged_fp8", lib().hyena_attn_paged_fp8(
