@@ -41,8 +41,6 @@ struct Place {
   int ahead;                 // position of the request's first query
 };
 
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // Tiles of a request per K/V head: 0 if it is not narrow or has no query, and
 // one (of masked tokens) if it has queries and nothing cached: their rows are
 // written too.
@@ -52,14 +50,14 @@ __device__ __forceinline__ int unit_tiles(int queries, int len, int group, int l
 }
 
 __device__ __forceinline__ void set_request(const AttnArgs& a, int limit, int r, Place& p) {
-  int t, q, n;
-  request_of(a, r, t, q, n);
+  const int end = min(scalar(a.cu + r + 1), a.T);
   p.r = r;
-  p.tok0 = uni(t);
-  p.queries = uni(q);
-  p.len = uni(n);
-  p.ahead = p.len - (min(a.cu[r + 1], a.T) - p.tok0);
-  p.tiles = uni(unit_tiles(p.queries, p.len, a.Hq / a.Hkv, limit));
+  p.tok0 = max(scalar(a.cu + r), 0);
+  p.queries = min(max(end - p.tok0, 0), a.max_q);
+  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_lg;
+  p.len = static_cast<int>(min<int64_t>(max(scalar(a.lens + r), 0), cap));
+  p.ahead = p.len - (end - p.tok0);
+  p.tiles = unit_tiles(p.queries, p.len, a.Hq / a.Hkv, limit);
 }
 
 // The tile after p; there is one.
@@ -169,7 +167,7 @@ __device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, in
 // Two waves per SIMD with 16 KiB of the next tile in flight each: 128 KiB per
 // CU, against ~25 bytes a cycle that a CU's share of HBM delivers in ~2000
 // cycles of latency.
-template <typename IO, int DH, bool WHOLE>
+template <typename IO, int DH, bool BIG>
 __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int limit, void* space, int nt) {
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
   constexpr int KH = DH / 64;            // 16-byte loads per K row and lane
@@ -183,50 +181,60 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
   const int group = a.Hq / a.Hkv;
   const NarrowSpace ws = narrow_space(space, nt);
   Place cur;
-  long long at = 0, per = 1, left;
-  if constexpr (WHOLE) {
+  long long at = 0, per = 1;
+  int left;
+  if (!space) {                          // short tables: a unit per wave
     if (wave >= static_cast<int64_t>(a.R) * a.Hkv) return;
     set_request(a, limit, wave / a.Hkv, cur);
     cur.head = wave % a.Hkv;
     cur.tile = 0;
     left = cur.tiles;
   } else {
-    left = find_share(a, limit, wave, sh, cur, at, per);
+    left = uni(static_cast<int>(find_share(a, limit, wave, sh, cur, at, per)));
   }
   int4 header{0, 0, 0, 0};
   if (left > 0) {
     const int lg = a.page_lg, pmask = (1 << lg) - 1;
     const int64_t page_bytes = (static_cast<int64_t>(a.Hkv) << lg) * DH;
     const float scale2 = a.scale * AT_LOG2E;
+    const int krow = 16 * (i >> 2) + (i & 3);            // this lane's token of K's sub-tile 0
 
     u32x4 kr[4][KH], vr[DT];
-    float ks, vs;
     bf16x8 qf[KS][NS];
-    int ck, cv;                            // pages of the tile to load next: of K's run, of this lane's run
-    auto pages = [&](const Place& p) {
-      const int32_t* table = a.block_table + p.r * a.table_stride;
-      ck = table_page(a, table, p.tile * AT_TILE + 16 * (i >> 2), p.len);
-      cv = table_page(a, table, p.tile * AT_TILE + 16 * g, p.len);
+    auto pages_of = [&](const Place& p) {
+      return tile_pages<BIG>(a, a.block_table + p.r * a.table_stride, p.tile, p.len);
     };
-    auto load_k = [&](const Place& p) {
-      const uint8_t* at0 = a.k_cache + max(ck, 0) * page_bytes + ((static_cast<int64_t>(p.head) << lg) * DH) + 16 * g;
+    // the block of a page; per lane unless BIG
+    auto block = [&](const uint8_t* cache, int page, int head) {
+      return cache + max(page, 0) * page_bytes + ((static_cast<int64_t>(head) << lg) * DH);
+    };
+    auto load_k = [&](const Place& p, const PerRun<int, BIG>& pages) {
+      const uint8_t* b = block(a.k_cache, pages.at(i >> 2), p.head);
+      int off;
+      if constexpr (BIG) {
+        b += ((p.tile * AT_TILE) & pmask) * DH;
+        off = krow * DH + 16 * g;
+      } else {
+        off = ((p.tile * AT_TILE + krow) & pmask) * DH + 16 * g;   // 4 t + krow stays in the run's page
+      }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int tok = p.tile * AT_TILE + 16 * (i >> 2) + 4 * t + (i & 3);
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int h = 0; h < KH; ++h)
-          kr[t][h] = *reinterpret_cast<const u32x4*>(at0 + (tok & pmask) * DH + 64 * h);
-      }
-      const int64_t si = static_cast<int64_t>(max(cv, 0)) * a.Hkv + p.head;
-      ks = a.k_scale[si];
-      vs = a.v_scale[si];
+          kr[t][h] = *reinterpret_cast<const u32x4*>(b + off + 4 * t * DH + 64 * h);
     };
-    auto load_v = [&](const Place& p, int page) {
-      const uint8_t* at0 = a.v_cache + max(page, 0) * page_bytes + ((static_cast<int64_t>(p.head) << lg) * DH) +
-                           ((p.tile * AT_TILE + 16 * g) & pmask);
+    auto load_v = [&](const Place& p, const PerRun<int, BIG>& pages) {
+      const uint8_t* b = block(a.v_cache, pages.at(g), p.head);
+      int off;
+      if constexpr (BIG) {
+        b += (p.tile * AT_TILE) & pmask;
+        off = (i << lg) + 16 * g;
+      } else {
+        off = (i << lg) + ((p.tile * AT_TILE + 16 * g) & pmask);
+      }
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        vr[d] = *reinterpret_cast<const u32x4*>(at0 + (static_cast<int64_t>(16 * d + i) << lg));
+        vr[d] = *reinterpret_cast<const u32x4*>(b + off + (d << (lg + 4)));
     };
     auto load_q = [&](const Place& p) {
       const int cols = p.queries * group;
@@ -249,22 +257,24 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       l = 0.0f;
     };
 
-    Place next = cur, later;
+    Place next = cur, later = cur;
     int from = cur.tile;                   // the unit's first tile in this share
-    pages(cur);
+    PerRun<int, BIG> pg = pages_of(cur), pg_next = pg, pg_later = pg;
     load_q(cur);
-    load_k(cur);
-    int pv = cv;
-    load_v(cur, pv);
+    load_k(cur, pg);
+    load_v(cur, pg);
+    PerRun<float, BIG> ks = run_scales(a, a.k_scale, pg, cur.head), vs = run_scales(a, a.v_scale, pg, cur.head);
     if (left > 1) {
       advance(a, limit, next);
-      pages(next);
+      pg_next = pages_of(next);
     }
     clear();
     for (;;) {
-      // cur is loaded or in flight; next's pages are known
-      const float c = ks * scale2;
+      // cur is in flight or loaded, next's pages are known
       const bool more = left > 1;
+      const float c = ks.at(g) * scale2;
+      const int page = pg.at(g);
+      const float v_scale = page >= 0 ? vs.at(g) : 0.0f;
       f32x4 s[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -277,10 +287,13 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
           for (int n = NS - 1; n >= 0; --n) s[t] = mfma16(kf, qf[k][n], s[t]);
         }
       }
-      const float v_scale = pv >= 0 ? vs : 0.0f;
       const int run0 = cur.tile * AT_TILE + 16 * g;
-      const int places = pv >= 0 ? min(max(cur.len - run0, 0), 16) : 0;
-      if (more) load_k(next);
+      const int places = page >= 0 ? min(max(cur.len - run0, 0), 16) : 0;
+      if (more) {
+        load_k(next, pg_next);
+        ks = run_scales(a, a.k_scale, pg_next, next.head);
+        vs = run_scales(a, a.v_scale, pg_next, next.head);
+      }
 
       const int pos = cur.ahead + i / group;               // last token this column sees
       float x[4][4];
@@ -340,12 +353,11 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
         }
       }
       if (more) {
-        pv = cv;
-        load_v(next, pv);
-        later = next;
+        load_v(next, pg_next);
         if (left > 2) {
+          later = next;
           advance(a, limit, later);
-          pages(later);
+          pg_later = pages_of(later);
         }
       }
 
@@ -387,10 +399,12 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       }
       cur = next;
       next = later;
+      pg = pg_next;
+      pg_next = pg_later;
       --left;
     }
   }
-  if (!WHOLE && lane == 0) ws.head[wave] = header;
+  if (space && lane == 0) ws.head[wave] = header;
 }
 
 // Joins the pieces of the unit that begins in wave blockIdx.x and ends in a
@@ -476,14 +490,20 @@ size_t attn_narrow_workspace(int64_t max_pages, int page_lg, int64_t cols, int D
 hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* workspace) {
   const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
   const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
-  auto go = [&](auto one, auto many, auto join) {
+  const bool big = (1 << a.page_lg) >= AT_TILE;
+  auto go = [&](auto big_pages, auto small_pages, auto join) {
+    auto launch = [&](unsigned grid, void* space) {
+      if (big) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
+      else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
+    };
+    const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
     if (whole(a.max_pages, a.page_lg)) {
-      const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
-      one<<<static_cast<unsigned>((units + 3) / 4), AT_T, 0, a.stream>>>(a, limit, nullptr, nt);
+      launch(static_cast<unsigned>((units + 3) / 4), nullptr);
       return;
     }
-    many<<<AN_GROUPS, AT_T, 0, a.stream>>>(a, limit, workspace, nt);
-    join<<<dim3(AN_WAVES, nt < 4 ? nt : 4), AT_T, 0, a.stream>>>(a, workspace, nt);
+    launch(AN_GROUPS, workspace);
+    // few units have many pieces each: their columns to workgroups of their own
+    join<<<dim3(AN_WAVES, units < 256 && nt > 1 ? (nt < 4 ? nt : 4) : 1), AT_T, 0, a.stream>>>(a, workspace, nt);
   };
   if (a.bf16) {
     if (a.DH == 64)

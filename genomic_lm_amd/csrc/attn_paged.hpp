@@ -31,6 +31,8 @@ constexpr int AT_T = 256;                 // threads
 constexpr int AT_TILE = 64;               // cached tokens per tile
 constexpr int AT_NARROW = 16;             // columns up to which a request is narrow
 
+// Request r: first query token, queries, cached tokens (each cut to what
+// exists).
 __device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, int& queries, int& len) {
   const int c0 = a.cu[r], c1 = min(a.cu[r + 1], a.T);
   tok0 = max(c0, 0);
@@ -84,12 +86,59 @@ __device__ __forceinline__ uint32_t keep_places(uint32_t w, int at, int n) {
   return k >= 4 ? w : k <= 0 ? 0u : w & ((1u << (8 * k)) - 1);
 }
 
-// The page of a token.
-__device__ __forceinline__ int table_page(const AttnArgs& a, const int32_t* table, int tok, int len) {
-  const int j = tok >> a.page_lg;
-  // -1 past the end or where the table holds no page
-  const int p = tok < len && j < a.max_pages ? table[j] : -1;
-  return p >= 0 && p < a.num_pages ? p : -1;
+// A load whose address is the same in every lane, through the scalar cache:
+// its wait does not queue behind the cache's tiles, which vector loads return
+// in order.
+template <typename T>
+__device__ __forceinline__ T scalar(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)(reinterpret_cast<uintptr_t>(p));
+}
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// One value per 16-token run of a tile, the same in every lane; BIG (pages of
+// at least a tile): one value for all runs.
+template <typename T, bool BIG>
+struct PerRun {
+  T x[BIG ? 1 : 4];
+  // of run k, k per lane
+  __device__ __forceinline__ T at(int k) const {
+    if constexpr (BIG) {
+      return x[0];
+    } else {
+      // selects of values: an index per lane would move the array to memory
+      const T x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+      const T lo = (k & 1) ? x1 : x0, hi = (k & 1) ? x3 : x2;
+      return (k & 2) ? hi : lo;
+    }
+  }
+};
+
+// Pages of a tile's runs: -1 past the request's end, or where the table holds
+// no page.
+template <bool BIG>
+__device__ __forceinline__ PerRun<int, BIG> tile_pages(const AttnArgs& a, const int32_t* table, int tile, int len) {
+  PerRun<int, BIG> r;
+#pragma unroll
+  for (int k = 0; k < (BIG ? 1 : 4); ++k) {
+    const int tok = tile * AT_TILE + 16 * k, j = tok >> a.page_lg;
+    r.x[k] = -1;
+    if (tok < len && j < a.max_pages) {
+      const int p = scalar(table + j);
+      if (p >= 0 && p < a.num_pages) r.x[k] = p;
+    }
+  }
+  return r;
+}
+
+template <bool BIG>
+__device__ __forceinline__ PerRun<float, BIG> run_scales(const AttnArgs& a, const float* scales,
+                                                         const PerRun<int, BIG>& pages, int head) {
+  PerRun<float, BIG> r;
+#pragma unroll
+  for (int k = 0; k < (BIG ? 1 : 4); ++k)
+    r.x[k] = scalar(scales + static_cast<int64_t>(max(pages.x[k], 0)) * a.Hkv + head);
+  return r;
 }
 
 // Requests of up to `limit` columns (attn_narrow.hip) and of more than `limit`

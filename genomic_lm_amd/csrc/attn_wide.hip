@@ -229,7 +229,7 @@ __device__ __forceinline__ AttnSpace attn_space(void* p) {
 // lanes on consecutive rows read different banks.
 constexpr float AT_SLACK = 8.0f;      // how far (log2) scores may pass the reference before O is rescaled
 
-template <typename IO, int DH>
+template <typename IO, int DH, bool BIG>
 __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, void* space) {
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
   constexpr int KS = DH / 16;            // MFMA steps over the head dimension
@@ -290,7 +290,6 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   const int64_t page_bytes = (static_cast<int64_t>(a.Hkv) << lg) * DH;
   const int64_t head_off = (static_cast<int64_t>(head) << lg) * DH;
   const int32_t* table = a.block_table + w.r * a.table_stride;
-  auto page_of = [&](int tok) { return table_page(a, table, tok, w.len); };
 
   // ---- staging: step u of a thread is row kr + u KROWS of K (16 dimensions from
   // 16 kc) and row vd + 64 u of V^T (16 tokens from 16 vc)
@@ -299,25 +298,28 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   const int kr = tid / KP, kc = tid % KP;
   const int vd = tid >> 2, vc = tid & 3;
   u32x4 rk[STEPS], rv[STEPS];
-  int pk[STEPS], pv;
-  auto pages_of = [&](int tile) {
-#pragma unroll
-    for (int u = 0; u < STEPS; ++u) pk[u] = page_of(tile * AT_TILE + ((kr + u * KROWS) & ~15));
-    pv = page_of(tile * AT_TILE + 16 * vc);
-  };
-  auto fetch = [&](int tile) {
+  auto block = [&](const uint8_t* cache, int page) { return cache + max(page, 0) * page_bytes + head_off; };
+  auto fetch = [&](int tile, const PerRun<int, BIG>& pages) {
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-      const int tok = tile * AT_TILE + kr + u * KROWS;
-      rk[u] = *reinterpret_cast<const u32x4*>(a.k_cache + max(pk[u], 0) * page_bytes + head_off +
-                                              (tok & pmask) * DH + 16 * kc);
-      rv[u] = *reinterpret_cast<const u32x4*>(a.v_cache + max(pv, 0) * page_bytes + head_off +
-                                              (static_cast<int64_t>(vd + 64 * u) << lg) +
-                                              ((tile * AT_TILE + 16 * vc) & pmask));
+      const int row = kr + u * KROWS;
+      const uint8_t* kb = block(a.k_cache, pages.at(row >> 4));
+      const uint8_t* vb = block(a.v_cache, pages.at(vc));
+      if constexpr (BIG) {
+        kb += ((tile * AT_TILE) & pmask) * DH;
+        vb += (tile * AT_TILE) & pmask;
+        rk[u] = *reinterpret_cast<const u32x4*>(kb + (row * DH + 16 * kc));
+        rv[u] = *reinterpret_cast<const u32x4*>(vb + (((vd + 64 * u) << lg) + 16 * vc));
+      } else {
+        rk[u] = *reinterpret_cast<const u32x4*>(kb + (((tile * AT_TILE + row) & pmask) * DH + 16 * kc));
+        rv[u] = *reinterpret_cast<const u32x4*>(vb + (((vd + 64 * u) << lg) + ((tile * AT_TILE + 16 * vc) & pmask)));
+      }
     }
-    // places of this thread's V run that hold tokens: the rest must not reach
-    // the product (0 * NaN)
-    const int n = pv >= 0 ? w.len - (tile * AT_TILE + 16 * vc) : 0;
+  };
+  // places of this thread's V run that hold tokens: the rest must not reach
+  // the product (0 * NaN)
+  auto cut = [&](int tile, const PerRun<int, BIG>& pages) {
+    const int n = pages.at(vc) >= 0 ? w.len - (tile * AT_TILE + 16 * vc) : 0;
     if (n < 16) {
 #pragma unroll
       for (int u = 0; u < STEPS; ++u)
@@ -347,35 +349,41 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
     for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
   float m = AT_NEG, l = 0.0f;
 
+  PerRun<int, BIG> pg{}, pg_next{}, pg_later{};
+  PerRun<float, BIG> ks{}, vs{};
   if (t_begin < t_end) {
-    pages_of(t_begin);
-    fetch(t_begin);
+    pg = tile_pages<BIG>(a, table, t_begin, w.len);
+    fetch(t_begin, pg);
+    cut(t_begin, pg);
     stage(0);
-    if (t_begin + 1 < t_end) pages_of(t_begin + 1);
+    ks = run_scales(a, a.k_scale, pg, head);
+    vs = run_scales(a, a.v_scale, pg, head);
+    if (t_begin + 1 < t_end) pg_next = tile_pages<BIG>(a, table, t_begin + 1, w.len);
   }
   __syncthreads();
   for (int tile = t_begin; tile < t_end; ++tile) {
     const int buf = (tile - t_begin) & 1;
     const bool more = tile + 1 < t_end;
+    // scales and places of this lane's two runs
+    float c[2], vl[2], iv[2];
+    int places[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int run = tile * AT_TILE + 32 * h + 16 * hf;
+      const int p = pg.at(2 * h + hf);
+      const float v = vs.at(2 * h + hf);
+      places[h] = p >= 0 ? min(w.len - run, 16) : 0;
+      c[h] = ks.at(2 * h + hf) * scale2;
+      vl[h] = p >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
+      iv[h] = p >= 0 ? 1.0f / v : 0.0f;
+    }
     if (more) {
-      fetch(tile + 1);
-      if (tile + 2 < t_end) pages_of(tile + 2);
+      fetch(tile + 1, pg_next);
+      ks = run_scales(a, a.k_scale, pg_next, head);
+      vs = run_scales(a, a.v_scale, pg_next, head);
+      if (tile + 2 < t_end) pg_later = tile_pages<BIG>(a, table, tile + 2, w.len);
     }
     if (tile < t_wave) {
-      // scales and places of this lane's two runs
-      float c[2], vl[2], iv[2];
-      int places[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int run = tile * AT_TILE + 32 * h + 16 * hf;
-        const int p = page_of(run);
-        const int64_t si = static_cast<int64_t>(max(p, 0)) * a.Hkv + head;
-        places[h] = p >= 0 ? min(w.len - run, 16) : 0;
-        c[h] = a.k_scale[si] * scale2;
-        const float vs = a.v_scale[si];
-        vl[h] = p >= 0 ? __builtin_amdgcn_logf(vs) : AT_NEG;
-        iv[h] = p >= 0 ? 1.0f / vs : 0.0f;
-      }
       f32x16 s[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -444,7 +452,12 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
         l = fmaf(sum, iv[h], l);
       }
     }
-    if (more) stage(buf ^ 1);
+    if (more) {
+      cut(tile + 1, pg_next);
+      stage(buf ^ 1);
+    }
+    pg = pg_next;
+    pg_next = pg_later;
     __syncthreads();
   }
 
@@ -582,16 +595,22 @@ hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* workspace) {
   const unsigned grid = static_cast<unsigned>(attn_wide_grid(a.R, a.T, a.max_q, a.Hq, a.Hkv));
   const bool split = may_split(a.max_pages, a.page_lg);
   void* space = split ? workspace : nullptr;
-  auto go = [&](auto kernel, auto join) {
-    kernel<<<grid, AT_T, 0, a.stream>>>(a, limit, space);
+  const bool big = (1 << a.page_lg) >= AT_TILE;
+  auto go = [&](auto big_pages, auto small_pages, auto join) {
+    if (big) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space);
+    else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space);
     if (split) join<<<AT_JOIN, AT_T, 0, a.stream>>>(a, workspace);
   };
   if (a.bf16) {
-    if (a.DH == 64) go(attn_wide_kernel<bf16_t, 64>, attn_wide_join_kernel<bf16_t, 64>);
-    else go(attn_wide_kernel<bf16_t, 128>, attn_wide_join_kernel<bf16_t, 128>);
+    if (a.DH == 64)
+      go(attn_wide_kernel<bf16_t, 64, true>, attn_wide_kernel<bf16_t, 64, false>, attn_wide_join_kernel<bf16_t, 64>);
+    else
+      go(attn_wide_kernel<bf16_t, 128, true>, attn_wide_kernel<bf16_t, 128, false>, attn_wide_join_kernel<bf16_t, 128>);
   } else {
-    if (a.DH == 64) go(attn_wide_kernel<float, 64>, attn_wide_join_kernel<float, 64>);
-    else go(attn_wide_kernel<float, 128>, attn_wide_join_kernel<float, 128>);
+    if (a.DH == 64)
+      go(attn_wide_kernel<float, 64, true>, attn_wide_kernel<float, 64, false>, attn_wide_join_kernel<float, 64>);
+    else
+      go(attn_wide_kernel<float, 128, true>, attn_wide_kernel<float, 128, false>, attn_wide_join_kernel<float, 128>);
   }
   return hipGetLastError();
 }
