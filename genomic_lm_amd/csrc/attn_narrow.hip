@@ -236,14 +236,24 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       for (int d = 0; d < DT; ++d)
         vr[d] = *reinterpret_cast<const u32x4*>(b + off + (d << (lg + 4)));
     };
+    // the queries of the next unit, on their way while this one's last tiles are
+    // computed, and their operands once they are needed
+    Vec8<IO> qr[KS];
     auto load_q = [&](const Place& p) {
-      const int cols = p.queries * group;
       const IO* qp = static_cast<const IO*>(a.q) + (p.tok0 + i / group) * a.q_tok +
-                     (static_cast<int64_t>(p.head) * group + i % group) * a.q_head;
+                     (static_cast<int64_t>(p.head) * group + i % group) * a.q_head + 16 * g;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        float x[8] = {};
-        if (i < cols) load8(qp + 64 * (s >> 1) + 16 * g + 8 * (s & 1), 8, x);
+        qr[s] = Vec8<IO>{};
+        if (i < p.queries * group) qr[s].load(qp + 64 * (s >> 1) + 8 * (s & 1));
+      }
+    };
+    auto set_q = [&]() {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = qr[s].get(e);
         parts<NS>(x, qf[s]);
       }
     };
@@ -264,9 +274,11 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
     load_k(cur, pg);
     load_v(cur, pg);
     PerRun<float, BIG> ks = run_scales(a, a.k_scale, pg, cur.head), vs = run_scales(a, a.v_scale, pg, cur.head);
+    set_q();
     if (left > 1) {
       advance(a, limit, next);
       pg_next = pages_of(next);
+      if (next.tile == 0) load_q(next);
     }
     clear();
     for (;;) {
@@ -275,6 +287,12 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       const float c = ks.at(g) * scale2;
       const int page = pg.at(g);
       const float v_scale = page >= 0 ? vs.at(g) : 0.0f;
+      const bool ends = cur.tile + 1 == cur.tiles;
+      if (left > 2) {
+        later = next;
+        advance(a, limit, later);
+        pg_later = pages_of(later);
+      }
       f32x4 s[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -290,6 +308,8 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       const int run0 = cur.tile * AT_TILE + 16 * g;
       const int places = page >= 0 ? min(max(cur.len - run0, 0), 16) : 0;
       if (more) {
+        if (ends) set_q();
+        if (left > 2 && later.tile == 0) load_q(later);
         load_k(next, pg_next);
         ks = run_scales(a, a.k_scale, pg_next, next.head);
         vs = run_scales(a, a.v_scale, pg_next, next.head);
@@ -352,16 +372,8 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
           for (int n = NS - 1; n >= 0; --n) o[d] = mfma16(vf, pf[h][n], o[d]);
         }
       }
-      if (more) {
-        load_v(next, pg_next);
-        if (left > 2) {
-          later = next;
-          advance(a, limit, later);
-          pg_later = pages_of(later);
-        }
-      }
+      if (more) load_v(next, pg_next);
 
-      const bool ends = cur.tile + 1 == cur.tiles;
       if (ends || !more) {
         // leave the unit: its columns are on lanes i of every g
         l += xor16(l, lane);
@@ -395,7 +407,6 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
         if (!more) break;
         clear();
         from = 0;
-        load_q(next);
       }
       cur = next;
       next = later;
