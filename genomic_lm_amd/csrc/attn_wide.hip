@@ -179,16 +179,19 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     w.split = sh.found[3];
   }
   // the same in every lane from here on
-  w.r = __builtin_amdgcn_readfirstlane(w.r);
-  at = __builtin_amdgcn_readfirstlane(at);
+  w.r = uni(w.r);
+  at = uni(at);
+  w.tiles = uni(tiles);
   request_of(a, w.r, w.tok0, w.queries, w.len);
-  w.ahead = w.len - (min(a.cu[w.r + 1], a.T) - w.tok0);
-  w.tiles = __builtin_amdgcn_readfirstlane(tiles);
-  w.pieces = pieces_of(w.len);
-  w.unit = at / w.pieces;
-  w.piece = at % w.pieces;
-  w.slot = __builtin_amdgcn_readfirstlane(w.slot) + w.unit * w.pieces;
-  w.split = __builtin_amdgcn_readfirstlane(w.split) + w.unit;
+  w.tok0 = uni(w.tok0);
+  w.queries = uni(w.queries);
+  w.len = uni(w.len);
+  w.ahead = w.len - (min(scalar(a.cu + w.r + 1), a.T) - w.tok0);
+  w.pieces = uni(pieces_of(w.len));
+  w.unit = uni(at / w.pieces);
+  w.piece = at - w.unit * w.pieces;
+  w.slot = uni(w.slot) + w.unit * w.pieces;
+  w.split = uni(w.split) + w.unit;
   return true;
 }
 
@@ -240,7 +243,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   __shared__ __align__(16) u32x4 s_k[2][AT_TILE * KC];
   __shared__ __align__(16) u32x4 s_v[2][DH * 8];
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
   const int i = lane & 31, hf = lane >> 5;
   const int head = static_cast<int>(blockIdx.x % a.Hkv);
   const int item = static_cast<int>(blockIdx.x / a.Hkv);
@@ -262,12 +265,12 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   const bool live = col < cols;
   const int qi = live ? col / group : 0, qh = live ? col % group : 0;
   const int pos = live ? w.ahead + qi : -1;
-  const int first_pos = w.ahead + wc / group;                // of the wave's first column
+  const int first_pos = uni(w.ahead + wc / group);                // of the wave's first column
   const int wave_seen = wc < cols ? max(w.ahead + (min(wc + 32, cols) - 1) / group + 1, 0) : 0;
   const int seen = max(w.ahead + (min(c0 + AT_WNT, cols) - 1) / group + 1, 0);
   const int t_begin = w.piece * w.tiles;
-  const int t_end = min((seen + AT_TILE - 1) / AT_TILE, t_begin + w.tiles);
-  const int t_wave = min((wave_seen + AT_TILE - 1) / AT_TILE, t_end);
+  const int t_end = uni(min((seen + AT_TILE - 1) / AT_TILE, t_begin + w.tiles));
+  const int t_wave = uni(min((wave_seen + AT_TILE - 1) / AT_TILE, t_end));
 
   // queries, with the sign of the scale so that scores only grow with them
   bf16x8 qf[KS][NS];
@@ -373,9 +376,10 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
       const int p = pg.at(2 * h + hf);
       const float v = vs.at(2 * h + hf);
       places[h] = p >= 0 ? min(w.len - run, 16) : 0;
-      c[h] = ks.at(2 * h + hf) * scale2;
+      // above 0 (and no NaN where there is no page): a masked score stays -inf
+      c[h] = fmaxf(ks.at(2 * h + hf) * scale2, 0x1p-126f);
       vl[h] = p >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
-      iv[h] = p >= 0 ? 1.0f / v : 0.0f;
+      iv[h] = p >= 0 ? __builtin_amdgcn_rcpf(v) : 0.0f;
     }
     if (more) {
       fetch(tile + 1, pg_next);
@@ -386,17 +390,18 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
     if (tile < t_wave) {
       f32x16 s[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[h][r] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           const int row = 32 * h + i;
           const bf16x8 kf = __builtin_bit_cast(bf16x8, s_k[buf][row * KC + ((2 * k + hf) ^ (row & (KC - 1)))]);
 #pragma unroll
           for (int n = NS - 1; n >= 0; --n) s[h] = mfma(kf, qf[k][n], s[h]);
         }
-      }
       const bool masked = __any(places[0] < 16 || places[1] < 16) ||
                           tile * AT_TILE + AT_TILE - 1 > first_pos;
       float top = AT_NEG;
@@ -411,8 +416,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
         float t = s[h][0];
 #pragma unroll
         for (int r = 1; r < 16; ++r) t = fmaxf(t, s[h][r]);
-        // a masked score times a scale of 0, or times what stands for no page, would be NaN
-        top = fmaxf(top, t == AT_NEG ? AT_NEG : t * c[h]);
+        top = fmaxf(top, t * c[h]);
       }
       top = fmaxf(top, xor32(top, hf));
       if (__any(top > m + AT_SLACK || (m == AT_NEG && top > m))) {
@@ -435,8 +439,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
           float p[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = s[h][8 * q + e];
-            p[e] = __builtin_amdgcn_exp2f(masked && x == AT_NEG ? AT_NEG : fmaf(x, c[h], off));
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[h][8 * q + e], c[h], off));
             sum += p[e];
           }
           bf16x8 pf[NS];
