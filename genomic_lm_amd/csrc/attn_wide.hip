@@ -6,17 +6,19 @@
 
 namespace hyena {
 
-// A unit is AT_WNT columns of one request on one K/V head; its tokens are cut
-// into pieces of `tiles` 64-token tiles, the same for all requests and chosen
-// so that about AT_WTARGET pieces exist: chunks with few columns over long
-// contexts then still fill the chip.  A unit of several pieces leaves partial
-// results in the workspace, one slot per piece and head, which
-// attn_wide_join_kernel adds up; a unit of one piece writes its rows directly.
-constexpr int AT_WNT = 128;               // columns per unit
-constexpr int AT_WTARGET = 512;           // pieces aimed at: two workgroups per CU
+// A unit is NT columns of one request on one K/V head; its tokens are cut into
+// pieces of `tiles` 64-token tiles, the same for all requests and chosen so
+// that about wide_target(W) pieces exist, what the chip holds at once: chunks
+// with few columns over long contexts then still fill it.  A unit of several
+// pieces leaves partial results in the workspace, one slot per piece and head,
+// which attn_wide_join_kernel adds up; a unit of one piece writes its rows
+// directly.
 constexpr int AT_MIN_PIECE = 4;           // tiles
-constexpr int AT_WSLOTS = 2 * AT_WTARGET; // a unit worth x > 1 pieces is cut into fewer than 2 x
 constexpr int AT_JOIN = 512;              // workgroups of the joining launch
+// eight waves per CU: two workgroups of four, or one of eight
+constexpr int wide_target(int waves) { return 2048 / waves; }
+// a unit worth x > 1 pieces is cut into fewer than 2 x
+constexpr int wide_slots(int waves) { return 2 * wide_target(waves); }
 
 struct AttnWork {
   int tok0, queries, len;    // the request: first query token, queries (up to max_q), cached tokens
@@ -29,8 +31,8 @@ struct AttnWork {
 };
 
 struct AttnShared {
-  unsigned long long part[AT_T / 64];
-  int items[AT_T / 64], slots[AT_T / 64], splits[AT_T / 64];
+  unsigned long long part[8];        // per wave
+  int items[8], slots[8], splits[8];
   int found[5];              // request, item within it, first slot, first split unit, set
 };
 
@@ -54,17 +56,18 @@ __device__ __forceinline__ void wave_scan3(int& x, int& y, int& z) {
 // all requests itself (two sums and a scan over them): a launch of its own for
 // that costs more at every R up to the limit.  Up to 64 requests each wave
 // does it alone, without a barrier; one request needs no scan.
+template <int NT, int W>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, AttnShared& sh,
                                           AttnWork& w, int& splits) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = a.Hq / a.Hkv;
   auto units_of = [&](int queries) {
     const int64_t cols = static_cast<int64_t>(queries) * group;
-    return cols > lo ? static_cast<int>((cols + AT_WNT - 1) / AT_WNT) : 0;
+    return cols > lo ? static_cast<int>((cols + NT - 1) / NT) : 0;
   };
   auto tiles_of = [](int len) { return (len + AT_TILE - 1) / AT_TILE; };
   auto piece_tiles = [&](unsigned long long work) {
-    const unsigned long long even = (work * a.Hkv + AT_WTARGET - 1) / AT_WTARGET;
+    const unsigned long long even = (work * a.Hkv + wide_target(W) - 1) / wide_target(W);
     return static_cast<int>(even > AT_MIN_PIECE ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_MIN_PIECE);
   };
   int tiles = 0, at = 0;
@@ -102,7 +105,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     w.slot = __shfl(slots_in - slots, w.r);
     w.split = __shfl(split_in - split, w.r);
   } else {
-    const int run = (a.R + AT_T - 1) / AT_T;
+    const int run = (a.R + 64 * W - 1) / (64 * W);
     const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
     unsigned long long work = 0;
     for (int r = r0; r < r1; ++r) {
@@ -117,7 +120,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     __syncthreads();
     work = 0;
 #pragma unroll
-    for (int i = 0; i < AT_T / 64; ++i) work += sh.part[i];
+    for (int i = 0; i < W; ++i) work += sh.part[i];
     tiles = piece_tiles(work);
     int items = 0, slots = 0, split = 0;
     for (int r = r0; r < r1; ++r) {
@@ -143,7 +146,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     __syncthreads();
     splits = 0;
 #pragma unroll
-    for (int i = 0; i < AT_T / 64; ++i) {
+    for (int i = 0; i < W; ++i) {
       if (i < wave) {
         before += sh.items[i];
         sbefore += sh.slots[i];
@@ -196,8 +199,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
 }
 
 // ---------------------------------------------------------------- workspace
-// the count of units of several pieces, a header for each, then m, l (AT_WNT
-// each) and O (AT_WNT x DH) per slot
+// the count of units of several pieces, a header for each, then m, l (NT each)
+// and O (NT x DH) per slot
 struct AttnUnit {
   int pieces, slot;          // and its first slot; piece p lies p * heads slots on
   int tok0, col0, cols;      // the request's first query token; the unit's first column, its columns
@@ -209,12 +212,12 @@ struct AttnSpace {
   float* ml;
   float* o;
 };
-__device__ __forceinline__ AttnSpace attn_space(void* p) {
+__device__ __forceinline__ AttnSpace attn_space(void* p, int nt, int waves) {
   AttnSpace s;
   s.used = static_cast<int*>(p);
   s.head = reinterpret_cast<AttnUnit*>(static_cast<char*>(p) + 16);
-  s.ml = reinterpret_cast<float*>(s.head + AT_WSLOTS / 2);      // a split unit has at least two slots
-  s.o = s.ml + static_cast<size_t>(AT_WSLOTS) * 2 * AT_WNT;
+  s.ml = reinterpret_cast<float*>(s.head + wide_slots(waves) / 2);      // a split unit has at least two slots
+  s.o = s.ml + static_cast<size_t>(wide_slots(waves)) * 2 * nt;
   return s;
 }
 
@@ -232,13 +235,15 @@ __device__ __forceinline__ AttnSpace attn_space(void* p) {
 // lanes on consecutive rows read different banks.
 constexpr float AT_SLACK = 8.0f;      // how far (log2) scores may pass the reference before O is rescaled
 
-template <typename IO, int DH, bool BIG>
-__global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, void* space) {
+template <typename IO, int DH, bool BIG, int CW, int W>
+__global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo, void* space) {
+  constexpr int THREADS = 64 * W;
+  constexpr int WNT = 32 * CW * W;       // columns per unit
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
   constexpr int KS = DH / 16;            // MFMA steps over the head dimension
   constexpr int DT = DH / 32;            // 32-row tiles of O^T
   constexpr int KC = DH / 8;             // 16-byte pieces of a K row in LDS
-  constexpr int STEPS = DH / 64;         // 16-byte loads per thread of K, and of V
+  constexpr int STEPS = 4 * DH / THREADS; // 16-byte loads per thread of K, and of V
   __shared__ AttnShared sh;
   __shared__ __align__(16) u32x4 s_k[2][AT_TILE * KC];
   __shared__ __align__(16) u32x4 s_v[2][DH * 8];
@@ -248,43 +253,50 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   const int head = static_cast<int>(blockIdx.x % a.Hkv);
   const int item = static_cast<int>(blockIdx.x / a.Hkv);
   const int group = a.Hq / a.Hkv;
-  const AttnSpace ws = attn_space(space);
+  const AttnSpace ws = attn_space(space, WNT, W);
   AttnWork w;
   int splits;
-  const bool have = find_work(a, lo, item, sh, w, splits);
+  const bool have = find_work<WNT, W>(a, lo, item, sh, w, splits);
   if (blockIdx.x == 0 && tid == 0 && space) *ws.used = splits * a.Hkv;
   if (!have) return;
 
   const int cols = w.queries * group;
   // the units that see most tokens first
-  const int units = (cols + AT_WNT - 1) / AT_WNT;
+  const int units = (cols + WNT - 1) / WNT;
   const int unit = units - 1 - w.unit;
-  const int c0 = unit * AT_WNT;
-  const int wc = c0 + wave * 32;                             // the wave's first column
-  const int col = wc + i;
-  const bool live = col < cols;
-  const int qi = live ? col / group : 0, qh = live ? col % group : 0;
-  const int pos = live ? w.ahead + qi : -1;
-  const int first_pos = uni(w.ahead + wc / group);                // of the wave's first column
-  const int wave_seen = wc < cols ? max(w.ahead + (min(wc + 32, cols) - 1) / group + 1, 0) : 0;
-  const int seen = max(w.ahead + (min(c0 + AT_WNT, cols) - 1) / group + 1, 0);
+  const int c0 = unit * WNT;
+  const int wc = c0 + wave * 32 * CW;                        // the wave's first column
+  bool live[CW];
+  int qi[CW], qh[CW], pos[CW];                               // query, head, last token seen
+#pragma unroll
+  for (int b = 0; b < CW; ++b) {
+    const int col = wc + 32 * b + i;
+    live[b] = col < cols;
+    qi[b] = live[b] ? col / group : 0;
+    qh[b] = live[b] ? col % group : 0;
+    pos[b] = live[b] ? w.ahead + qi[b] : -1;
+  }
+  const int first_pos = uni(w.ahead + wc / group);           // of the wave's first column
+  const int wave_seen = wc < cols ? max(w.ahead + (min(wc + 32 * CW, cols) - 1) / group + 1, 0) : 0;
+  const int seen = max(w.ahead + (min(c0 + WNT, cols) - 1) / group + 1, 0);
   const int t_begin = w.piece * w.tiles;
   const int t_end = uni(min((seen + AT_TILE - 1) / AT_TILE, t_begin + w.tiles));
   const int t_wave = uni(min((wave_seen + AT_TILE - 1) / AT_TILE, t_end));
 
   // queries, with the sign of the scale so that scores only grow with them
-  bf16x8 qf[KS][NS];
-  {
-    const IO* qp = static_cast<const IO*>(a.q) + (w.tok0 + qi) * a.q_tok +
-                   (static_cast<int64_t>(head) * group + qh) * a.q_head;
+  bf16x8 qf[CW][KS][NS];
+#pragma unroll
+  for (int b = 0; b < CW; ++b) {
+    const IO* qp = static_cast<const IO*>(a.q) + (w.tok0 + qi[b]) * a.q_tok +
+                   (static_cast<int64_t>(head) * group + qh[b]) * a.q_head;
     const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       float x[8] = {};
-      if (live) load8(qp + 16 * s + 8 * hf, 8, x);
+      if (live[b]) load8(qp + 16 * s + 8 * hf, 8, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= sign;
-      parts<NS>(x, qf[s]);
+      parts<NS>(x, qf[b][s]);
     }
   }
   const float scale2 = fabsf(a.scale) * AT_LOG2E;
@@ -297,40 +309,63 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
   // ---- staging: step u of a thread is row kr + u KROWS of K (16 dimensions from
   // 16 kc) and row vd + 64 u of V^T (16 tokens from 16 vc)
   constexpr int KP = DH / 16;            // 16-code pieces of a K row
-  constexpr int KROWS = AT_T / KP;
+  constexpr int KROWS = THREADS / KP;
   const int kr = tid / KP, kc = tid % KP;
+  constexpr int VROWS = THREADS / 4;
   const int vd = tid >> 2, vc = tid & 3;
   u32x4 rk[STEPS], rv[STEPS];
+  // Pages and scales of AHEAD tiles at a time, a run (BIG: a tile) per lane; a
+  // tile's are then read from its lanes, without a load to wait for.
+  constexpr int RUNS = BIG ? 1 : 4;
+  constexpr int AHEAD = 64 / RUNS;
+  struct TileInfo {
+    PerRun<int, BIG> page;
+    PerRun<float, BIG> ks, vs;
+  };
+  int ahead_from = 0, ahead_page = -1;
+  float ahead_ks = 0.0f, ahead_vs = 0.0f;
+  auto look_ahead = [&](int from) {
+    ahead_from = from;
+    const int tok = (from + lane / RUNS) * AT_TILE + (lane % RUNS) * 16, j = tok >> lg;
+    const int p = tok < w.len && j < a.max_pages ? table[j] : -1;
+    ahead_page = p >= 0 && p < a.num_pages ? p : -1;
+    const int64_t si = static_cast<int64_t>(max(ahead_page, 0)) * a.Hkv + head;
+    ahead_ks = a.k_scale[si];
+    ahead_vs = a.v_scale[si];
+  };
+  auto info_of = [&](int tile) {
+    if (tile >= ahead_from + AHEAD) look_ahead(tile);
+    TileInfo t;
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const int from = (tile - ahead_from) * RUNS + k;
+      t.page.x[k] = __builtin_amdgcn_readlane(ahead_page, from);
+      t.ks.x[k] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ahead_ks), from));
+      t.vs.x[k] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ahead_vs), from));
+    }
+    return t;
+  };
   auto block = [&](const uint8_t* cache, int page) { return cache + max(page, 0) * page_bytes + head_off; };
-  auto fetch = [&](int tile, const PerRun<int, BIG>& pages) {
+  auto fetch_k = [&](int tile, const PerRun<int, BIG>& pages) {
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       const int row = kr + u * KROWS;
-      const uint8_t* kb = block(a.k_cache, pages.at(row >> 4));
-      const uint8_t* vb = block(a.v_cache, pages.at(vc));
-      if constexpr (BIG) {
-        kb += ((tile * AT_TILE) & pmask) * DH;
-        vb += (tile * AT_TILE) & pmask;
-        rk[u] = *reinterpret_cast<const u32x4*>(kb + (row * DH + 16 * kc));
-        rv[u] = *reinterpret_cast<const u32x4*>(vb + (((vd + 64 * u) << lg) + 16 * vc));
-      } else {
-        rk[u] = *reinterpret_cast<const u32x4*>(kb + (((tile * AT_TILE + row) & pmask) * DH + 16 * kc));
-        rv[u] = *reinterpret_cast<const u32x4*>(vb + (((vd + 64 * u) << lg) + ((tile * AT_TILE + 16 * vc) & pmask)));
-      }
+      const uint8_t* b = block(a.k_cache, pages.at(row >> 4));
+      if constexpr (BIG)
+        rk[u] = *reinterpret_cast<const u32x4*>(b + ((tile * AT_TILE) & pmask) * DH + (row * DH + 16 * kc));
+      else
+        rk[u] = *reinterpret_cast<const u32x4*>(b + (((tile * AT_TILE + row) & pmask) * DH + 16 * kc));
     }
   };
-  // places of this thread's V run that hold tokens: the rest must not reach
-  // the product (0 * NaN)
-  auto cut = [&](int tile, const PerRun<int, BIG>& pages) {
-    const int n = pages.at(vc) >= 0 ? w.len - (tile * AT_TILE + 16 * vc) : 0;
-    if (n < 16) {
+  auto fetch_v = [&](int tile, const PerRun<int, BIG>& pages) {
+    const uint8_t* b = block(a.v_cache, pages.at(vc));
+    if constexpr (BIG) b += (tile * AT_TILE) & pmask;
 #pragma unroll
-      for (int u = 0; u < STEPS; ++u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rv[u][e] = keep_places(rv[u][e], e, n);
-    }
+    for (int u = 0; u < STEPS; ++u)
+      rv[u] = *reinterpret_cast<const u32x4*>(
+          b + (((vd + VROWS * u) << lg) + (BIG ? 16 * vc : (tile * AT_TILE + 16 * vc) & pmask)));
   };
-  auto stage = [&](int buf) {
+  auto stage_k = [&](int buf) {
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       const int row = kr + u * KROWS;                        // token of the tile
@@ -338,164 +373,233 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
       u32x4* kd = s_k[buf] + at * KC;
       kd[(2 * kc) ^ (at & (KC - 1))] = __builtin_bit_cast(u32x4, widen(rk[u][0], rk[u][1]));
       kd[(2 * kc + 1) ^ (at & (KC - 1))] = __builtin_bit_cast(u32x4, widen(rk[u][2], rk[u][3]));
-      const int d = vd + 64 * u;
+    }
+  };
+  // places of this thread's V run that hold tokens: the rest must not reach the
+  // product (0 * NaN)
+  auto cut = [&](int tile, const PerRun<int, BIG>& pages) {
+    const int n = pages.at(vc) >= 0 ? w.len - (tile * AT_TILE + 16 * vc) : 0;
+    if (__any(n < 16)) {
+#pragma unroll
+      for (int u = 0; u < STEPS; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rv[u][e] = keep_places(rv[u][e], e, n);
+    }
+  };
+  auto stage_v = [&](int buf) {
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int d = vd + VROWS * u;
       u32x4* vdst = s_v[buf] + d * 8;
-      vdst[(2 * vc) ^ (d & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][0], rv[u][1]));
-      vdst[(2 * vc + 1) ^ (d & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][2], rv[u][3]));
+      vdst[(2 * vc) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][0], rv[u][1]));
+      vdst[(2 * vc + 1) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][2], rv[u][3]));
     }
   };
 
-  f32x16 o[DT];
+  f32x16 o[CW][DT];
+  float m[CW], l[CW];
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int b = 0; b < CW; ++b) {
+    m[b] = AT_NEG;
+    l[b] = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-  float m = AT_NEG, l = 0.0f;
-
-  PerRun<int, BIG> pg{}, pg_next{}, pg_later{};
-  PerRun<float, BIG> ks{}, vs{};
-  if (t_begin < t_end) {
-    pg = tile_pages<BIG>(a, table, t_begin, w.len);
-    fetch(t_begin, pg);
-    cut(t_begin, pg);
-    stage(0);
-    ks = run_scales(a, a.k_scale, pg, head);
-    vs = run_scales(a, a.v_scale, pg, head);
-    if (t_begin + 1 < t_end) pg_next = tile_pages<BIG>(a, table, t_begin + 1, w.len);
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[b][d][r] = 0.0f;
   }
-  __syncthreads();
-  for (int tile = t_begin; tile < t_end; ++tile) {
-    const int buf = (tile - t_begin) & 1;
-    const bool more = tile + 1 < t_end;
-    // scales and places of this lane's two runs
-    float c[2], vl[2], iv[2];
-    int places[2];
+
+  // S^T of a tile from K's buffer
+  auto scores = [&](int buf, f32x16 (&s)[CW][2]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int run = tile * AT_TILE + 32 * h + 16 * hf;
-      const int p = pg.at(2 * h + hf);
-      const float v = vs.at(2 * h + hf);
-      places[h] = p >= 0 ? min(w.len - run, 16) : 0;
-      // above 0 (and no NaN where there is no page): a masked score stays -inf
-      c[h] = fmaxf(ks.at(2 * h + hf) * scale2, 0x1p-126f);
-      vl[h] = p >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
-      iv[h] = p >= 0 ? __builtin_amdgcn_rcpf(v) : 0.0f;
-    }
-    if (more) {
-      fetch(tile + 1, pg_next);
-      ks = run_scales(a, a.k_scale, pg_next, head);
-      vs = run_scales(a, a.v_scale, pg_next, head);
-      if (tile + 2 < t_end) pg_later = tile_pages<BIG>(a, table, tile + 2, w.len);
-    }
-    if (tile < t_wave) {
-      f32x16 s[2];
+    for (int b = 0; b < CW; ++b)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[h][r] = 0.0f;
+        for (int r = 0; r < 16; ++r) s[b][h][r] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 32 * h + i;
-          const bf16x8 kf = __builtin_bit_cast(bf16x8, s_k[buf][row * KC + ((2 * k + hf) ^ (row & (KC - 1)))]);
-#pragma unroll
-          for (int n = NS - 1; n >= 0; --n) s[h] = mfma(kf, qf[k][n], s[h]);
-        }
-      const bool masked = __any(places[0] < 16 || places[1] < 16) ||
-                          tile * AT_TILE + AT_TILE - 1 > first_pos;
-      float top = AT_NEG;
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (masked) {
-          const int lim = min(places[h], pos - (tile * AT_TILE + 32 * h + 16 * hf) + 1);
+        const int row = 32 * h + i;
+        const bf16x8 kf = __builtin_bit_cast(bf16x8, s_k[buf][row * KC + ((2 * k + hf) ^ (row & (KC - 1)))]);
+#pragma unroll
+        for (int b = 0; b < CW; ++b)
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) s[b][h] = mfma(kf, qf[b][k][n], s[b][h]);
+      }
+  };
+
+  // scales of this lane's two runs of the tile in work: of the scores, log2 and
+  // reciprocal of V's
+  float c[2], vl[2], iv[2];
+  // masks of a tile's scores, the columns' maxima, and O moved to a new
+  // reference where one has risen by more than AT_SLACK
+  auto judge = [&](int tile, f32x16 (&s)[CW][2], const TileInfo& t) {
+    int places[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int p = t.page.at(2 * h + hf);
+      const float v = t.vs.at(2 * h + hf);
+      places[h] = p >= 0 ? min(w.len - (tile * AT_TILE + 32 * h + 16 * hf), 16) : 0;
+      // above 0 (and no NaN where there is no page): a masked score stays -inf
+      c[h] = fmaxf(t.ks.at(2 * h + hf) * scale2, 0x1p-126f);
+      vl[h] = p >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
+      iv[h] = p >= 0 ? __builtin_amdgcn_rcpf(v) : 0.0f;
+    }
+    if (__any(places[0] < 16 || places[1] < 16) || tile * AT_TILE + AT_TILE - 1 > first_pos) {
+#pragma unroll
+      for (int b = 0; b < CW; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int lim = min(places[h], pos[b] - (tile * AT_TILE + 32 * h + 16 * hf) + 1);
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (r >= lim) s[h][r] = AT_NEG;
+            if (r >= lim) s[b][h][r] = AT_NEG;
         }
-        float t = s[h][0];
+    }
+    float top[CW];
+    bool risen = false;
 #pragma unroll
-        for (int r = 1; r < 16; ++r) t = fmaxf(t, s[h][r]);
-        top = fmaxf(top, t * c[h]);
+    for (int b = 0; b < CW; ++b) {
+      top[b] = AT_NEG;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = s[b][h][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) x = fmaxf(x, s[b][h][r]);
+        top[b] = fmaxf(top[b], x * c[h]);
       }
-      top = fmaxf(top, xor32(top, hf));
-      if (__any(top > m + AT_SLACK || (m == AT_NEG && top > m))) {
-        const float m_new = fmaxf(m, top);
-        const float f = m_new == AT_NEG ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
-        l *= f;
+      top[b] = fmaxf(top[b], xor32(top[b], hf));
+      risen |= top[b] > m[b] + AT_SLACK;
+    }
+    if (__any(risen)) {
+#pragma unroll
+      for (int b = 0; b < CW; ++b) {
+        const float m_new = fmaxf(m[b], top[b]);
+        const float f = m_new == AT_NEG ? 1.0f : __builtin_amdgcn_exp2f(m[b] - m_new);
+        l[b] *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[d][r] *= f;
-        m = m_new;
+          for (int r = 0; r < 16; ++r) o[b][d][r] *= f;
+        m[b] = m_new;
       }
-      const float base = m == AT_NEG ? 0.0f : m;
+    }
+  };
+
+  // P = 2^(c s + log2 v_scale - m), its sums, and O^T += V^T P^T
+  auto weigh = [&](int buf, const f32x16 (&s)[CW][2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float off = vl[h] - base;
-        float sum = 0.0f;
+    for (int h = 0; h < 2; ++h) {
+      float off[CW], sum[CW];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+      for (int b = 0; b < CW; ++b) {
+        off[b] = vl[h] - (m[b] == AT_NEG ? 0.0f : m[b]);
+        sum[b] = 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        bf16x8 pf[CW][NS];
+#pragma unroll
+        for (int b = 0; b < CW; ++b) {
           float p[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[h][8 * q + e], c[h], off));
-            sum += p[e];
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[b][h][8 * q + e], c[h], off[b]));
+            sum[b] += p[e];
           }
-          bf16x8 pf[NS];
-          parts<NS>(p, pf);
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const int row = 32 * d + i;
-            const bf16x8 vf = __builtin_bit_cast(bf16x8, s_v[buf][row * 8 + ((4 * h + 2 * hf + q) ^ (row & 7))]);
-#pragma unroll
-            for (int n = NS - 1; n >= 0; --n) o[d] = mfma(vf, pf[n], o[d]);
-          }
+          parts<NS>(p, pf[b]);
         }
-        l = fmaf(sum, iv[h], l);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const int row = 32 * d + i;
+          const bf16x8 vf =
+              __builtin_bit_cast(bf16x8, s_v[buf][row * 8 + ((4 * h + 2 * hf + q) ^ ((row >> 1) & 7))]);
+#pragma unroll
+          for (int b = 0; b < CW; ++b)
+#pragma unroll
+            for (int n = NS - 1; n >= 0; --n) o[b][d] = mfma(vf, pf[b][n], o[b][d]);
+        }
       }
+#pragma unroll
+      for (int b = 0; b < CW; ++b) l[b] = fmaf(sum[b], iv[h], l[b]);
     }
-    if (more) {
-      cut(tile + 1, pg_next);
-      stage(buf ^ 1);
-    }
-    pg = pg_next;
-    pg_next = pg_later;
+  };
+
+  // Tile t + 1 is written to the other buffers beside tile t's first product, so
+  // one barrier per tile is enough, and tile t + 2 is then requested.  Past the
+  // end the last tile is requested and written again.
+  if (t_begin < t_end) {
+    const int last = t_end - 1;
+    look_ahead(t_begin);
+    TileInfo t0 = info_of(t_begin), t1 = info_of(min(t_begin + 1, last));
+    fetch_k(t_begin, t0.page);
+    fetch_v(t_begin, t0.page);
+    cut(t_begin, t0.page);
+    stage_k(0);
+    stage_v(0);
+    fetch_k(min(t_begin + 1, last), t1.page);
+    fetch_v(min(t_begin + 1, last), t1.page);
     __syncthreads();
+    for (int tile = t_begin; tile < t_end; ++tile) {
+      const int buf = (tile - t_begin) & 1, after = min(tile + 2, last);
+      const TileInfo t2 = info_of(after);
+      cut(min(tile + 1, last), t1.page);
+      if (tile < t_wave) {
+        f32x16 s[CW][2];
+        scores(buf, s);
+        stage_k(buf ^ 1);
+        stage_v(buf ^ 1);
+        fetch_k(after, t2.page);
+        fetch_v(after, t2.page);
+        judge(tile, s, t0);
+        weigh(buf, s);
+      } else {
+        stage_k(buf ^ 1);
+        stage_v(buf ^ 1);
+        fetch_k(after, t2.page);
+        fetch_v(after, t2.page);
+      }
+      t0 = t1;
+      t1 = t2;
+      __syncthreads();
+    }
   }
 
-  l += xor32(l, hf);
-  if (!live) return;
-  if (w.pieces == 1) {
-    IO* op = static_cast<IO*>(a.out) +
-             ((static_cast<int64_t>(w.tok0) + qi) * a.Hq + static_cast<int64_t>(head) * group + qh) * DH;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+  for (int b = 0; b < CW; ++b) {
+    l[b] += xor32(l[b], hf);
+    if (!live[b]) continue;
+    if (w.pieces == 1) {
+      IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(w.tok0) + qi[b]) * a.Hq +
+                                          static_cast<int64_t>(head) * group + qh[b]) * DH;
+      const float inv = l[b] == 0.0f ? 0.0f : 1.0f / l[b];
+      // rows 8 e + 4 hf .. + 3 of each 32
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        // rows 8 b + 4 hf .. + 3 of the 32
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) Io<IO>::st(op, 32 * d + 8 * b + 4 * hf + r, o[d][4 * b + r] * inv);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) Io<IO>::st(op, 32 * d + 8 * e + 4 * hf + r, o[b][d][4 * e + r] * inv);
+    } else {
+      const int64_t slot = static_cast<int64_t>(w.slot + w.piece) * a.Hkv + head;
+      const int oc = wave * 32 * CW + 32 * b + i;
+      if (hf == 0) {
+        ws.ml[slot * 2 * WNT + oc] = m[b];
+        ws.ml[slot * 2 * WNT + WNT + oc] = l[b];
       }
-  } else {
-    const int64_t slot = static_cast<int64_t>(w.slot + w.piece) * a.Hkv + head;
-    if (tid == 0 && w.piece == 0)
-      ws.head[static_cast<int64_t>(w.split) * a.Hkv + head] =
-          AttnUnit{w.pieces, static_cast<int>(slot), w.tok0, c0, min(AT_WNT, cols - c0), {0, 0, 0}};
-    const int oc = wave * 32 + i;
-    if (hf == 0) {
-      ws.ml[slot * 2 * AT_WNT + oc] = m;
-      ws.ml[slot * 2 * AT_WNT + AT_WNT + oc] = l;
+      float* op = ws.o + (slot * WNT + oc) * DH;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<f32x4*>(op + 32 * d + 8 * e + 4 * hf) =
+              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]};
     }
-    float* op = ws.o + (slot * AT_WNT + oc) * DH;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        *reinterpret_cast<f32x4*>(op + 32 * d + 8 * b + 4 * hf) =
-            f32x4{o[d][4 * b], o[d][4 * b + 1], o[d][4 * b + 2], o[d][4 * b + 3]};
   }
+  if (w.pieces > 1 && tid == 0 && w.piece == 0)
+    ws.head[static_cast<int64_t>(w.split) * a.Hkv + head] =
+        AttnUnit{w.pieces, static_cast<int>(w.slot * a.Hkv + head), w.tok0, c0, min(WNT, cols - c0), {0, 0, 0}};
 }
 
 // ---------------------------------------------------------------- joining pieces
@@ -504,14 +608,13 @@ __global__ __launch_bounds__(AT_T, 2) void attn_wide_kernel(AttnArgs a, int lo, 
 // each; with fewer columns than it has lanes for, the lanes left over take
 // every other (fourth, eighth) piece and are added through LDS.  The grid is
 // fixed and walks the units, whose number only the device knows.
-template <typename IO, int DH>
+template <typename IO, int DH, int NT, int W>
 __global__ __launch_bounds__(AT_T) void attn_wide_join_kernel(AttnArgs a, void* space) {
-  constexpr int NT = AT_WNT;
   constexpr int LPC = DH / 4;              // lanes per column
   constexpr int SETS = AT_T / LPC;         // columns the workgroup holds at once
   __shared__ float s_m[SETS], s_l[SETS];
   __shared__ __align__(16) f32x4 s_o[SETS][LPC];
-  const AttnSpace ws = attn_space(space);
+  const AttnSpace ws = attn_space(space, NT, W);
   const int64_t tasks = static_cast<int64_t>(*ws.used) * (NT / 16);
   const int group = a.Hq / a.Hkv;
   const int set = threadIdx.x / LPC, d = (threadIdx.x % LPC) * 4;
@@ -582,38 +685,49 @@ static bool may_split(int64_t max_pages, int page_lg) {
 
 size_t attn_wide_workspace(int64_t max_pages, int page_lg, int DH) {
   if (!may_split(max_pages, page_lg)) return 0;
-  return 16 + static_cast<size_t>(AT_WSLOTS) * (sizeof(AttnUnit) / 2 + 4 * (2 * AT_WNT + AT_WNT * DH));
+  // slots times columns is the same for both of a head dimension's units (below);
+  // headers are most for the narrower one
+  const int64_t columns = DH == 64 ? 1024 * 256 : 1024 * 128;
+  return 16 + wide_slots(4) * (sizeof(AttnUnit) / 2) + static_cast<size_t>(columns) * (4 * (2 + DH));
 }
 
-int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv) {
+static int64_t grid_of(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int nt, int waves) {
   // ceil per request: at most one unit more than its columns' share, and at
   // most the units of max_q queries
   const int64_t group = Hq / Hkv;
-  const int64_t share = T * group / AT_WNT + R;
-  const int64_t each = R * ((max_q * group + AT_WNT - 1) / AT_WNT);
-  return ((share < each ? share : each) + AT_WTARGET / Hkv + 1) * Hkv;
+  const int64_t share = T * group / nt + R;
+  const int64_t each = R * ((max_q * group + nt - 1) / nt);
+  return ((share < each ? share : each) + wide_target(waves) / Hkv + 1) * Hkv;
+}
+
+int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv) {
+  return 2 * grid_of(R, T, max_q, Hq, Hkv, 128, 4);     // the most there can be, in workgroups of four waves
+}
+
+template <typename IO, int DH, int CW, int W>
+static void launch_wide(const AttnArgs& a, int limit, void* workspace) {
+  constexpr int NT = 32 * CW * W;
+  const unsigned grid = static_cast<unsigned>(grid_of(a.R, a.T, a.max_q, a.Hq, a.Hkv, NT, W));
+  const bool split = may_split(a.max_pages, a.page_lg);
+  void* space = split ? workspace : nullptr;
+  if ((1 << a.page_lg) >= AT_TILE)
+    attn_wide_kernel<IO, DH, true, CW, W><<<grid, 64 * W, 0, a.stream>>>(a, limit, space);
+  else
+    attn_wide_kernel<IO, DH, false, CW, W><<<grid, 64 * W, 0, a.stream>>>(a, limit, space);
+  if (split) attn_wide_join_kernel<IO, DH, NT, W><<<AT_JOIN, AT_T, 0, a.stream>>>(a, space);
 }
 
 hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* workspace) {
-  const unsigned grid = static_cast<unsigned>(attn_wide_grid(a.R, a.T, a.max_q, a.Hq, a.Hkv));
-  const bool split = may_split(a.max_pages, a.page_lg);
-  void* space = split ? workspace : nullptr;
-  const bool big = (1 << a.page_lg) >= AT_TILE;
-  auto go = [&](auto big_pages, auto small_pages, auto join) {
-    if (big) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space);
-    else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space);
-    if (split) join<<<AT_JOIN, AT_T, 0, a.stream>>>(a, workspace);
-  };
-  if (a.bf16) {
-    if (a.DH == 64)
-      go(attn_wide_kernel<bf16_t, 64, true>, attn_wide_kernel<bf16_t, 64, false>, attn_wide_join_kernel<bf16_t, 64>);
-    else
-      go(attn_wide_kernel<bf16_t, 128, true>, attn_wide_kernel<bf16_t, 128, false>, attn_wide_join_kernel<bf16_t, 128>);
+  const bool long_chunks = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv) > 128;
+  if (!a.bf16) {
+    if (a.DH == 64) launch_wide<float, 64, 1, 4>(a, limit, workspace);
+    else launch_wide<float, 128, 1, 4>(a, limit, workspace);
+  } else if (long_chunks) {
+    if (a.DH == 64) launch_wide<bf16_t, 64, 2, 4>(a, limit, workspace);
+    else launch_wide<bf16_t, 128, 1, 8>(a, limit, workspace);
   } else {
-    if (a.DH == 64)
-      go(attn_wide_kernel<float, 64, true>, attn_wide_kernel<float, 64, false>, attn_wide_join_kernel<float, 64>);
-    else
-      go(attn_wide_kernel<float, 128, true>, attn_wide_kernel<float, 128, false>, attn_wide_join_kernel<float, 128>);
+    if (a.DH == 64) launch_wide<bf16_t, 64, 1, 4>(a, limit, workspace);
+    else launch_wide<bf16_t, 128, 1, 4>(a, limit, workspace);
   }
   return hipGetLastError();
 }
