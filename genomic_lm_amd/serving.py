@@ -80,9 +80,11 @@ def _norm_args(x, weight, residual, residual_out):
     rs = ros = 0
     if residual is not None:
         rp, rs = _rows("residual", residual, x)
-        if residual_out is None:
+        if residual_out is None:           # what is made here needs no check
             residual_out = _like(x)
-        rop, ros = _rows("residual_out", residual_out, x)
+            rop, ros = residual_out.data_ptr(), D
+        else:
+            rop, ros = _rows("residual_out", residual_out, x)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     T = x.numel() // D if D else 0
@@ -98,7 +100,9 @@ def add_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out=None, resi
     head, tail, residual_out = _norm_args(x, weight, residual, residual_out)
     if out is None:
         out = _like(x)
-    yp, ys = _rows("out", out, x)
+        yp, ys = out.data_ptr(), x.shape[-1]
+    else:
+        yp, ys = _rows("out", out, x)
     _check("hyena_add_rmsnorm", lib().hyena_add_rmsnorm(*head, eps, yp, ys, *tail))
     return out, residual_out
 
@@ -112,14 +116,19 @@ def add_rmsnorm_fp8(x, weight=None, residual=None, eps: float = 1e-6, group: int
     head, tail, residual_out = _norm_args(x, weight, residual, residual_out)
     if group not in (0, NORM_GROUP):
         raise ValueError(f"group must be 0 or {NORM_GROUP}")
-    shape, dev = x.shape, x.get_device()
+    shape = x.shape
     sshape = shape[:-1] if group == 0 else (*shape[:-1], (shape[-1] + group - 1) // group)
     if q is None:
         q = _like(x, torch.float8_e4m3fn)
+        qp = q.data_ptr()
+    else:
+        qp = _vec("q", q, q.dtype if getattr(q, "dtype", None) in _FP8 else torch.float8_e4m3fn, shape,
+                  x.get_device())
     if scale is None:
         scale = x.new_empty(sshape, dtype=torch.float32)
-    qp = _vec("q", q, q.dtype if getattr(q, "dtype", None) in _FP8 else torch.float8_e4m3fn, shape, dev)
-    sp = _vec("scale", scale, torch.float32, sshape, dev)
+        sp = scale.data_ptr()
+    else:
+        sp = _vec("scale", scale, torch.float32, sshape, x.get_device())
     _check("hyena_add_rmsnorm_fp8", lib().hyena_add_rmsnorm_fp8(*head, eps, qp, sp, group, *tail))
     return q, scale, residual_out
 
@@ -155,16 +164,21 @@ def page_map(old_lens, new_lens, block_table, free_pages, free_head, page_size: 
     fp = _vec("free_pages", free_pages, i32, None, dev)
     hp = None if free_head is None else _vec("free_head", free_head, i32, (1,), dev)
     T = int(T)
-    if cu is None or lens is None or positions is None or status is None:
-        # one allocation for the outputs that were not given
-        a, b, c, d = block_table.new_empty(2 * R + T + 3).split_with_sizes((R + 1, R, T, 2))
-        cu, lens = a if cu is None else cu, b if lens is None else lens
-        positions, status = c if positions is None else positions, d if status is None else status
-    if slots is None:
+    if cu is lens is positions is slots is status is None:
+        # one allocation for all outputs but the 64-bit one; what is made here needs no check
+        cu, lens, positions, status = block_table.new_empty(2 * R + T + 3).split_with_sizes((R + 1, R, T, 2))
         slots = block_table.new_empty(T, dtype=torch.int64)
-    cp, lp = _vec("cu", cu, i32, (R + 1,), dev), _vec("lens", lens, i32, (R,), dev)
-    pp, slp = _vec("positions", positions, i32, (T,), dev), _vec("slots", slots, torch.int64, (T,), dev)
-    stp = _vec("status", status, i32, (2,), dev)
+        cp, lp, pp, slp, stp = (t.data_ptr() for t in (cu, lens, positions, slots, status))
+    else:
+        new = block_table.new_empty
+        cu = new(R + 1) if cu is None else cu
+        lens = new(R) if lens is None else lens
+        positions = new(T) if positions is None else positions
+        slots = new(T, dtype=torch.int64) if slots is None else slots
+        status = new(2) if status is None else status
+        cp, lp = _vec("cu", cu, i32, (R + 1,), dev), _vec("lens", lens, i32, (R,), dev)
+        pp, slp = _vec("positions", positions, i32, (T,), dev), _vec("slots", slots, torch.int64, (T,), dev)
+        stp = _vec("status", status, i32, (2,), dev)
     _check("hyena_page_map", lib().hyena_page_map(
         op, np_, R, tp, step, width, fp, free_pages.numel(), hp, page_size, cp, lp, pp, slp, T, stp,
         _stream(block_table)))
