@@ -611,3 +611,144 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         for k in want[i]:
             assert bits_equal(st[k], want[i][k]), (i, k)
+
+
+# ------------------------------------------------------------------ paths that small cases do not reach
+@pytest.mark.parametrize("P", [16, 64])
+def test_append_gaps_inside_long_runs(P):
+    """Tokens without a slot between the tokens of one page, in runs of the workgroup's size.  Each
+    page's first token has its largest values, so the scale does not depend on how a run is cut."""
+    H, DH, N = 2, 128, 12
+    rng = np.random.default_rng(21)
+    slots = []
+    for page in (4, 1, 9):
+        here = list(page * P + np.arange(P))
+        for at in sorted(rng.choice(np.arange(2, P), 5, replace=False))[::-1]:
+            here[at:at] = [-1] * int(rng.integers(1, 4))
+        slots += here + [-1] * 3
+    for pad in (0, 4300):                           # short calls, and the long ones' token groups
+        s = np.array([-1] * pad + slots)
+        T = len(s)
+        k, v = (rng.uniform(-1, 1, (T, H, DH)) for _ in range(2))
+        first = [i for i in range(T) if s[i] >= 0 and s[i] % P == 0]
+        k[first], v[first] = 3.0, -3.0
+        k, v = tensor(k, BF), tensor(v, BF)
+        cache = random_cache(N, H, P, DH, 22)
+        want = host_cache(cache)
+        ref.append(to_f64(k), to_f64(v), s, *want, P)
+        G.kv_append_fp8(k, v, tensor(s, torch.int64), *cache)
+        check_append(cache, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R", [70, 300])
+def test_attn_many_requests(R, dtype):
+    """More requests than a wave has lanes: decodes, chunks, idle ones and empty ones together."""
+    rng = np.random.default_rng(R)
+    old = rng.integers(0, 60, R)
+    new = np.where(rng.random(R) < 0.1, rng.integers(2, 40, R), rng.integers(0, 2, R))
+    old[R // 2], new[R // 2] = 900, 1
+    old[-1], new[-1] = 150, 30
+    c = attn_case(old.tolist(), new.tolist(), 4, 2, 64, 16, dtype, seed=R)
+    c["lens"][3] = 0
+    check_attn(c, attend(c), label=f"{R} requests")
+
+
+@pytest.mark.parametrize("P,width", [(16, 16), (64, 4), (128, 1)])
+def test_attn_short_tables(P, width):
+    """Tables of at most four tiles: a unit per wave, no workspace."""
+    c = attn_case([P * width - 3, 0, 5, 100], [3, 1, 2, 1], 6, 2, 128, P, BF, seed=30, width=width)
+    assert G.attn_paged_workspace_size(4, 7, 3, width, P, 6, 2, 128) == 0
+    check_attn(c, attend(c), label="short tables")
+
+
+def exact_attention(c, rows):
+    """torch in 64 bits on the device, for one request: out of the queries `rows`, and the sums of
+    the absolute terms."""
+    P, n = c["P"], int(c["lens"][0])
+    pages = c["table"][0, :-(-n // P)].long()
+    f = torch.float64
+    k = (c["k"].view(torch.uint8)[pages].view(torch.float8_e4m3fn).to(f) * c["ks"][pages].to(f)[..., None, None])
+    v = (c["v"].view(torch.uint8)[pages].view(torch.float8_e4m3fn).to(f) * c["vs"][pages].to(f)[..., None, None])
+    k = k.permute(1, 0, 2, 3).flatten(1, 2)[:, :n]
+    v = v.permute(1, 0, 3, 2).flatten(1, 2)[:, :n]
+    q = c["q"].to(f)
+    T, Hq, DH = q.shape
+    group = Hq // k.shape[0]
+    outs, mags = [], []
+    for h in range(Hq):
+        s = (q[rows, h] @ k[h // group].t().contiguous()) * DH ** -0.5
+        pos = torch.arange(n - T, n, device=s.device)[rows]
+        s.masked_fill_(torch.arange(n, device=s.device)[None] > pos[:, None], float("-inf"))
+        w = s.softmax(-1)
+        outs.append(w @ v[h // group])
+        mags.append(w @ v[h // group].abs())
+    return torch.stack(outs, 1), torch.stack(mags, 1)
+
+
+def long_case(n, T, Hq, Hkv, DH, P, dtype, seed):
+    """One request of n cached tokens, made on the device, with one scale for all blocks: the same
+    tokens for every page size."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = (torch.randn((n, Hkv, DH), generator=g, device=dev()) * 100).clamp(-448, 448)
+    v = (torch.randn((n, Hkv, DH), generator=g, device=dev()) * 100).clamp(-448, 448)
+    q = torch.randn((T, Hq, DH), generator=g, device=dev()).to(dtype)
+    pages = -(-n // P)
+    pad = torch.full((pages * P - n, Hkv, DH), float("nan"), device=dev())
+    f8 = torch.float8_e4m3fn
+    k = torch.cat([k, pad]).to(f8).view(torch.uint8).view(pages, P, Hkv, DH).permute(0, 2, 1, 3).contiguous()
+    v = torch.cat([v, pad]).to(f8).view(torch.uint8).view(pages, P, Hkv, DH).permute(0, 2, 3, 1).contiguous()
+    order = torch.randperm(pages, generator=g, device=dev())
+    one = torch.full((pages, Hkv), 2.0 ** -6, device=dev())
+    return {"q": q, "k": k[order].view(f8), "v": v[order].view(f8), "ks": one, "vs": one,
+            "table": torch.argsort(order).to(I32)[None], "lens": torch.tensor([n], dtype=I32, device=dev()),
+            "cu": torch.tensor([0, T], dtype=I32, device=dev()), "P": P, "max_q": T, "DH": DH, "dtype": dtype}
+
+
+@pytest.mark.parametrize("DH,Hq,Hkv,n,T", [(128, 8, 2, 20000, 2048), (64, 8, 4, 9001, 1500), (128, 2, 2, 40000, 3)])
+def test_attn_long_pieces(DH, Hq, Hkv, n, T):
+    """Pieces longer than the tables are looked ahead for; the result does not depend on the page
+    size, bit for bit."""
+    outs = {}
+    for P in (16, 32, 64, 256):
+        c = long_case(n, T, Hq, Hkv, DH, P, BF, 40)
+        outs[P] = attend(c)
+        if P == 16:
+            rows = torch.cat([torch.arange(0, T, max(1, T // 200)), torch.tensor([T - 1])]).to(dev())
+            want, mag = exact_attention(c, rows)
+            # as check_attn, with the scores' error bounded by the largest |q||k| of 448 * 2^-6 * 5 * DH
+            reach = 7 * 5 * DH * DH ** -0.5
+            lim = mag * (2 * (DH + 8) * 2.0 ** -24 * reach + 2.0 ** -21 + n * 2.0 ** -24 + 2.0 ** -8) + 2.0 ** -8 * want.abs() * 1.01
+            e = (outs[P][rows].double() - want).abs()
+            log(f"  long DH={DH} n={n} T={T}: worst error / bound {(e / lim).max().item():.3f}")
+            assert (e <= lim).all()
+    for P in (32, 64, 256):
+        assert bits_equal(outs[P], outs[16]), P
+
+
+def test_graph_of_a_mixed_step():
+    """Chunks and decodes in one captured call, both kernels with their joins, replayed with other
+    queries and lengths between."""
+    c = attn_case([3000, 40, 2500, 7], [1, 200, 2, 1], 8, 2, 128, 64, BF, seed=50)
+    need = G.attn_paged_workspace_size(4, c["q"].shape[0], 200, c["table"].shape[1], 64, 8, 2, 128)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev())
+    out = torch.empty_like(c["q"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        attend(c, out=out, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attend(c, out=out, workspace=ws)
+    lens = c["lens"].clone()
+    for i in range(4):
+        c["q"].mul_(0.9)
+        c["lens"].copy_(lens - 5 * i)
+        want = attend(c)
+        out.fill_(float("nan"))
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bits_equal(out, want), i
+        check_attn(c, out, label=f"replay {i}")
