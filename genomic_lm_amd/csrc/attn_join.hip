@@ -1,0 +1,128 @@
+// attn_join.hip -- the pieces of attention units added up (attn_paged.hpp):
+//     out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p,   m = max m_p.
+// One launch for what both kernels left: its time is that of a launch and of
+// four dependent loads (4 us on an idle chip), the data is small.
+#include "attn_paged.hpp"
+
+namespace hyena {
+
+constexpr int AJ_WIDE = 512;               // workgroups that walk the wide units
+
+template <int DH>
+struct JoinShared {
+  static constexpr int LPC = DH / 4;       // lanes per column, four values each
+  static constexpr int SETS = AT_T / LPC;  // columns the workgroup holds at once
+  float m[SETS], l[SETS];
+  __align__(16) f32x4 o[SETS][LPC];
+};
+
+// Columns first, first + step, ... (`count` of them) of a unit.  The sets of
+// lanes that they leave over take every other (fourth, ...) piece and are added
+// through LDS.
+template <typename IO, int DH, typename Slot>
+__device__ __forceinline__ void join_columns(const AttnArgs& a, JoinShared<DH>& sh, const float* ml,
+                                             const float* part, int nt, int pieces, Slot slot_of,
+                                             int first, int step, int count, int tok0, int col0, int head) {
+  using S = JoinShared<DH>;
+  const int set = threadIdx.x / S::LPC, d = (threadIdx.x % S::LPC) * 4;
+  const int group = a.Hq / a.Hkv;
+  int lg = 0;                              // log2 of the columns side by side
+  while ((1 << lg) < count && (1 << lg) < S::SETS) ++lg;
+  const int side = 1 << lg, ways = S::SETS >> lg, way = set >> lg;
+  for (int k0 = 0; k0 < count; k0 += side) {
+    const int k = k0 + (set & (side - 1));
+    const int c = first + k * step;
+    float m = AT_NEG, l = 0.0f;
+    f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+    if (k < count) {
+#pragma unroll 8
+      for (int p = way; p < pieces; p += ways) {
+        const int64_t slot = slot_of(p);
+        const float pm = ml[(slot * 2) * nt + c], pl = ml[(slot * 2 + 1) * nt + c];
+        const f32x4 po = *reinterpret_cast<const f32x4*>(part + (slot * nt + c) * DH + d);
+        const float big = fmaxf(m, pm);
+        const float fo = m == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(m - big);
+        const float fp = pm == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(pm - big);
+        l = l * fo + pl * fp;
+        o = o * fo + po * fp;
+        m = big;
+      }
+    }
+    if (ways > 1) {
+      if (d == 0) {
+        sh.m[set] = m;
+        sh.l[set] = l;
+      }
+      sh.o[set][d >> 2] = o;
+      __syncthreads();
+      float big = AT_NEG;
+      for (int y = 0; y < ways; ++y) big = fmaxf(big, sh.m[(y << lg) + (set & (side - 1))]);
+      l = 0.0f;
+      o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int y = 0; y < ways; ++y) {
+        const int z = (y << lg) + (set & (side - 1));
+        const float f = sh.m[z] == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(sh.m[z] - big);
+        l += f * sh.l[z];
+        o += f * sh.o[z][d >> 2];
+      }
+      __syncthreads();
+    }
+    if (way == 0 && k < count) {
+      const int cc = col0 + c;
+      IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(tok0) + cc / group) * a.Hq +
+                                          static_cast<int64_t>(head) * group + cc % group) * DH + d;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Io<IO>::st(op, e, o[e] * inv);
+    }
+  }
+}
+
+// Workgroups [0, AN_WAVES * ny): the narrow unit that begins in a wave, its
+// columns shared by ny workgroups; the others walk the wide units, 16 columns
+// at a time, whose number only the device knows.
+template <typename IO, int DH>
+__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, void* narrow, int nt, int ny, void* wide,
+                                                         WideForm form) {
+  __shared__ JoinShared<DH> sh;
+  const int narrow_groups = narrow ? AN_WAVES * ny : 0;
+  const int b = static_cast<int>(blockIdx.x);
+  if (b < narrow_groups) {
+    const NarrowSpace ws = narrow_space(narrow, nt);
+    const int w = b / ny, y = b % ny;
+    const int4 h = ws.head[w];             // pieces, first query token, head, columns
+    if (h.x == 0) return;
+    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0); };
+    join_columns<IO, DH>(a, sh, ws.ml, ws.o, nt, h.x, slot_of, y, ny, (h.w - y + ny - 1) / ny, h.y, 0, h.z);
+    return;
+  }
+  const WideSpace ws = wide_space(wide, form.nt, form.waves);
+  const int64_t tasks = static_cast<int64_t>(*ws.used) * (form.nt / 16);
+  for (int64_t task = b - narrow_groups; task < tasks; task += gridDim.x - narrow_groups) {
+    const int64_t unit = task / (form.nt / 16);
+    const int first = static_cast<int>(task % (form.nt / 16)) * 16;
+    const AttnUnit u = ws.head[unit];
+    auto slot_of = [&](int p) { return u.slot + static_cast<int64_t>(p) * a.Hkv; };
+    join_columns<IO, DH>(a, sh, ws.ml, ws.o, form.nt, u.pieces, slot_of, first, 1, min(u.cols - first, 16),
+                         u.tok0, u.col0, static_cast<int>(unit % a.Hkv));
+  }
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide) {
+  const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
+  const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
+  // few units have many pieces each: their columns to workgroups of their own
+  const int ny = static_cast<int64_t>(a.R) * a.Hkv < 256 ? (nt < 4 ? nt : 4) : 1;
+  const unsigned grid = (narrow ? AN_WAVES * ny : 0) + (wide ? AJ_WIDE : 0);
+  auto go = [&](auto kernel) {
+    kernel<<<grid, AT_T, 0, a.stream>>>(a, narrow, nt, ny, wide, wide_form(cols, a.DH, a.bf16));
+  };
+  if (a.bf16) {
+    if (a.DH == 64) go(attn_join_kernel<bf16_t, 64>); else go(attn_join_kernel<bf16_t, 128>);
+  } else {
+    if (a.DH == 64) go(attn_join_kernel<float, 64>); else go(attn_join_kernel<float, 128>);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace hyena

@@ -9,30 +9,10 @@
 // tile always in flight, across the border of two units as within one.  A unit
 // that lies within one wave's share is written by it; the others leave partial
 // results (m, l, O) in the workspace, at most two per wave, which
-// attn_narrow_join_kernel adds up.
+// attn_join.hip adds up.
 #include "attn_paged.hpp"
 
 namespace hyena {
-
-constexpr int AN_GROUPS = 512;                    // workgroups: two per CU, all resident
-constexpr int AN_WAVES = AN_GROUPS * (AT_T / 64);
-constexpr int AN_WHOLE = 4;                       // tables of up to so many tiles: a unit per wave, no join
-
-// Partial results: wave w's first unit, begun by an earlier wave, in slot 2 w,
-// its last one, continued by the next, in 2 w + 1; nt columns each.
-struct NarrowSpace {
-  int4* head;      // per wave: pieces of the unit that begins in it and ends elsewhere (0: none),
-                   // its first query token, K/V head, columns
-  float* ml;
-  float* o;
-};
-__device__ __forceinline__ NarrowSpace narrow_space(void* p, int nt) {
-  NarrowSpace s;
-  s.head = static_cast<int4*>(p);
-  s.ml = reinterpret_cast<float*>(s.head + AN_WAVES);
-  s.o = s.ml + static_cast<size_t>(2 * AN_WAVES) * 2 * nt;
-  return s;
-}
 
 // A tile in the list, and its request; the same in every lane.
 struct Place {
@@ -418,114 +398,22 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
   if (space && lane == 0) ws.head[wave] = header;
 }
 
-// Joins the pieces of the unit that begins in wave blockIdx.x and ends in a
-// later one:  out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p.  Lanes: DH / 4
-// per column, four values each; the sets of lanes that the unit's columns
-// leave over take every other (fourth, ...) piece and are added through LDS.
-// Workgroups y share the columns of a unit.
-template <typename IO, int DH>
-__global__ __launch_bounds__(AT_T) void attn_narrow_join_kernel(AttnArgs a, void* space, int nt) {
-  constexpr int LPC = DH / 4;
-  constexpr int SETS = AT_T / LPC;
-  __shared__ float s_m[SETS], s_l[SETS];
-  __shared__ __align__(16) f32x4 s_o[SETS][LPC];
-  const NarrowSpace ws = narrow_space(space, nt);
-  const int w = blockIdx.x;
-  const int4 h = ws.head[w];               // pieces, first query token, head, columns
-  if (h.x == 0) return;
-  const int group = a.Hq / a.Hkv;
-  const int set = threadIdx.x / LPC, d = (threadIdx.x % LPC) * 4;
-  const int mine = (h.w - static_cast<int>(blockIdx.y) + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
-  int lg = 0;                              // log2 of the columns side by side
-  while ((1 << lg) < mine && (1 << lg) < SETS) ++lg;
-  const int side = 1 << lg, ways = SETS >> lg, way = set >> lg;
-  for (int c0 = 0; c0 < mine; c0 += side) {
-    const int k = c0 + (set & (side - 1));
-    const int c = static_cast<int>(blockIdx.y) + k * static_cast<int>(gridDim.y);
-    float m = AT_NEG, l = 0.0f;
-    f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
-    if (k < mine) {
-#pragma unroll 8
-      for (int p = way; p < h.x; p += ways) {
-        const int64_t slot = 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0);
-        const float pm = ws.ml[(slot * 2) * nt + c], pl = ws.ml[(slot * 2 + 1) * nt + c];
-        const f32x4 po = *reinterpret_cast<const f32x4*>(ws.o + (slot * nt + c) * DH + d);
-        const float big = fmaxf(m, pm);
-        const float fo = m == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(m - big);
-        const float fp = pm == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(pm - big);
-        l = l * fo + pl * fp;
-        o = o * fo + po * fp;
-        m = big;
-      }
-    }
-    if (ways > 1) {
-      if (d == 0) {
-        s_m[set] = m;
-        s_l[set] = l;
-      }
-      s_o[set][d >> 2] = o;
-      __syncthreads();
-      float big = AT_NEG;
-      for (int y = 0; y < ways; ++y) big = fmaxf(big, s_m[(y << lg) + (set & (side - 1))]);
-      l = 0.0f;
-      o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int y = 0; y < ways; ++y) {
-        const int z = (y << lg) + (set & (side - 1));
-        const float f = s_m[z] == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(s_m[z] - big);
-        l += f * s_l[z];
-        o += f * s_o[z][d >> 2];
-      }
-      __syncthreads();
-    }
-    if (way == 0 && k < mine) {
-      IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(h.y) + c / group) * a.Hq +
-                                          static_cast<int64_t>(h.z) * group + c % group) * DH + d;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) Io<IO>::st(op, e, o[e] * inv);
-    }
-  }
-}
-
 // ---------------------------------------------------------------- host
-static bool whole(int64_t max_pages, int page_lg) {
-  return (max_pages << page_lg) <= AN_WHOLE * AT_TILE;
-}
-
-size_t attn_narrow_workspace(int64_t max_pages, int page_lg, int64_t cols, int DH) {
-  if (whole(max_pages, page_lg)) return 0;
-  const int64_t nt = cols < AT_NARROW ? cols : AT_NARROW;
-  return static_cast<size_t>(AN_WAVES) * (sizeof(int4) + 2 * 4 * (2 * nt + nt * DH));
-}
-
-hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* workspace) {
+hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* space) {
   const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
   const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
-  const bool big = (1 << a.page_lg) >= AT_TILE;
-  auto go = [&](auto big_pages, auto small_pages, auto join) {
-    auto launch = [&](unsigned grid, void* space) {
-      if (big) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
-      else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
-    };
-    const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
-    if (whole(a.max_pages, a.page_lg)) {
-      launch(static_cast<unsigned>((units + 3) / 4), nullptr);
-      return;
-    }
-    launch(AN_GROUPS, workspace);
-    // few units have many pieces each: their columns to workgroups of their own
-    join<<<dim3(AN_WAVES, units < 256 && nt > 1 ? (nt < 4 ? nt : 4) : 1), AT_T, 0, a.stream>>>(a, workspace, nt);
+  const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
+  const unsigned grid = space ? AN_GROUPS : static_cast<unsigned>((units + AT_T / 64 - 1) / (AT_T / 64));
+  auto go = [&](auto big_pages, auto small_pages) {
+    if ((1 << a.page_lg) >= AT_TILE) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
+    else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
   };
   if (a.bf16) {
-    if (a.DH == 64)
-      go(attn_narrow_kernel<bf16_t, 64, true>, attn_narrow_kernel<bf16_t, 64, false>, attn_narrow_join_kernel<bf16_t, 64>);
-    else
-      go(attn_narrow_kernel<bf16_t, 128, true>, attn_narrow_kernel<bf16_t, 128, false>, attn_narrow_join_kernel<bf16_t, 128>);
+    if (a.DH == 64) go(attn_narrow_kernel<bf16_t, 64, true>, attn_narrow_kernel<bf16_t, 64, false>);
+    else go(attn_narrow_kernel<bf16_t, 128, true>, attn_narrow_kernel<bf16_t, 128, false>);
   } else {
-    if (a.DH == 64)
-      go(attn_narrow_kernel<float, 64, true>, attn_narrow_kernel<float, 64, false>, attn_narrow_join_kernel<float, 64>);
-    else
-      go(attn_narrow_kernel<float, 128, true>, attn_narrow_kernel<float, 128, false>, attn_narrow_join_kernel<float, 128>);
+    if (a.DH == 64) go(attn_narrow_kernel<float, 64, true>, attn_narrow_kernel<float, 64, false>);
+    else go(attn_narrow_kernel<float, 128, true>, attn_narrow_kernel<float, 128, false>);
   }
   return hipGetLastError();
 }

@@ -141,12 +141,88 @@ __device__ __forceinline__ PerRun<float, BIG> run_scales(const AttnArgs& a, cons
   return r;
 }
 
-// Requests of up to `limit` columns (attn_narrow.hip) and of more than `limit`
-// (attn_wide.hip), each with its launches, workspace and largest grid.
-hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* workspace);
-hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* workspace);
-size_t attn_narrow_workspace(int64_t max_pages, int page_lg, int64_t cols, int DH);
-size_t attn_wide_workspace(int64_t max_pages, int page_lg, int DH);
-int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv);
+// ---------------------------------------------------------------- partial results
+// Where a unit (columns of one request on one K/V head) is worked on by several
+// waves or workgroups, each leaves m, l and O of its tokens in the workspace;
+// attn_join.hip adds them up.  nt columns per slot: m and l (nt each), O (nt x DH).
+
+// Tables of at most AT_SHORT tiles are not split.
+constexpr int AT_SHORT = 4;
+inline bool short_table(int64_t max_pages, int page_lg) {
+  return (max_pages << page_lg) <= AT_SHORT * AT_TILE;
+}
+
+// Narrow: wave w's first unit, begun by an earlier wave, in slot 2 w, its last
+// one, continued by the next, in 2 w + 1.
+constexpr int AN_GROUPS = 512;            // workgroups: two per CU, all resident
+constexpr int AN_WAVES = AN_GROUPS * (AT_T / 64);
+struct NarrowSpace {
+  int4* head;                // per wave: pieces of the unit that begins in it and ends elsewhere (0: none),
+                             // its first query token, K/V head, columns
+  float* ml;
+  float* o;
+};
+__device__ __forceinline__ NarrowSpace narrow_space(void* p, int nt) {
+  NarrowSpace s;
+  s.head = static_cast<int4*>(p);
+  s.ml = reinterpret_cast<float*>(s.head + AN_WAVES);
+  s.o = s.ml + static_cast<size_t>(2 * AN_WAVES) * 2 * nt;
+  return s;
+}
+inline size_t narrow_bytes(int64_t nt, int DH) {
+  return static_cast<size_t>(AN_WAVES) * (sizeof(int4) + 2 * 4 * (2 * nt + nt * DH));
+}
+
+// Wide: a slot per piece and head.  Eight waves per CU hold wide_target pieces
+// at once (two workgroups of four, or one of eight); a unit worth x > 1 of
+// them is cut into fewer than 2 x.
+constexpr int wide_target(int waves) { return 2048 / waves; }
+constexpr int wide_slots(int waves) { return 2 * wide_target(waves); }
+struct AttnUnit {
+  int pieces, slot;          // and its first slot; piece p lies p * heads slots on
+  int tok0, col0, cols;      // the request's first query token; the unit's first column, its columns
+  int pad[3];
+};
+struct WideSpace {
+  int* used;                 // units of several pieces
+  AttnUnit* head;
+  float* ml;
+  float* o;
+};
+__device__ __forceinline__ WideSpace wide_space(void* p, int nt, int waves) {
+  WideSpace s;
+  s.used = static_cast<int*>(p);
+  s.head = reinterpret_cast<AttnUnit*>(static_cast<char*>(p) + 16);
+  s.ml = reinterpret_cast<float*>(s.head + wide_slots(waves) / 2);      // a split unit has at least two slots
+  s.o = s.ml + static_cast<size_t>(wide_slots(waves)) * 2 * nt;
+  return s;
+}
+inline size_t wide_bytes(int nt, int waves, int DH) {
+  return 16 + static_cast<size_t>(wide_slots(waves)) * (sizeof(AttnUnit) / 2 + 4 * (2 * nt + nt * DH));
+}
+
+// Columns and waves of a wide unit.  128 columns if no request has more; else
+// 256, so that a tile is widened for twice as many.  Heads of 128: eight waves
+// of 32 columns (2.26 -> 2.13 ms for a 4096-token chunk at 32768); 64 columns
+// per wave need more registers than two waves per SIMD have (2.57 ms).  Heads
+// of 64: four waves of 64 columns (1.31 -> 1.20 ms).  fp32's operands fill the
+// registers: 32 columns per wave.
+struct WideForm {
+  int nt, waves;
+};
+inline WideForm wide_form(int64_t cols, int DH, bool bf16) {
+  if (!bf16) return DH == 64 ? WideForm{128, 4} : WideForm{256, 8};
+  if (cols <= 128) return WideForm{128, 4};
+  return DH == 64 ? WideForm{256, 4} : WideForm{256, 8};
+}
+
+// ---------------------------------------------------------------- launches
+// Requests of up to `limit` columns (attn_narrow.hip) and of more
+// (attn_wide.hip); space NULL: short tables, nothing is split.
+hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* space);
+hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* space);
+int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, const WideForm& f);
+// Adds up what either left (NULL: was not launched).
+hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide);
 
 }  // namespace hyena

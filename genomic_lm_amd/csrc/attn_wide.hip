@@ -11,15 +11,8 @@ namespace hyena {
 // that about wide_target(W) pieces exist, what the chip holds at once: chunks
 // with few columns over long contexts then still fill it.  A unit of several
 // pieces leaves partial results in the workspace, one slot per piece and head,
-// which attn_wide_join_kernel adds up; a unit of one piece writes its rows
+// which attn_join.hip adds up; a unit of one piece writes its rows
 // directly.
-constexpr int AT_MIN_PIECE = 4;           // tiles
-constexpr int AT_JOIN = 512;              // workgroups of the joining launch
-// eight waves per CU: two workgroups of four, or one of eight
-constexpr int wide_target(int waves) { return 2048 / waves; }
-// a unit worth x > 1 pieces is cut into fewer than 2 x
-constexpr int wide_slots(int waves) { return 2 * wide_target(waves); }
-
 struct AttnWork {
   int tok0, queries, len;    // the request: first query token, queries (up to max_q), cached tokens
   int ahead;                 // position of the first query
@@ -68,7 +61,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
   auto tiles_of = [](int len) { return (len + AT_TILE - 1) / AT_TILE; };
   auto piece_tiles = [&](unsigned long long work) {
     const unsigned long long even = (work * a.Hkv + wide_target(W) - 1) / wide_target(W);
-    return static_cast<int>(even > AT_MIN_PIECE ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_MIN_PIECE);
+    return static_cast<int>(even > AT_SHORT ? (even < 0x7FFFFFFF ? even : 0x7FFFFFFF) : AT_SHORT);
   };
   int tiles = 0, at = 0;
   auto pieces_of = [&](int len) {
@@ -198,29 +191,6 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
   return true;
 }
 
-// ---------------------------------------------------------------- workspace
-// the count of units of several pieces, a header for each, then m, l (NT each)
-// and O (NT x DH) per slot
-struct AttnUnit {
-  int pieces, slot;          // and its first slot; piece p lies p * heads slots on
-  int tok0, col0, cols;      // the request's first query token; the unit's first column, its columns
-  int pad[3];
-};
-struct AttnSpace {
-  int* used;                 // units of several pieces
-  AttnUnit* head;
-  float* ml;
-  float* o;
-};
-__device__ __forceinline__ AttnSpace attn_space(void* p, int nt, int waves) {
-  AttnSpace s;
-  s.used = static_cast<int*>(p);
-  s.head = reinterpret_cast<AttnUnit*>(static_cast<char*>(p) + 16);
-  s.ml = reinterpret_cast<float*>(s.head + wide_slots(waves) / 2);      // a split unit has at least two slots
-  s.o = s.ml + static_cast<size_t>(wide_slots(waves)) * 2 * nt;
-  return s;
-}
-
 // ---------------------------------------------------------------- wide units
 // S^T and O^T of 32 columns per wave on 32x32x16 MFMAs.  Lane l: i = l % 32 its
 // row of A and column of B and C, hf = l / 32 its half.  Row i of a 32-token
@@ -253,7 +223,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
   const int head = static_cast<int>(blockIdx.x % a.Hkv);
   const int item = static_cast<int>(blockIdx.x / a.Hkv);
   const int group = a.Hq / a.Hkv;
-  const AttnSpace ws = attn_space(space, WNT, W);
+  const WideSpace ws = wide_space(space, WNT, W);
   AttnWork w;
   int splits;
   const bool have = find_work<WNT, W>(a, lo, item, sh, w, splits);
@@ -602,137 +572,33 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
         AttnUnit{w.pieces, static_cast<int>(w.slot * a.Hkv + head), w.tok0, c0, min(WNT, cols - c0), {0, 0, 0}};
 }
 
-// ---------------------------------------------------------------- joining pieces
-// out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p over a unit's pieces.  A
-// workgroup takes 16 columns of a unit: DH / 4 lanes per column, four values
-// each; with fewer columns than it has lanes for, the lanes left over take
-// every other (fourth, eighth) piece and are added through LDS.  The grid is
-// fixed and walks the units, whose number only the device knows.
-template <typename IO, int DH, int NT, int W>
-__global__ __launch_bounds__(AT_T) void attn_wide_join_kernel(AttnArgs a, void* space) {
-  constexpr int LPC = DH / 4;              // lanes per column
-  constexpr int SETS = AT_T / LPC;         // columns the workgroup holds at once
-  __shared__ float s_m[SETS], s_l[SETS];
-  __shared__ __align__(16) f32x4 s_o[SETS][LPC];
-  const AttnSpace ws = attn_space(space, NT, W);
-  const int64_t tasks = static_cast<int64_t>(*ws.used) * (NT / 16);
-  const int group = a.Hq / a.Hkv;
-  const int set = threadIdx.x / LPC, d = (threadIdx.x % LPC) * 4;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int64_t unit = task / (NT / 16);
-    const int first = static_cast<int>(task % (NT / 16)) * 16;
-    const AttnUnit u = ws.head[unit];
-    const int head = static_cast<int>(unit % a.Hkv);
-    const int cols = min(u.cols - first, 16);
-    if (cols <= 0) continue;
-    int lg = 0;                            // log2 of the columns side by side
-    while ((1 << lg) < cols && (1 << lg) < SETS) ++lg;
-    const int side = 1 << lg, ways = SETS >> lg;
-    const int way = set >> lg;
-    for (int c0 = 0; c0 < cols; c0 += side) {
-      const int c = c0 + (set & (side - 1));
-      float m = AT_NEG, l = 0.0f;
-      f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
-      if (c < cols) {
-#pragma unroll 4
-        for (int p = way; p < u.pieces; p += ways) {
-          const int64_t s = u.slot + static_cast<int64_t>(p) * a.Hkv;
-          const float pm = ws.ml[s * 2 * NT + first + c], pl = ws.ml[s * 2 * NT + NT + first + c];
-          const f32x4 po = *reinterpret_cast<const f32x4*>(ws.o + (s * NT + first + c) * DH + d);
-          const float big = fmaxf(m, pm);
-          const float fo = m == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(m - big);
-          const float fp = pm == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(pm - big);
-          l = l * fo + pl * fp;
-          o = o * fo + po * fp;
-          m = big;
-        }
-      }
-      if (ways > 1) {
-        if (d == 0) {
-          s_m[set] = m;
-          s_l[set] = l;
-        }
-        s_o[set][d >> 2] = o;
-        __syncthreads();
-        float big = AT_NEG;
-        for (int k = 0; k < ways; ++k) big = fmaxf(big, s_m[(k << lg) + (set & (side - 1))]);
-        l = 0.0f;
-        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int k = 0; k < ways; ++k) {
-          const int from = (k << lg) + (set & (side - 1));
-          const float f = s_m[from] == AT_NEG ? 0.0f : __builtin_amdgcn_exp2f(s_m[from] - big);
-          l += f * s_l[from];
-          o += f * s_o[from][d >> 2];
-        }
-        __syncthreads();
-      }
-      if (way == 0 && c < cols) {
-        const int cc = u.col0 + first + c;
-        IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(u.tok0) + cc / group) * a.Hq +
-                                            static_cast<int64_t>(head) * group + cc % group) * DH + d;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) Io<IO>::st(op, e, o[e] * inv);
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------- host
-static bool may_split(int64_t max_pages, int page_lg) {
-  return (max_pages << page_lg) > AT_MIN_PIECE * AT_TILE;
-}
-
-size_t attn_wide_workspace(int64_t max_pages, int page_lg, int DH) {
-  if (!may_split(max_pages, page_lg)) return 0;
-  // slots times columns is the same for both of a head dimension's units (below);
-  // headers are most for the narrower one
-  const int64_t columns = DH == 64 ? 1024 * 256 : 1024 * 128;
-  return 16 + wide_slots(4) * (sizeof(AttnUnit) / 2) + static_cast<size_t>(columns) * (4 * (2 + DH));
-}
-
-static int64_t grid_of(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int nt, int waves) {
+int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, const WideForm& f) {
   // ceil per request: at most one unit more than its columns' share, and at
   // most the units of max_q queries
   const int64_t group = Hq / Hkv;
-  const int64_t share = T * group / nt + R;
-  const int64_t each = R * ((max_q * group + nt - 1) / nt);
-  return ((share < each ? share : each) + wide_target(waves) / Hkv + 1) * Hkv;
+  const int64_t share = T * group / f.nt + R;
+  const int64_t each = R * ((max_q * group + f.nt - 1) / f.nt);
+  return ((share < each ? share : each) + wide_target(f.waves) / Hkv + 1) * Hkv;
 }
 
-int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv) {
-  return 2 * grid_of(R, T, max_q, Hq, Hkv, 128, 4);     // the most there can be, in workgroups of four waves
-}
-
-template <typename IO, int DH, int CW, int W>
-static void launch_wide(const AttnArgs& a, int limit, void* workspace) {
-  constexpr int NT = 32 * CW * W;
-  const unsigned grid = static_cast<unsigned>(grid_of(a.R, a.T, a.max_q, a.Hq, a.Hkv, NT, W));
-  const bool split = may_split(a.max_pages, a.page_lg);
-  void* space = split ? workspace : nullptr;
-  if ((1 << a.page_lg) >= AT_TILE)
-    attn_wide_kernel<IO, DH, true, CW, W><<<grid, 64 * W, 0, a.stream>>>(a, limit, space);
-  else
-    attn_wide_kernel<IO, DH, false, CW, W><<<grid, 64 * W, 0, a.stream>>>(a, limit, space);
-  if (split) attn_wide_join_kernel<IO, DH, NT, W><<<AT_JOIN, AT_T, 0, a.stream>>>(a, space);
-}
-
-hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* workspace) {
-  const bool long_chunks = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv) > 128;
-  // more than 128 columns: 256 to a unit, so that a tile is widened for twice as
-  // many.  Heads of 128: eight waves of 32 columns (2.26 -> 2.13 ms for a
-  // 4096-token chunk at 32768); 64 columns per wave need more registers than
-  // two waves per SIMD have (2.57 ms).  Heads of 64: four waves of 64 columns
-  // (1.31 -> 1.20 ms).
+hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* space) {
+  const WideForm f = wide_form(static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv), a.DH, a.bf16);
+  const unsigned grid = static_cast<unsigned>(attn_wide_grid(a.R, a.T, a.max_q, a.Hq, a.Hkv, f));
+  auto go = [&](auto big_pages, auto small_pages) {
+    if ((1 << a.page_lg) >= AT_TILE) big_pages<<<grid, 64 * f.waves, 0, a.stream>>>(a, limit, space);
+    else small_pages<<<grid, 64 * f.waves, 0, a.stream>>>(a, limit, space);
+  };
+  // columns per wave in sets of 32: nt = 32 CW W
   if (!a.bf16) {
-    if (a.DH == 64) launch_wide<float, 64, 1, 4>(a, limit, workspace);
-    else launch_wide<float, 128, 1, 8>(a, limit, workspace);
-  } else if (long_chunks) {
-    if (a.DH == 64) launch_wide<bf16_t, 64, 2, 4>(a, limit, workspace);
-    else launch_wide<bf16_t, 128, 1, 8>(a, limit, workspace);
+    if (a.DH == 64) go(attn_wide_kernel<float, 64, true, 1, 4>, attn_wide_kernel<float, 64, false, 1, 4>);
+    else go(attn_wide_kernel<float, 128, true, 1, 8>, attn_wide_kernel<float, 128, false, 1, 8>);
+  } else if (f.nt == 256) {
+    if (a.DH == 64) go(attn_wide_kernel<bf16_t, 64, true, 2, 4>, attn_wide_kernel<bf16_t, 64, false, 2, 4>);
+    else go(attn_wide_kernel<bf16_t, 128, true, 1, 8>, attn_wide_kernel<bf16_t, 128, false, 1, 8>);
   } else {
-    if (a.DH == 64) launch_wide<bf16_t, 64, 1, 4>(a, limit, workspace);
-    else launch_wide<bf16_t, 128, 1, 4>(a, limit, workspace);
+    if (a.DH == 64) go(attn_wide_kernel<bf16_t, 64, true, 1, 4>, attn_wide_kernel<bf16_t, 64, false, 1, 4>);
+    else go(attn_wide_kernel<bf16_t, 128, true, 1, 4>, attn_wide_kernel<bf16_t, 128, false, 1, 4>);
   }
   return hipGetLastError();
 }
