@@ -78,34 +78,33 @@ __device__ __forceinline__ void join_columns(const AttnArgs& a, JoinShared<DH>& 
   }
 }
 
-// Workgroups [0, AN_WAVES * ny): the narrow unit that begins in a wave, its
-// columns shared by ny workgroups; the others walk the wide units, 16 columns
-// at a time, whose number only the device knows.
+// Workgroups [0, wide_groups) walk the wide units, 16 columns at a time, whose
+// number only the device knows; ny each of the others share the columns of the
+// narrow unit that begins in a wave.
 template <typename IO, int DH>
 __global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, void* narrow, int nt, int ny, void* wide,
-                                                         WideForm form) {
+                                                         WideForm form, int wide_groups) {
   __shared__ JoinShared<DH> sh;
-  const int narrow_groups = narrow ? AN_WAVES * ny : 0;
   const int b = static_cast<int>(blockIdx.x);
-  if (b < narrow_groups) {
-    const NarrowSpace ws = narrow_space(narrow, nt);
-    const int w = b / ny, y = b % ny;
-    const int4 h = ws.head[w];             // pieces, first query token, head, columns
-    if (h.x == 0) return;
-    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0); };
-    join_columns<IO, DH>(a, sh, ws.ml, ws.o, nt, h.x, slot_of, y, ny, (h.w - y + ny - 1) / ny, h.y, 0, h.z);
+  if (b < wide_groups) {
+    const WideSpace ws = wide_space(wide, form.nt, form.waves);
+    const int64_t tasks = static_cast<int64_t>(*ws.used) * (form.nt / 16);
+    for (int64_t task = b; task < tasks; task += wide_groups) {
+      const int64_t unit = task / (form.nt / 16);
+      const int first = static_cast<int>(task % (form.nt / 16)) * 16;
+      const AttnUnit u = ws.head[unit];
+      auto slot_of = [&](int p) { return u.slot + static_cast<int64_t>(p) * a.Hkv; };
+      join_columns<IO, DH>(a, sh, ws.ml, ws.o, form.nt, u.pieces, slot_of, first, 1, min(u.cols - first, 16),
+                           u.tok0, u.col0, static_cast<int>(unit % a.Hkv));
+    }
     return;
   }
-  const WideSpace ws = wide_space(wide, form.nt, form.waves);
-  const int64_t tasks = static_cast<int64_t>(*ws.used) * (form.nt / 16);
-  for (int64_t task = b - narrow_groups; task < tasks; task += gridDim.x - narrow_groups) {
-    const int64_t unit = task / (form.nt / 16);
-    const int first = static_cast<int>(task % (form.nt / 16)) * 16;
-    const AttnUnit u = ws.head[unit];
-    auto slot_of = [&](int p) { return u.slot + static_cast<int64_t>(p) * a.Hkv; };
-    join_columns<IO, DH>(a, sh, ws.ml, ws.o, form.nt, u.pieces, slot_of, first, 1, min(u.cols - first, 16),
-                         u.tok0, u.col0, static_cast<int>(unit % a.Hkv));
-  }
+  const NarrowSpace ws = narrow_space(narrow, nt);
+  const int w = (b - wide_groups) / ny, y = (b - wide_groups) % ny;
+  const int4 h = ws.head[w];               // pieces, first query token, head, columns
+  if (h.x == 0) return;
+  auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0); };
+  join_columns<IO, DH>(a, sh, ws.ml, ws.o, nt, h.x, slot_of, y, ny, (h.w - y + ny - 1) / ny, h.y, 0, h.z);
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide) {
@@ -113,9 +112,11 @@ hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide) {
   const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
   // few units have many pieces each: their columns to workgroups of their own
   const int ny = static_cast<int64_t>(a.R) * a.Hkv < 256 ? (nt < 4 ? nt : 4) : 1;
-  const unsigned grid = (narrow ? AN_WAVES * ny : 0) + (wide ? AJ_WIDE : 0);
+  const int wide_groups = wide ? AJ_WIDE : 0;
+  const unsigned grid = wide_groups + (narrow ? AN_WAVES * ny : 0);
   auto go = [&](auto kernel) {
-    kernel<<<grid, AT_T, 0, a.stream>>>(a, narrow, nt, ny, wide, wide_form(cols, a.DH, a.bf16));
+    kernel<<<grid, AT_T, 0, a.stream>>>(a, narrow, nt, ny, wide, wide_form(cols, a.DH, a.bf16),
+                                         wide_groups);
   };
   if (a.bf16) {
     if (a.DH == 64) go(attn_join_kernel<bf16_t, 64>); else go(attn_join_kernel<bf16_t, 128>);
