@@ -79,10 +79,12 @@ __device__ __forceinline__ void join_columns(const AttnArgs& a, JoinShared<DH>& 
 }
 
 // Workgroups [0, wide_groups) walk the wide units, 16 columns at a time, whose
-// number only the device knows; ny each of the others share the columns of the
-// narrow unit that begins in a wave.
+// number only the device knows.  Of the others each belongs to a wave of the
+// narrow kernel and to the two units that it may have left in part; the
+// workgroups of one unit share its columns, so that few units of many pieces
+// still occupy many.
 template <typename IO, int DH>
-__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, void* narrow, int nt, int ny, void* wide,
+__global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, void* narrow, int nt, void* wide,
                                                          WideForm form, int wide_groups) {
   __shared__ JoinShared<DH> sh;
   const int b = static_cast<int>(blockIdx.x);
@@ -100,22 +102,30 @@ __global__ __launch_bounds__(AT_T) void attn_join_kernel(AttnArgs a, void* narro
     return;
   }
   const NarrowSpace ws = narrow_space(narrow, nt);
-  const int w = (b - wide_groups) / ny, y = (b - wide_groups) % ny;
-  const int4 h = ws.head[w];               // pieces, first query token, head, columns
-  if (h.x == 0) return;
-  auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(w + p) + (p == 0 ? 1 : 0); };
-  join_columns<IO, DH>(a, sh, ws.ml, ws.o, nt, h.x, slot_of, y, ny, (h.w - y + ny - 1) / ny, h.y, 0, h.z);
+  const int w = b - wide_groups;
+  const int4 slots[2] = {ws.head[2 * w], ws.head[2 * w + 1]};
+#pragma unroll
+  for (int z = 1; z >= 0; --z) {
+    const int4 h = slots[z];               // first wave, pieces, first query token, head and columns
+    // of the unit's waves as many workgroups as give each lane eight pieces, the
+    // loads it has in flight
+    constexpr int BATCH = 8 * JoinShared<DH>::SETS;
+    const int y = w - h.x, cols = h.w >> 16;
+    const int n = min(min(h.y, cols), (h.y * cols + BATCH - 1) / BATCH);
+    if (y >= n) continue;
+    auto slot_of = [&](int p) { return 2 * static_cast<int64_t>(h.x + p) + (p == 0 ? 1 : 0); };
+    join_columns<IO, DH>(a, sh, ws.ml, ws.o, nt, h.y, slot_of, y, n, (cols - y + n - 1) / n, h.z, 0,
+                         h.w & 0xFFFF);
+  }
 }
 
-hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide) {
+hipError_t launch_attn_join(const AttnArgs& a, int limit, void* narrow, void* wide) {
   const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
-  const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
-  // few units have many pieces each: their columns to workgroups of their own
-  const int ny = static_cast<int64_t>(a.R) * a.Hkv < 256 ? (nt < 4 ? nt : 4) : 1;
+  const int nt = narrow_columns(limit, cols);
   const int wide_groups = wide ? AJ_WIDE : 0;
-  const unsigned grid = wide_groups + (narrow ? AN_WAVES * ny : 0);
+  const unsigned grid = wide_groups + (narrow ? AN_WAVES : 0);
   auto go = [&](auto kernel) {
-    kernel<<<grid, AT_T, 0, a.stream>>>(a, narrow, nt, ny, wide, wide_form(cols, a.DH, a.bf16),
+    kernel<<<grid, AT_T, 0, a.stream>>>(a, narrow, nt, wide, wide_form(cols, a.DH, a.bf16),
                                          wide_groups);
   };
   if (a.bf16) {

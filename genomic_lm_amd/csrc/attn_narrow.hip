@@ -49,6 +49,8 @@ __device__ __forceinline__ void advance(const AttnArgs& a, int limit, Place& p) 
   do set_request(a, limit, p.r + 1, p); while (p.tiles == 0 && p.r + 1 < a.R);
 }
 
+constexpr int AN_PAIR = 4;
+
 struct NarrowShared {
   unsigned long long before[AT_T], part[AT_T / 64];
 };
@@ -65,8 +67,13 @@ __device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, in
     request_of(a, r, t, q, n);
     return static_cast<long long>(unit_tiles(q, n, group, limit)) * a.Hkv;
   };
+  // With more than AN_PAIR columns two tiles at least: a piece of one tile would
+  // write and read again as many bytes as the tile (1 x 65536 tokens of one head,
+  // 16 columns 26 -> 19 us, 32 columns 28 -> 22 us; four tiles at 32 columns are
+  // as fast there and slower in short calls, 17.4 against 15.7 us at 1 x 16384).
+  const int least = min(a.max_q * group, limit) > AN_PAIR ? 2 : 1;
   auto share = [&](long long total) {
-    per = (total + AN_WAVES - 1) / AN_WAVES;
+    per = max((total + AN_WAVES - 1) / AN_WAVES, static_cast<long long>(least));
     at = per * w;
     return min(per, total - at);
   };
@@ -147,12 +154,13 @@ __device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, in
 // Two waves per SIMD with 16 KiB of the next tile in flight each: 128 KiB per
 // CU, against ~25 bytes a cycle that a CU's share of HBM delivers in ~2000
 // cycles of latency.
-template <typename IO, int DH, bool BIG>
+template <typename IO, int DH, bool BIG, int CT>
 __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int limit, void* space, int nt) {
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
   constexpr int KH = DH / 64;            // 16-byte loads per K row and lane
   constexpr int KS = DH / 32;            // MFMA steps over the head dimension
   constexpr int DT = DH / 16;            // 16-row tiles of O^T
+  constexpr bool AHEAD = CT == 1;        // the next unit's queries are loaded early: registers allow it
   __shared__ NarrowShared sh;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
   } else {
     left = uni(static_cast<int>(find_share(a, limit, wave, sh, cur, at, per)));
   }
-  int4 header{0, 0, 0, 0};
+  if (space && lane < 2) ws.head[2 * wave + lane] = int4{0, 0, 0, 0};   // no partial results yet
   if (left > 0) {
     const int lg = a.page_lg, pmask = (1 << lg) - 1;
     const int64_t page_bytes = (static_cast<int64_t>(a.Hkv) << lg) * DH;
@@ -180,7 +188,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
     const int krow = 16 * (i >> 2) + (i & 3);            // this lane's token of K's sub-tile 0
 
     u32x4 kr[4][KH], vr[DT];
-    bf16x8 qf[KS][NS];
+    bf16x8 qf[CT][KS][NS];
     auto pages_of = [&](const Place& p) {
       return tile_pages<BIG>(a, a.block_table + p.r * a.table_stride, p.tile, p.len);
     };
@@ -216,35 +224,44 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       for (int d = 0; d < DT; ++d)
         vr[d] = *reinterpret_cast<const u32x4*>(b + off + (d << (lg + 4)));
     };
-    // the queries of the next unit, on their way while this one's last tiles are
-    // computed, and their operands once they are needed
-    Vec8<IO> qr[KS];
+    // the queries of a unit, on their way while another's last tiles are computed,
+    // and their operands once they are needed
+    Vec8<IO> qr[CT][KS];
     auto load_q = [&](const Place& p) {
-      const IO* qp = static_cast<const IO*>(a.q) + (p.tok0 + i / group) * a.q_tok +
-                     (static_cast<int64_t>(p.head) * group + i % group) * a.q_head + 16 * g;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        qr[s] = Vec8<IO>{};
-        if (i < p.queries * group) qr[s].load(qp + 64 * (s >> 1) + 8 * (s & 1));
+      for (int n = 0; n < CT; ++n) {
+        const int col = 16 * n + i;
+        const IO* qp = static_cast<const IO*>(a.q) + (p.tok0 + col / group) * a.q_tok +
+                       (static_cast<int64_t>(p.head) * group + col % group) * a.q_head + 16 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          qr[n][s] = Vec8<IO>{};
+          if (col < p.queries * group) qr[n][s].load(qp + 64 * (s >> 1) + 8 * (s & 1));
+        }
       }
     };
     auto set_q = [&]() {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        float x[8];
+      for (int n = 0; n < CT; ++n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = qr[s].get(e);
-        parts<NS>(x, qf[s]);
-      }
+        for (int s = 0; s < KS; ++s) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = qr[n][s].get(e);
+          parts<NS>(x, qf[n][s]);
+        }
     };
 
-    f32x4 o[DT];
-    float m, l;
+    f32x4 o[CT][DT];
+    float m[CT], l[CT];
     auto clear = [&]() {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      m = AT_NEG;
-      l = 0.0f;
+      for (int n = 0; n < CT; ++n) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[n][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        m[n] = AT_NEG;
+        l[n] = 0.0f;
+      }
     };
 
     Place next = cur, later = cur;
@@ -258,7 +275,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
     if (left > 1) {
       advance(a, limit, next);
       pg_next = pages_of(next);
-      if (next.tile == 0) load_q(next);
+      if (AHEAD && next.tile == 0) load_q(next);
     }
     clear();
     for (;;) {
@@ -273,75 +290,87 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
         advance(a, limit, later);
         pg_later = pages_of(later);
       }
-      f32x4 s[4];
+      f32x4 s[CT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < CT; ++n) s[n][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const u32x4 raw = kr[t][k >> 1];
           const bf16x8 kf = (k & 1) ? widen(raw[2], raw[3]) : widen(raw[0], raw[1]);
 #pragma unroll
-          for (int n = NS - 1; n >= 0; --n) s[t] = mfma16(kf, qf[k][n], s[t]);
+          for (int n = 0; n < CT; ++n)
+#pragma unroll
+            for (int e = NS - 1; e >= 0; --e) s[n][t] = mfma16(kf, qf[n][k][e], s[n][t]);
         }
       }
       const int run0 = cur.tile * AT_TILE + 16 * g;
       const int places = page >= 0 ? min(max(cur.len - run0, 0), 16) : 0;
       if (more) {
-        if (ends) set_q();
-        if (left > 2 && later.tile == 0) load_q(later);
+        if (ends) {
+          if (!AHEAD) load_q(next);
+          set_q();
+        }
+        if (AHEAD && left > 2 && later.tile == 0) load_q(later);
         load_k(next, pg_next);
         ks = run_scales(a, a.k_scale, pg_next, next.head);
         vs = run_scales(a, a.v_scale, pg_next, next.head);
       }
 
-      const int pos = cur.ahead + i / group;               // last token this column sees
-      float x[4][4];
-      float top = AT_NEG;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[t][r] = s[t][r] * c;
       // masks where a run is not whole or some column does not see all of it
-      if (__any(places < 16) || cur.tile * AT_TILE + AT_TILE - 1 > cur.ahead) {
-        const int lim = min(places, pos - run0 + 1);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (4 * t + r >= lim) x[t][r] = AT_NEG;
+      const bool mask = __any(places < 16) || cur.tile * AT_TILE + AT_TILE - 1 > cur.ahead;
+      if (mask) {
         // 0 * NaN: whatever lies past the end must not reach the product
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int e = 0; e < 4; ++e) vr[d][e] = keep_places(vr[d][e], e, places);
       }
+      bf16x8 pf[CT][2][NS];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int n = 0; n < CT; ++n) {
+        const int pos = cur.ahead + (16 * n + i) / group;  // last token this column sees
+        float x[4][4];
+        float top = AT_NEG;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) top = fmaxf(top, x[t][r]);
-      top = fmaxf(top, xor16(top, lane));
-      top = fmaxf(top, xor32(top, lane >> 5));
-      const float m_new = fmaxf(m, top);
-      const float base = m_new == AT_NEG ? 0.0f : m_new;    // nothing seen yet: 2^-inf = 0
-      if (__any(m_new > m)) {
-        const float f = __builtin_amdgcn_exp2f(m - base);
-        l *= f;
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= f;
-      }
-      m = m_new;
-      bf16x8 pf[2][NS];
+          for (int r = 0; r < 4; ++r) x[t][r] = s[n][t][r] * c;
+        if (mask) {
+          const int lim = min(places, pos - run0 + 1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float p[8];
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - base);
-          l += p[e];
-          p[e] *= v_scale;
+            for (int r = 0; r < 4; ++r)
+              if (4 * t + r >= lim) x[t][r] = AT_NEG;
         }
-        parts<NS>(p, pf[h]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = fmaxf(top, x[t][r]);
+        top = fmaxf(top, xor16(top, lane));
+        top = fmaxf(top, xor32(top, lane >> 5));
+        const float m_new = fmaxf(m[n], top);
+        const float base = m_new == AT_NEG ? 0.0f : m_new;  // nothing seen yet: 2^-inf = 0
+        if (__any(m_new > m[n])) {
+          const float f = __builtin_amdgcn_exp2f(m[n] - base);
+          l[n] *= f;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) o[n][d] *= f;
+        }
+        m[n] = m_new;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - base);
+            l[n] += p[e];
+            p[e] *= v_scale;
+          }
+          parts<NS>(p, pf[n][h]);
+        }
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
@@ -349,45 +378,54 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
         for (int h = 0; h < 2; ++h) {
           const bf16x8 vf = widen(vr[d][2 * h], vr[d][2 * h + 1]);
 #pragma unroll
-          for (int n = NS - 1; n >= 0; --n) o[d] = mfma16(vf, pf[h][n], o[d]);
+          for (int n = 0; n < CT; ++n)
+#pragma unroll
+            for (int e = NS - 1; e >= 0; --e) o[n][d] = mfma16(vf, pf[n][h][e], o[n][d]);
         }
       }
       if (more) load_v(next, pg_next);
 
       if (ends || !more) {
         // leave the unit: its columns are on lanes i of every g
-        l += xor16(l, lane);
-        l += xor32(l, lane >> 5);
         const int cols = cur.queries * group;
-        if (i < cols) {
+#pragma unroll
+        for (int n = 0; n < CT; ++n) {
+          const int col = 16 * n + i;
+          l[n] += xor16(l[n], lane);
+          l[n] += xor32(l[n], lane >> 5);
+          if (col >= cols) continue;
           if (from == 0 && ends) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(cur.tok0) + i / group) * a.Hq +
-                                                static_cast<int64_t>(cur.head) * group + i % group) * DH;
+            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+            IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(cur.tok0) + col / group) * a.Hq +
+                                                static_cast<int64_t>(cur.head) * group + col % group) * DH;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) Io<IO>::st(op, 16 * d + 4 * g + r, o[d][r] * inv);
+              for (int r = 0; r < 4; ++r) Io<IO>::st(op, 16 * d + 4 * g + r, o[n][d][r] * inv);
           } else {
             const int64_t slot = 2 * static_cast<int64_t>(wave) + (from == 0 ? 1 : 0);
             if (g == 0) {
-              ws.ml[(slot * 2) * nt + i] = m;
-              ws.ml[(slot * 2 + 1) * nt + i] = l;
+              ws.ml[(slot * 2) * nt + col] = m[n];
+              ws.ml[(slot * 2 + 1) * nt + col] = l[n];
             }
-            float* op = ws.o + (slot * nt + i) * DH;
+            float* op = ws.o + (slot * nt + col) * DH;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(op + 16 * d + 4 * g) = o[d];
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(op + 16 * d + 4 * g) = o[n][d];
           }
         }
-        if (from == 0 && !ends) {
-          // begun here, continued by the waves up to the one with its last tile
-          const long long last = at + per - 1 + (cur.tiles - 1 - cur.tile);
-          header = make_int4(static_cast<int>(last / per) - wave + 1, cur.tok0, cur.head, cols);
+        if (!(from == 0 && ends)) {
+          // the waves that share the unit: the list's places of its tiles by `per`
+          const long long begin = at - cur.tile, last = begin + cur.tiles - 1;
+          const int w0 = from == 0 ? wave : static_cast<int>(begin / per);
+          if (lane == (from == 0 ? 1 : 0))   // the lane that cleared it
+            ws.head[2 * wave + lane] =
+                make_int4(w0, static_cast<int>(last / per) - w0 + 1, cur.tok0, cur.head | cols << 16);
         }
         if (!more) break;
         clear();
         from = 0;
       }
+      ++at;
       cur = next;
       next = later;
       pg = pg_next;
@@ -395,25 +433,27 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       --left;
     }
   }
-  if (space && lane == 0) ws.head[wave] = header;
 }
 
 // ---------------------------------------------------------------- host
 hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* space) {
-  const int64_t cols = static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv);
-  const int nt = static_cast<int>(cols < AT_NARROW ? cols : AT_NARROW);
+  const int nt = narrow_columns(limit, static_cast<int64_t>(a.max_q) * (a.Hq / a.Hkv));
   const int64_t units = static_cast<int64_t>(a.R) * a.Hkv;
   const unsigned grid = space ? AN_GROUPS : static_cast<unsigned>((units + AT_T / 64 - 1) / (AT_T / 64));
   auto go = [&](auto big_pages, auto small_pages) {
     if ((1 << a.page_lg) >= AT_TILE) big_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
     else small_pages<<<grid, AT_T, 0, a.stream>>>(a, limit, space, nt);
   };
+  auto sets = [&](auto ct) {
+    constexpr int CT = decltype(ct)::value;
+    if (a.DH == 64) go(attn_narrow_kernel<bf16_t, 64, true, CT>, attn_narrow_kernel<bf16_t, 64, false, CT>);
+    else go(attn_narrow_kernel<bf16_t, 128, true, CT>, attn_narrow_kernel<bf16_t, 128, false, CT>);
+  };
   if (a.bf16) {
-    if (a.DH == 64) go(attn_narrow_kernel<bf16_t, 64, true>, attn_narrow_kernel<bf16_t, 64, false>);
-    else go(attn_narrow_kernel<bf16_t, 128, true>, attn_narrow_kernel<bf16_t, 128, false>);
+    if (nt <= 16) sets(std::integral_constant<int, 1>{}); else sets(std::integral_constant<int, 2>{});
   } else {
-    if (a.DH == 64) go(attn_narrow_kernel<float, 64, true>, attn_narrow_kernel<float, 64, false>);
-    else go(attn_narrow_kernel<float, 128, true>, attn_narrow_kernel<float, 128, false>);
+    if (a.DH == 64) go(attn_narrow_kernel<float, 64, true, 1>, attn_narrow_kernel<float, 64, false, 1>);
+    else go(attn_narrow_kernel<float, 128, true, 1>, attn_narrow_kernel<float, 128, false, 1>);
   }
   return hipGetLastError();
 }

@@ -1,9 +1,16 @@
 // attn_paged.hip -- which kernels a call of attention over the paged cache takes
-// (attn_paged.hpp): requests of up to AT_NARROW columns (queries times query
-// heads per K/V head) are bound by reading the cache, wider ones by the matrix
-// cores.  The lengths are on the device, so each kernel picks its requests
-// there; a call that cannot hold wide requests launches only the narrow one,
-// and a single request goes to the kernel that its largest width asks for.
+// (attn_paged.hpp): requests of few columns (queries times query heads per K/V
+// head) are bound by reading the cache, wider ones by the matrix cores.  The
+// lengths are on the device, so each kernel picks its requests there; a call
+// that cannot hold wide requests launches only the narrow kernel, and a single
+// request goes to the kernel that its largest width asks for.
+//
+// Up to 16 columns are narrow; in bf16 calls whose widest request has at most
+// 32, all are (two sets of 16 per wave): single tokens of 32 query heads on one
+// K/V head, or four tokens of 8.  32 columns over 64 x 8192 tokens of 8 K/V
+// heads of 128: 142 us there, 214 us as wide units, which are laid out for 128;
+// one request of 65536 tokens on one K/V head: 22 against 65 us.  fp32's
+// operands leave no registers for a second set.
 #include "attn_paged.hpp"
 
 namespace hyena {
@@ -13,17 +20,18 @@ struct AttnRoute {
   int limit;                 // a request of up to so many columns is narrow
 };
 
-static AttnRoute route_of(int64_t R, int64_t max_q, int64_t Hq, int64_t Hkv) {
+static AttnRoute route_of(int64_t R, int64_t max_q, int64_t Hq, int64_t Hkv, bool bf16) {
   AttnRoute r;
-  r.wide = max_q * (Hq / Hkv) > AT_NARROW;
-  r.limit = r.wide && R == 1 ? 0 : AT_NARROW;
+  const int64_t cols = max_q * (Hq / Hkv);
+  r.limit = bf16 && cols <= AT_NARROW2 ? AT_NARROW2 : AT_NARROW;
+  r.wide = cols > r.limit;
+  if (r.wide && R == 1) r.limit = 0;
   r.narrow = r.limit > 0;
   return r;
 }
 
 static size_t narrow_space_bytes(const AttnRoute& r, int64_t max_q, int64_t Hq, int64_t Hkv, int DH) {
-  const int64_t cols = max_q * (Hq / Hkv);
-  return r.narrow ? (narrow_bytes(cols < AT_NARROW ? cols : AT_NARROW, DH) + 15) / 16 * 16 : 0;
+  return r.narrow ? (narrow_bytes(narrow_columns(r.limit, max_q * (Hq / Hkv)), DH) + 15) / 16 * 16 : 0;
 }
 
 bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv) {
@@ -35,18 +43,18 @@ bool attn_paged_fits(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hk
 size_t attn_paged_workspace(int64_t R, int64_t max_q, int64_t max_pages, int page_lg, int64_t Hq,
                             int64_t Hkv, int DH) {
   if (short_table(max_pages, page_lg)) return 0;
-  const AttnRoute r = route_of(R, max_q, Hq, Hkv);
-  size_t wide = 0;
+  size_t most = 0;
   for (bool bf16 : {false, true}) {
+    const AttnRoute r = route_of(R, max_q, Hq, Hkv, bf16);
     const WideForm f = wide_form(max_q * (Hq / Hkv), DH, bf16);
-    const size_t n = wide_bytes(f.nt, f.waves, DH);
-    wide = r.wide && n > wide ? n : wide;
+    const size_t n = narrow_space_bytes(r, max_q, Hq, Hkv, DH) + (r.wide ? wide_bytes(f.nt, f.waves, DH) : 0);
+    most = n > most ? n : most;
   }
-  return narrow_space_bytes(r, max_q, Hq, Hkv, DH) + wide;
+  return most;
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a) {
-  const AttnRoute r = route_of(a.R, a.max_q, a.Hq, a.Hkv);
+  const AttnRoute r = route_of(a.R, a.max_q, a.Hq, a.Hkv, a.bf16);
   const bool split = !short_table(a.max_pages, a.page_lg);
   void* narrow = split && r.narrow ? a.workspace : nullptr;
   void* wide = split && r.wide ? static_cast<char*>(a.workspace) +
@@ -55,7 +63,7 @@ hipError_t launch_attn_paged(const AttnArgs& a) {
   hipError_t e = hipSuccess;
   if (r.wide) e = launch_attn_wide(a, r.limit, wide);
   if (e == hipSuccess && r.narrow) e = launch_attn_narrow(a, r.limit, narrow);
-  if (e == hipSuccess && split) e = launch_attn_join(a, narrow, wide);
+  if (e == hipSuccess && split) e = launch_attn_join(a, r.limit, narrow, wide);
   return e;
 }
 

@@ -30,6 +30,7 @@ constexpr float AT_NEG = -__builtin_inff();
 constexpr int AT_T = 256;                 // threads
 constexpr int AT_TILE = 64;               // cached tokens per tile
 constexpr int AT_NARROW = 16;             // columns up to which a request is narrow
+constexpr int AT_NARROW2 = 32;            // and in bf16 calls that hold no wider one
 
 // Request r: first query token, queries, cached tokens (each cut to what
 // exists).
@@ -157,20 +158,25 @@ inline bool short_table(int64_t max_pages, int page_lg) {
 constexpr int AN_GROUPS = 512;            // workgroups: two per CU, all resident
 constexpr int AN_WAVES = AN_GROUPS * (AT_T / 64);
 struct NarrowSpace {
-  int4* head;                // per wave: pieces of the unit that begins in it and ends elsewhere (0: none),
-                             // its first query token, K/V head, columns
+  int4* head;                // per slot: the unit's first wave, its pieces (0: none), its first query
+                             // token, K/V head and columns (from bit 16)
   float* ml;
   float* o;
 };
 __device__ __forceinline__ NarrowSpace narrow_space(void* p, int nt) {
   NarrowSpace s;
   s.head = static_cast<int4*>(p);
-  s.ml = reinterpret_cast<float*>(s.head + AN_WAVES);
+  s.ml = reinterpret_cast<float*>(s.head + 2 * AN_WAVES);
   s.o = s.ml + static_cast<size_t>(2 * AN_WAVES) * 2 * nt;
   return s;
 }
+// Columns per slot where requests of up to `limit` columns are narrow and the
+// call's widest has `cols`.
+inline int narrow_columns(int limit, int64_t cols) {
+  return static_cast<int>(cols < limit ? cols : limit);
+}
 inline size_t narrow_bytes(int64_t nt, int DH) {
-  return static_cast<size_t>(AN_WAVES) * (sizeof(int4) + 2 * 4 * (2 * nt + nt * DH));
+  return static_cast<size_t>(2 * AN_WAVES) * (sizeof(int4) + 4 * (2 * nt + nt * DH));
 }
 
 // Wide: a slot per piece and head.  Eight waves per CU hold wide_target pieces
@@ -223,6 +229,6 @@ hipError_t launch_attn_narrow(const AttnArgs& a, int limit, void* space);
 hipError_t launch_attn_wide(const AttnArgs& a, int limit, void* space);
 int64_t attn_wide_grid(int64_t R, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, const WideForm& f);
 // Adds up what either left (NULL: was not launched).
-hipError_t launch_attn_join(const AttnArgs& a, void* narrow, void* wide);
+hipError_t launch_attn_join(const AttnArgs& a, int limit, void* narrow, void* wide);
 
 }  // namespace hyena

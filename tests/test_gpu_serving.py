@@ -752,3 +752,22 @@ def test_graph_of_a_mixed_step():
         torch.cuda.synchronize()
         assert bits_equal(out, want), i
         check_attn(c, out, label=f"replay {i}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P,DH,Hq,Hkv,most", [(64, 128, 32, 1, 1), (16, 128, 8, 1, 4), (128, 64, 10, 1, 3), (32, 64, 34, 2, 1),
+                                              (64, 128, 6, 2, 10), (256, 64, 64, 2, 1), (64, 64, 8, 1, 5)])
+def test_attn_some_columns(P, DH, Hq, Hkv, most, dtype):
+    """Single tokens under many shared heads and a few tokens under some: 16 to 40 columns, requests
+    of one tile, of no token and of many pieces."""
+    old = [0, 5, 63, 64, 2000, 15, 0, 129, 640, 31]
+    new = [1, most, 1, most, most, 0, 1, 1, most, max(1, most - 1)]
+    c = attn_case(old, new, Hq, Hkv, DH, P, dtype, seed=P + Hq)
+    c["lens"][8] = 0
+    out = attend(c)
+    check_attn(c, out, label=f"P={P} DH={DH} Hq={Hq}/{Hkv} x{most} {dtype}")
+    assert bits_equal(out, attend(c))
+    one = attn_case([6000], [most], Hq, Hkv, DH, P, dtype, seed=P)
+    check_attn(one, attend(one), label="  one request")
+    short = attn_case([100, 0, 7], [most, 1, most], Hq, Hkv, DH, 64, dtype, seed=P, width=3)
+    check_attn(short, attend(short), label="  short tables")
