@@ -1,7 +1,8 @@
 // attn_join.hip -- the pieces of attention units added up (attn_paged.hpp):
 //     out = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p,   m = max m_p.
 // One launch for what both kernels left: its time is that of a launch and of
-// four dependent loads (4 us on an idle chip), the data is small.
+// four dependent loads (4 us on an idle chip); the data is small, 6 us for 64
+// tokens over 8192 of 8 heads.
 #include "attn_paged.hpp"
 
 namespace hyena {

@@ -56,8 +56,9 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
 }
 
 // Eight floats as NS bf16 parts: one rounding (NS = 1: bf16 queries are exact,
-// and P's 2^-9 per weight is below the output's own rounding), or three that
-// carry fp32 (NS = 3, fp32 activations).
+// and P's relative 2^-8 at most per weight, of either sign, is averaged over the
+// tokens and never above the output's own rounding), or three that carry fp32
+// (NS = 3, fp32 activations).
 template <int NS>
 __device__ __forceinline__ void parts(const float (&x)[8], bf16x8 (&p)[NS]) {
   if constexpr (NS == 1) {

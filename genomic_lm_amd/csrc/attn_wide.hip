@@ -2,6 +2,17 @@
 // (attn_paged.hpp): prefill chunks.  4 DH flops per column and cached token
 // against 2 DH bytes per cached token, so from some tens of columns on the
 // matrix cores and the softmax's vector work bound it.
+//
+// 4096 tokens at the end of 32768 of 32 heads of 128, bf16: 1.90 ms, 1.08
+// PFLOP/s of the 2.06 TFLOP under the mask; the library's square product of 16384
+// reaches 1.34 and one of 8192 1.20.  Power bounds both: with cache and queries
+// all zero, the same instructions take 1.83 ms where random ones took 2.25 (128
+// columns per unit then), and the product of 8192 runs at 1.72 PFLOP/s.  So what
+// counts is work per column: 256 columns to a unit widen and stage a tile for
+// twice as many (2.26 -> 2.13 ms), and O is rescaled only where a maximum rises by
+// more than AT_SLACK.  Scores of the next tile ahead of this one's softmax (2.29
+// ms), fixed orders of matrix and vector instructions (2.32 to 2.50) and
+// accumulators in the other register file (2.29) were slower than the plain order.
 #include "attn_paged.hpp"
 
 namespace hyena {
@@ -46,8 +57,8 @@ __device__ __forceinline__ void wave_scan3(int& x, int& y, int& z) {
 // Finds the work of item `item` among the requests of more than `lo` columns;
 // false if there is none.  Every thread of the workgroup
 // takes part.  splits: units of several pieces per head.  Each workgroup walks
-// all requests itself (two sums and a scan over them): a launch of its own for
-// that costs more at every R up to the limit.  Up to 64 requests each wave
+// all requests itself (two sums and a scan over them, of lengths that L2 holds)
+// instead of waiting for a launch that does it once.  Up to 64 requests each wave
 // does it alone, without a barrier; one request needs no scan.
 template <int NT, int W>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, AttnShared& sh,
@@ -199,10 +210,12 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
 // the second product, whose k index runs over tokens of one half the same way.
 //
 // A tile is read once per workgroup (16 bytes per thread and step), widened to
-// bf16 and kept in LDS for the four waves, in two buffers: tile t + 1 is in
-// flight from HBM while tile t is multiplied, and written to the other buffer
-// after it.  16-byte pieces of a row are permuted by the row's number so that
-// lanes on consecutive rows read different banks.
+// bf16 and kept in LDS for the W waves of 32 CW columns each, in two buffers:
+// tile t + 1, in flight from HBM since tile t - 1, is written to the other buffer
+// beside tile t's scores.  16-byte pieces of a row are permuted by the row's
+// number so that lanes on consecutive rows read different banks: 16-byte reads
+// run at 188 bytes a cycle and CU; V's rows, two of which span all banks, are
+// permuted by half their number (by their number: 123).
 constexpr float AT_SLACK = 8.0f;      // how far (log2) scores may pass the reference before O is rescaled
 
 template <typename IO, int DH, bool BIG, int CW, int W>

@@ -21,8 +21,11 @@
 // Scales are taken over finite values.
 //
 // Reads 2 DH (2 or 4) bytes per token and head and writes 2 DH: HBM bound for
-// chunks; for single tokens the writes to V are DH single bytes, each in a
-// line of its own, and the call is bound by their latency.
+// chunks (13624 tokens of 32 heads of 128, bf16: 79 us, 4.2 TB/s).  For single
+// tokens the writes to V are DH single bytes, each in a 64-byte row of its own,
+// and a row is what memory reads and writes for it: 128 tokens of 32 heads take
+// 10.8 us and move 36 MB out and 28 MB in for 3.1 MB of data.  The attention, for
+// which V lies so, reads every row thousands of times for that one write.
 #include "fp8.hpp"
 #include "serving.hpp"
 
@@ -274,7 +277,7 @@ struct Append {
 };
 
 // Four waves per SIMD for bf16 (128 VGPRs): 81 us against 86 us at three and 104
-// us at five (spills) for 13605 tokens of 32 heads of 128; fp32 would spill.
+// us at five (spills) for 13624 tokens of 32 heads of 128; fp32 would spill.
 template <typename IO, int DH>
 __global__ __launch_bounds__(KA_T, sizeof(IO) == 2 ? 4 : 2) void kv_append_kernel(KvPtr kp, KvPtr vp,
                                                          const int64_t* __restrict__ slots,

@@ -14,6 +14,11 @@
 // store for few.  A row lives in the registers of W waves, eight consecutive
 // columns per lane and step, so x and r are read with 16-byte loads and the
 // second reduction (the largest |y|) needs no second read.
+//
+// 32768 x 4096 bf16 with residual, e4m3 per 128 columns: 166 us, 5.7 TB/s of the
+// 944 MB it cannot do without (a 4 GiB copy: 4.75 TB/s counting both ways; three
+// of five bytes here are reads).  5000 x 1001 fp32: 17.7 us, 4.5 TB/s.  16 x
+// 4096: 4.2 us, a launch and the chain above.
 #include "fp8.hpp"
 #include "serving.hpp"
 
