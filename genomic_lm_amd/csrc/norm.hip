@@ -24,9 +24,14 @@
 
 namespace hyena {
 
-// Sum (or maximum of magnitude bits) over the W waves of a row.
-template <int W>
+// Sum (or maximum of magnitude bits) over the W waves of a row, or its LR lanes.
+template <int W, int LR>
 __device__ __forceinline__ float row_sum(float x, float* sh, int wave) {
+  if constexpr (LR < 64) {
+#pragma unroll
+    for (int o = 1; o < LR; o <<= 1) x += __shfl_xor(x, o);
+    return x;
+  }
   x = wave_sum(x);
   if constexpr (W == 1) return x;
   if ((threadIdx.x & 63) == 0) sh[wave] = x;
@@ -37,8 +42,13 @@ __device__ __forceinline__ float row_sum(float x, float* sh, int wave) {
   __syncthreads();
   return t;
 }
-template <int W>
+template <int W, int LR>
 __device__ __forceinline__ uint32_t row_max(uint32_t x, float* sh, int wave) {
+  if constexpr (LR < 64) {
+#pragma unroll
+    for (int o = 1; o < LR; o <<= 1) x = max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), o)));
+    return x;
+  }
   x = max64(x);
   if constexpr (W == 1) return x;
   if ((threadIdx.x & 63) == 0) sh[wave] = __uint_as_float(x);
@@ -53,18 +63,23 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, float* sh, int wave) {
   return t;
 }
 
+// W waves of LR = 64 lanes per row, or (W = NV = 1) 64 / LR rows per wave: rows of
+// 64 to 256 columns, such as a head's queries, would leave most of a wave idle
+// (262144 x 64 bf16 with residual, to bf16 87 and to e4m3 101 us that way, 22 and
+// 20 us with eight rows per wave; 262144 x 250 196 and 187, 119 and 113 with two).
 // OUT 0: y in the activations' type; 1: e4m3, one scale per row; 2: e4m3, one
 // scale per 128 columns (16 lanes).
-template <typename IO, int W, int NV, int OUT>
+template <typename IO, int W, int NV, int LR, int OUT>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
     const IO* x, int64_t x_stride, const IO* residual, int64_t residual_stride,
     const float* __restrict__ weight, float eps, IO* y, int64_t y_stride,
     uint8_t* __restrict__ q, float* __restrict__ q_scale, IO* residual_out,
     int64_t residual_out_stride, int64_t T, int D) {
   __shared__ float sh[W];
-  const int lane = threadIdx.x & 63;
+  static_assert(LR == 64 || (W == 1 && NV == 1), "several rows per wave: one step");
+  const int lane = threadIdx.x & (LR - 1);
   const int wave = W == 1 ? 0 : static_cast<int>(threadIdx.x >> 6);
-  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)
+  const int64_t row = W == 1 ? static_cast<int64_t>(blockIdx.x) * (256 / LR) + threadIdx.x / LR
                              : static_cast<int64_t>(blockIdx.x);
   if (row >= T) return;                 // W == 1 only; it has no barrier
   const IO* xr = x + row * x_stride;
@@ -91,7 +106,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(s[v][e], s[v][e], ss);
-  ss = row_sum<W>(ss, sh, wave);
+  ss = row_sum<W, LR>(ss, sh, wave);
   float inv;
   if (ss < 0x1p126f) {
     inv = rsqrtf(ss / static_cast<float>(D) + eps);
@@ -106,7 +121,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
         const float z = s[v][e] * 0x1p-64f;
         t = fmaf(z, z, t);
       }
-    t = row_sum<W>(t, sh, wave);
+    t = row_sum<W, LR>(t, sh, wave);
     inv = rsqrtf(t / static_cast<float>(D)) * 0x1p-64f;
   }
 
@@ -153,9 +168,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
     if constexpr (OUT == 1) {
 #pragma unroll
       for (int v = 1; v < NV; ++v) top[0] = top[v] > top[0] ? top[v] : top[0];
-      top[0] = row_max<W>(top[0], sh, wave);
+      top[0] = row_max<W, LR>(top[0], sh, wave);
 #pragma unroll
       for (int v = 1; v < NV; ++v) top[v] = top[0];
+    } else if constexpr (LR < 16) {
+      top[0] = row_max<W, LR>(top[0], sh, wave);           // the row is shorter than a group
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v) top[v] = max16(top[v]);
@@ -167,7 +184,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
       const float a = __uint_as_float(top[v]);
       const float scale = a > 0.0f ? a / FP8_MAX : 1.0f;     // NaN: 1, its codes say NaN
       if constexpr (OUT == 1) {
-        if (v == 0 && threadIdx.x == (W == 1 ? threadIdx.x & ~63u : 0u)) q_scale[row] = scale;
+        if (v == 0 && lane == 0 && wave == 0) q_scale[row] = scale;
       } else {
         if ((lane & 15) == 0 && c < D) q_scale[row * groups + (c >> 7)] = scale;
       }
@@ -196,9 +213,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
   }
 }
 
-template <typename IO, int W, int NV>
+template <typename IO, int W, int NV, int LR = 64>
 static void norm_out(const NormArgs& a) {
-  const unsigned grid = static_cast<unsigned>(W == 1 ? (a.T + 3) / 4 : a.T);
+  const unsigned grid = static_cast<unsigned>(W == 1 ? (a.T + 256 / LR - 1) / (256 / LR) : a.T);
   const unsigned block = W == 1 ? 256 : W * 64;
   auto go = [&](auto kernel) {
     kernel<<<grid, block, 0, a.stream>>>(
@@ -206,15 +223,18 @@ static void norm_out(const NormArgs& a) {
         a.weight, a.eps, static_cast<IO*>(a.y), a.y_stride, a.q, a.q_scale,
         static_cast<IO*>(a.residual_out), a.residual_out_stride, a.T, a.D);
   };
-  if (!a.q) go(add_rmsnorm_kernel<IO, W, NV, 0>);
-  else if (a.group == 0) go(add_rmsnorm_kernel<IO, W, NV, 1>);
-  else go(add_rmsnorm_kernel<IO, W, NV, 2>);
+  if (!a.q) go(add_rmsnorm_kernel<IO, W, NV, LR, 0>);
+  else if (a.group == 0) go(add_rmsnorm_kernel<IO, W, NV, LR, 1>);
+  else go(add_rmsnorm_kernel<IO, W, NV, LR, 2>);
 }
 
 template <typename IO>
 static void norm_rows(const NormArgs& a) {
   const int D = a.D;
-  if (D <= 512) norm_out<IO, 1, 1>(a);
+  if (D <= 64) norm_out<IO, 1, 1, 8>(a);
+  else if (D <= 128) norm_out<IO, 1, 1, 16>(a);
+  else if (D <= 256) norm_out<IO, 1, 1, 32>(a);
+  else if (D <= 512) norm_out<IO, 1, 1>(a);
   else if (D <= 1024) norm_out<IO, 1, 2>(a);
   else if (D <= 2048) norm_out<IO, 4, 1>(a);
   else if (D <= 4096) norm_out<IO, 4, 2>(a);

@@ -771,3 +771,37 @@ def test_attn_some_columns(P, DH, Hq, Hkv, most, dtype):
     check_attn(one, attend(one), label="  one request")
     short = attn_case([100, 0, 7], [most, 1, most], Hq, Hkv, DH, 64, dtype, seed=P, width=3)
     check_attn(short, attend(short), label="  short tables")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [1, 5, 8, 60, 64, 65, 72, 128, 130, 192, 255, 256, 257])
+def test_norm_short_rows(D, dtype):
+    """Rows that share a wave: counts that leave it part empty, and rows whose squares leave fp32, of
+    zeros and of NaN beside ordinary ones, which keep their bits."""
+    rng = np.random.default_rng(D)
+    w = tensor(1 + 0.1 * rng.standard_normal(D))
+    for T in (3, 31, 77, 1000):
+        x = tensor(rng.standard_normal((T, D)) * np.exp(rng.standard_normal((T, 1))), dtype)
+        r = tensor(rng.standard_normal((T, D)) * 8, dtype)
+        y, ro = G.add_rmsnorm(x, w, r)
+        check_norm(x, r, w, 1e-6, y, ro, dtype)
+        eights = {g: G.add_rmsnorm_fp8(x, w, r, group=g) for g in (0, 128)}
+        for g, (q, sc, ro8) in eights.items():
+            check_norm(x, r, w, 1e-6, None, ro8, dtype, q, sc, g)
+        odd = x.clone()
+        odd[1::5] = 1e30
+        odd[2::7] = float("nan")
+        same = torch.ones(T, dtype=torch.bool, device=dev())
+        same[1::5] = same[2::7] = False
+        y2, _ = G.add_rmsnorm(odd, w, r)
+        assert bits_equal(y2[same], y[same]) and y2[2::7].isnan().all()
+        huge = odd.clone()
+        huge[2::7] = 0
+        zero = r.clone()
+        zero[2::7] = 0
+        y3, ro3 = G.add_rmsnorm(huge, w, zero)
+        check_norm(huge, zero, w, 1e-6, y3, ro3, dtype)
+        for g, (q, sc, _) in eights.items():
+            q2, sc2, _ = G.add_rmsnorm_fp8(huge, w, zero, group=g)
+            assert bits_equal(q2.view(torch.uint8)[same], q.view(torch.uint8)[same]) and bits_equal(sc2[same], sc[same])
+            assert (q2.view(torch.uint8)[2::7] & 0x7F == 0).all() and (sc2[2::7] == 1).all()
