@@ -9,8 +9,8 @@
 // 32, all are (two sets of 16 per wave): single tokens of 32 query heads on one
 // K/V head, or four tokens of 8.  32 columns over 64 x 8192 tokens of 8 K/V
 // heads of 128: 142 us there, 214 us as wide units, which are laid out for 128;
-// one request of 65536 tokens on one K/V head: 22 against 65 us.  fp32's
-// operands leave no registers for a second set.
+// one request of 65536 tokens on one K/V head: 22 against 65 us.  fp32 heads
+// of 128 use 251 of 256 registers for one set, so fp32 keeps to 16.
 #include "attn_paged.hpp"
 
 namespace hyena {
