@@ -166,6 +166,8 @@ __device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, in
 template <typename IO, int DH, bool BIG, int CT>
 __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int limit, void* space, int nt) {
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
+  using PV = Second<NS>;
+  constexpr int TOP = PV::TOP;           // log2 of the largest weight
   constexpr int KH = DH / 64;            // 16-byte loads per K row and lane
   constexpr int KS = DH / 32;            // MFMA steps over the head dimension
   constexpr int DT = DH / 16;            // 16-row tiles of O^T
@@ -292,7 +294,8 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
       const bool more = left > 1;
       const float c = ks.at(g) * scale2;
       const int page = pg.at(g);
-      const float v_scale = page >= 0 ? vs.at(g) : 0.0f;
+      float lv, iv;                        // log2 of V's scale, its reciprocal (times 2^-TOP)
+      v_scale_of(vs.at(g), page, TOP, lv, iv);
       const bool ends = cur.tile + 1 == cur.tiles;
       if (left > 2) {
         later = next;
@@ -336,7 +339,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
 #pragma unroll
           for (int e = 0; e < 4; ++e) vr[d][e] = keep_places(vr[d][e], e, places);
       }
-      bf16x8 pf[CT][2][NS];
+      typename PV::Vec pf[CT][2][NS];
 #pragma unroll
       for (int n = 0; n < CT; ++n) {
         const int pos = cur.ahead + (16 * n + i) / group;  // last token this column sees
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) x[t][r] = s[n][t][r] * c;
+          for (int r = 0; r < 4; ++r) x[t][r] = fmaf(s[n][t][r], c, lv);
         if (mask) {
           const int lim = min(places, pos - run0 + 1);
 #pragma unroll
@@ -369,27 +372,29 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
           for (int d = 0; d < DT; ++d) o[n][d] *= f;
         }
         m[n] = m_new;
+        const float from_base = base - TOP;
+        float sum = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float p[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - base);
-            l[n] += p[e];
-            p[e] *= v_scale;
+            p[e] = __builtin_amdgcn_exp2f(x[2 * h + (e >> 2)][e & 3] - from_base);
+            sum += p[e];
           }
-          parts<NS>(p, pf[n][h]);
+          PV::weights(p, pf[n][h]);
         }
+        l[n] = fmaf(sum, iv, l[n]);
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const bf16x8 vf = widen(vr[d][2 * h], vr[d][2 * h + 1]);
+          const auto vf = PV::widen(vr[d][2 * h], vr[d][2 * h + 1]);
 #pragma unroll
           for (int n = 0; n < CT; ++n)
 #pragma unroll
-            for (int e = NS - 1; e >= 0; --e) o[n][d] = mfma16(vf, pf[n][h][e], o[n][d]);
+            for (int e = NS - 1; e >= 0; --e) o[n][d] = PV::mul(vf, pf[n][h][e], o[n][d]);
         }
       }
       if (more) load_v(next, pg_next);
@@ -404,7 +409,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
           l[n] += xor32(l[n], lane >> 5);
           if (col >= cols) continue;
           if (from == 0 && ends) {
-            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+            const float inv = l[n] == 0.0f ? 0.0f : ldexpf(1.0f, -TOP) / l[n];
             IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(cur.tok0) + col / group) * a.Hq +
                                                 static_cast<int64_t>(cur.head) * group + col % group) * DH;
 #pragma unroll
@@ -419,7 +424,7 @@ __global__ __launch_bounds__(AT_T, 2) void attn_narrow_kernel(AttnArgs a, int li
             }
             float* op = ws.o + (slot * nt + col) * DH;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(op + 16 * d + 4 * g) = o[n][d];
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(op + 16 * d + 4 * g) = o[n][d] * ldexpf(1.0f, -TOP);
           }
         }
         if (!(from == 0 && ends)) {

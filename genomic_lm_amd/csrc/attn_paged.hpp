@@ -7,7 +7,7 @@
 // queries being the last of them; query head h reads K/V head h / G.  With c =
 // scale * k_scale * log2 e per block and query i at position
 // pos = lens - (queries) + i,
-//     s_j = c q.k_j (j <= pos),  m = max s,  l = sum 2^(s_j - m),
+//     s_j = c q.k_j (j <= pos),  m = max (s_j + log2 v_scale),  l = sum 2^(s_j - m),
 //     o = sum 2^(s_j - m) v_scale v_j / l,   0 where no token is seen.
 //
 // The columns of the matrix products are (query, query head of the group)
@@ -15,8 +15,8 @@
 // S^T = K Q^T puts tokens on the rows: a lane then holds 16 consecutive
 // tokens of one column, the softmax of a column is its registers and one or
 // two lane exchanges, and the result is already the operand of O^T = V^T P^T.
-// V is stored transposed for that product.  e4m3 values are exact in bf16, so
-// codes are widened in registers and the block scales are applied to S and P.
+// V is stored transposed for that product.  e4m3 values are exact in bf16 and
+// fp16, so codes are widened in registers and the block scales are applied to S and P.
 #pragma once
 
 #include "fp8.hpp"
@@ -55,10 +55,8 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// Eight floats as NS bf16 parts: one rounding (NS = 1: bf16 queries are exact,
-// and P's relative 2^-8 at most per weight, of either sign, is averaged over the
-// tokens and never above the output's own rounding), or three that carry fp32
-// (NS = 3, fp32 activations).
+// Eight floats as NS bf16 parts: one (bf16 queries, exact), or three that carry
+// fp32 (fp32 queries and the weights of fp32 calls).
 template <int NS>
 __device__ __forceinline__ void parts(const float (&x)[8], bf16x8 (&p)[NS]) {
   if constexpr (NS == 1) {
@@ -80,6 +78,69 @@ __device__ __forceinline__ void parts(const float (&x)[8], bf16x8 (&p)[NS]) {
     p[1] = __builtin_bit_cast(bf16x8, w1);
     p[2] = __builtin_bit_cast(bf16x8, w2);
   }
+}
+
+// Operands of the second product O^T = V^T P^T: V's codes widened, and the weights
+// P = 2^(s + log2 v_scale - reference + an offset) in
+// * bf16 calls: fp16 of both, one MFMA at bf16's rate.  The codes are exact in it
+//   and a weight keeps 11 bits, so its rounding (2^-11 at most) is an eighth of
+//   the output's own.  In bf16, with 8 bits, it was as large: a 4096-token chunk
+//   at the end of 32768 was 0.0023 off where 32-bit weights and these are 0.0017
+//   off, and a row that one weight carries by up to 2^-8, for 1.91 ms instead
+//   of 1.98.  Calls bound by the cache take the same time with either.  The offset
+//   puts the largest weight near 2^AT_TOP; one below 2^-14 keeps 2^-25 absolutely,
+//   2^-32 and less of the largest (v_scale included), far below e4m3's own step;
+// * fp32 calls: three bf16 parts of P, without an offset.
+// The divisor sums the weights in fp32, unrounded, with v_scale taken out again.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+constexpr int AT_TOP = 15;                // log2 of the largest fp16 weight
+template <int NS> struct Second;
+template <> struct Second<1> {
+  typedef f16x8 Vec;
+  static constexpr int TOP = AT_TOP;
+  static __device__ __forceinline__ Vec widen(uint32_t lo, uint32_t hi) {
+    Vec r;
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+    r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+    return r;
+  }
+  static __device__ __forceinline__ void weights(const float (&x)[8], Vec (&p)[1]) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f32x2 v = {x[2 * e], x[2 * e + 1]};
+      w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+    }
+    p[0] = __builtin_bit_cast(Vec, w);
+  }
+  static __device__ __forceinline__ f32x16 mul(Vec a, Vec b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mul(Vec a, Vec b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct Second<3> {
+  typedef bf16x8 Vec;
+  static constexpr int TOP = 0;
+  static __device__ __forceinline__ Vec widen(uint32_t lo, uint32_t hi) { return hyena::widen(lo, hi); }
+  static __device__ __forceinline__ void weights(const float (&x)[8], Vec (&p)[3]) { parts<3>(x, p); }
+  static __device__ __forceinline__ f32x16 mul(Vec a, Vec b, f32x16 c) { return mfma(a, b, c); }
+  static __device__ __forceinline__ f32x4 mul(Vec a, Vec b, f32x4 c) { return mfma16(a, b, c); }
+};
+
+// log2 of a block's V scale and its reciprocal times 2^-top; -inf and 0 where
+// there is no page.  A scale of 0 (a cache that was cleared and not written)
+// counts as the smallest one.
+__device__ __forceinline__ void v_scale_of(float v, int page, int top, float& lv, float& iv) {
+  v = fmaxf(v, FP8_MIN_SCALE);
+  lv = page >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
+  iv = page >= 0 ? ldexpf(__builtin_amdgcn_rcpf(v), -top) : 0.0f;
 }
 
 // Codes of places >= n of the four in word `at` (places 4 at .. 4 at + 3) to 0.

@@ -3,8 +3,8 @@
 // against 2 DH bytes per cached token, so from some tens of columns on the
 // matrix cores and the softmax's vector work bound it.
 //
-// 4096 tokens at the end of 32768 of 32 heads of 128, bf16: 1.90 to 1.97
-// ms by card, 1.08 PFLOP/s of the 2.06 TFLOP under the mask; the library's square product of 16384
+// 4096 tokens at the end of 32768 of 32 heads of 128, bf16: 1.98 ms,
+// 1.04 PFLOP/s of the 2.06 TFLOP under the mask; the library's square product of 16384
 // reaches 1.34 and one of 8192 1.20.  Power bounds both: with cache and queries
 // all zero, the same instructions take 1.83 ms where random ones took 2.25 (128
 // columns per unit then), and the product of 8192 runs at 1.72 PFLOP/s.  So what
@@ -223,6 +223,8 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
   constexpr int THREADS = 64 * W;
   constexpr int WNT = 32 * CW * W;       // columns per unit
   constexpr int NS = sizeof(IO) == 2 ? 1 : 3;
+  using PV = Second<NS>;
+  constexpr int TOP = PV::TOP ? PV::TOP - static_cast<int>(AT_SLACK) : 0;   // of a weight at the reference
   constexpr int KS = DH / 16;            // MFMA steps over the head dimension
   constexpr int DT = DH / 32;            // 32-row tiles of O^T
   constexpr int KC = DH / 8;             // 16-byte pieces of a K row in LDS
@@ -374,8 +376,8 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
     for (int u = 0; u < STEPS; ++u) {
       const int d = vd + VROWS * u;
       u32x4* vdst = s_v[buf] + d * 8;
-      vdst[(2 * vc) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][0], rv[u][1]));
-      vdst[(2 * vc + 1) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, widen(rv[u][2], rv[u][3]));
+      vdst[(2 * vc) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, PV::widen(rv[u][0], rv[u][1]));
+      vdst[(2 * vc + 1) ^ ((d >> 1) & 7)] = __builtin_bit_cast(u32x4, PV::widen(rv[u][2], rv[u][3]));
     }
   };
 
@@ -413,21 +415,20 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
   };
 
   // scales of this lane's two runs of the tile in work: of the scores, log2 and
-  // reciprocal of V's
+  // reciprocal of V's (times 2^-TOP)
   float c[2], vl[2], iv[2];
-  // masks of a tile's scores, the columns' maxima, and O moved to a new
-  // reference where one has risen by more than AT_SLACK
+  // masks of a tile's scores, the columns' maxima (of s + log2 v_scale, what the
+  // weights hold), and O moved to a new reference where one has risen by more
+  // than AT_SLACK
   auto judge = [&](int tile, f32x16 (&s)[CW][2], const TileInfo& t) {
     int places[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int p = t.page.at(2 * h + hf);
-      const float v = t.vs.at(2 * h + hf);
       places[h] = p >= 0 ? min(w.len - (tile * AT_TILE + 32 * h + 16 * hf), 16) : 0;
       // above 0 (and no NaN where there is no page): a masked score stays -inf
       c[h] = fmaxf(t.ks.at(2 * h + hf) * scale2, 0x1p-126f);
-      vl[h] = p >= 0 ? __builtin_amdgcn_logf(v) : AT_NEG;
-      iv[h] = p >= 0 ? __builtin_amdgcn_rcpf(v) : 0.0f;
+      v_scale_of(t.vs.at(2 * h + hf), p, TOP, vl[h], iv[h]);
     }
     if (__any(places[0] < 16 || places[1] < 16) || tile * AT_TILE + AT_TILE - 1 > first_pos) {
 #pragma unroll
@@ -450,7 +451,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
         float x = s[b][h][0];
 #pragma unroll
         for (int r = 1; r < 16; ++r) x = fmaxf(x, s[b][h][r]);
-        top[b] = fmaxf(top[b], x * c[h]);
+        top[b] = fmaxf(top[b], fmaf(x, c[h], vl[h]));
       }
       top[b] = fmaxf(top[b], xor32(top[b], hf));
       risen |= top[b] > m[b] + AT_SLACK;
@@ -470,19 +471,19 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
     }
   };
 
-  // P = 2^(c s + log2 v_scale - m), its sums, and O^T += V^T P^T
+  // P = 2^(c s + log2 v_scale - m + TOP), its sums, and O^T += V^T P^T
   auto weigh = [&](int buf, const f32x16 (&s)[CW][2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float off[CW], sum[CW];
 #pragma unroll
       for (int b = 0; b < CW; ++b) {
-        off[b] = vl[h] - (m[b] == AT_NEG ? 0.0f : m[b]);
+        off[b] = vl[h] - (m[b] == AT_NEG ? 0.0f : m[b] - TOP);
         sum[b] = 0.0f;
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        bf16x8 pf[CW][NS];
+        typename PV::Vec pf[CW][NS];
 #pragma unroll
         for (int b = 0; b < CW; ++b) {
           float p[8];
@@ -491,17 +492,17 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
             p[e] = __builtin_amdgcn_exp2f(fmaf(s[b][h][8 * q + e], c[h], off[b]));
             sum[b] += p[e];
           }
-          parts<NS>(p, pf[b]);
+          PV::weights(p, pf[b]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const int row = 32 * d + i;
-          const bf16x8 vf =
-              __builtin_bit_cast(bf16x8, s_v[buf][row * 8 + ((4 * h + 2 * hf + q) ^ ((row >> 1) & 7))]);
+          const auto vf =
+              __builtin_bit_cast(typename PV::Vec, s_v[buf][row * 8 + ((4 * h + 2 * hf + q) ^ ((row >> 1) & 7))]);
 #pragma unroll
           for (int b = 0; b < CW; ++b)
 #pragma unroll
-            for (int n = NS - 1; n >= 0; --n) o[b][d] = mfma(vf, pf[b][n], o[b][d]);
+            for (int n = NS - 1; n >= 0; --n) o[b][d] = PV::mul(vf, pf[b][n], o[b][d]);
         }
       }
 #pragma unroll
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
     if (w.pieces == 1) {
       IO* op = static_cast<IO*>(a.out) + ((static_cast<int64_t>(w.tok0) + qi[b]) * a.Hq +
                                           static_cast<int64_t>(head) * group + qh[b]) * DH;
-      const float inv = l[b] == 0.0f ? 0.0f : 1.0f / l[b];
+      const float inv = l[b] == 0.0f ? 0.0f : ldexpf(1.0f, -TOP) / l[b];
       // rows 8 e + 4 hf .. + 3 of each 32
 #pragma unroll
       for (int d = 0; d < DT; ++d)
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<f32x4*>(op + 32 * d + 8 * e + 4 * hf) =
-              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]};
+              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]} * ldexpf(1.0f, -TOP);
     }
   }
   if (w.pieces > 1 && tid == 0 && w.piece == 0)

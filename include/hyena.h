@@ -567,7 +567,7 @@ hyena_status_t hyena_kv_append_fp8(const void* k, int64_t k_tok_stride, int64_t 
  *   cu (R + 1), lens (R) : int32
  *   max_q : no request has more queries (rows past it are not written)
  * Rows of q past cu[R] are not read, nor written in out.  Softmax statistics
- * and sums are fp32; for bf16 activations the weights are rounded to bf16 for
+ * and sums are fp32; for bf16 activations the weights are rounded to 11 bits for
  * the second product, for fp32 both products carry fp32.  Nothing past a
  * request's length reaches the result, whatever the cache holds there.
  * Workspace (device, 16-byte aligned, no initial contents) of

@@ -1,0 +1,117 @@
+"""The serving operators at the edges of what they accept, against 64-bit formulas.
+
+Tolerances are stated with each test, before its first run."""
+import numpy as np
+import pytest
+import torch
+
+import genomic_lm_amd as G
+from tests import serving_ref as ref
+from tests.gpu_util import dev, log, to_f64
+from tests.test_gpu_serving import BF, F32, I32, attend, attn_case, codes, tensor
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    G.lib()
+    yield
+
+
+# ------------------------------------------------------------------ the weights of bf16 attention
+# (old, new, query heads, K/V heads): requests for the kernel of few columns, and of many
+COLUMNS = {"few": ([700, 130], [1, 2], 4, 2), "many": ([700, 130], [70, 33], 4, 2)}
+
+
+def set_codes(t, a):
+    t.view(torch.uint8).copy_(torch.from_numpy(np.ascontiguousarray(a)))
+
+
+@pytest.mark.parametrize("kind", ["sharp", "flat"])
+@pytest.mark.parametrize("DH,P", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("columns", list(COLUMNS))
+def test_attn_equal_values(columns, DH, P, kind):
+    """Where all values of a dimension are equal, their average is that value whatever the weights:
+    the result has no rounding of its own (e4m3 values times a power of two are bf16 values), so
+    weights that keep 11 bits, off by 2^-11 of their sum at most, must give it back exactly (the
+    nearest bf16 values lie 2^-8 of it away, the halfway points 2^-9).  sharp: scores far apart, few
+    tokens carry a row.  flat: one token above all others, which have one weight that is
+    anything but a power of two, so their rounding has one sign."""
+    old, new, Hq, Hkv = COLUMNS[columns]
+    c = attn_case(old, new, Hq, Hkv, DH, P, BF, seed=DH)
+    rng = np.random.default_rng(DH)
+    row = ref.encode(rng.uniform(0.5, 2.0, (Hkv, DH, 1)))
+    v = np.where(codes(c["v"]) == 0xFF, np.uint8(0xFF), row[None])
+    set_codes(c["v"], v)
+    c["vs"].fill_(2.0 ** -3)
+    scale = 1.0
+    if kind == "flat":
+        k = codes(c["k"]).copy()
+        k[k != 0x7F] = 0
+        for r in range(2):
+            k[int(c["table"][r, 0]), :, 0, 0] = 0x38        # 1.0 in the first token
+        set_codes(c["k"], k)
+        c["ks"].fill_(1.0)
+        c["q"] = tensor(rng.uniform(0.2, 2.5, to_f64(c["q"]).shape), BF)
+    out = to_f64(attend(c, scale=scale))
+    want = ref.decode(row)[:, :, 0] * 2.0 ** -3
+    want = np.repeat(want, Hq // Hkv, 0)[None]
+    e = np.abs(out - want) / want
+    log(f"  {columns} {kind} DH={DH}: {np.mean(e > 0):.4f} of the outputs off, at most {e.max():.2e}")
+    assert (out == want).all()
+
+
+@pytest.mark.parametrize("DH,P", [(64, 16), (128, 64), (128, 128)])
+@pytest.mark.parametrize("columns", list(COLUMNS))
+def test_attn_weights_keep_11_bits(columns, DH, P):
+    """As test_gpu_serving's attention tolerance, with 2^-11 for the weights' rounding in the place of
+    2^-8, and 2^-32 of the largest weight times its value scale for each small one (times codes
+    of up to 448)."""
+    old, new, Hq, Hkv = COLUMNS[columns]
+    for scale in (DH ** -0.5, 0.6):
+        c = attn_case(old, new, Hq, Hkv, DH, P, BF, seed=P)
+        want, mag, reach = ref.attention(to_f64(c["q"]), codes(c["k"]), codes(c["v"]), to_f64(c["ks"]),
+                                         to_f64(c["vs"]), c["table"].cpu().numpy(), c["lens"].cpu().numpy(),
+                                         c["cu"].cpu().numpy(), scale, P)
+        n = int(c["lens"].max())
+        weight = 2 * (DH + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + n * 2.0 ** -24
+        floor = n * 2.0 ** -32 * 448 * float(np.nanmax(to_f64(c["vs"])))
+        lim = mag * (weight + 2.0 ** -11) + floor + 2.0 ** -8 * np.abs(want) * 1.01
+        e = np.abs(to_f64(attend(c, scale=scale)) - want)
+        log(f"  {columns} DH={DH} P={P}: worst error / bound {(e / lim).max():.3f}, "
+            f"rms {np.sqrt(np.mean(e ** 2) / np.mean(want ** 2)):.2e}")
+        assert (e <= lim).all()
+
+
+@pytest.mark.parametrize("columns", list(COLUMNS))
+def test_attn_small_weights_add_up(columns):
+    """One token of value 0 in front, all others 2^-22 to 2^-20 of its weight: they alone make the result.
+    Such a weight keeps 2^-32 of the largest, so at least 2^-10 of itself; 2^-11 for the largest,
+    2^-8 of the value for the output's rounding, 2^-16 for scores, exponentials and sums."""
+    old, new, Hq, Hkv = COLUMNS[columns]
+    c = attn_case(old, new, Hq, Hkv, 64, 64, BF, seed=3)
+    k, v = codes(c["k"]).copy(), codes(c["v"]).copy()
+    k[k != 0x7F] = 0
+    v[v != 0xFF] = 0x38
+    for r in range(2):
+        p = int(c["table"][r, 0])
+        k[p, :, 0, 0] = 0x38
+        v[p, :, :, 0] = 0
+    set_codes(c["k"], k)
+    set_codes(c["v"], v)
+    c["ks"].fill_(1.0)
+    c["vs"].fill_(1.0)
+    rng = np.random.default_rng(4)
+    c["q"] = tensor(rng.uniform(20 * np.log(2), 21.9 * np.log(2), to_f64(c["q"]).shape), BF)
+    out = to_f64(attend(c, scale=1.0))
+    cu, lens = c["cu"].cpu().numpy(), c["lens"].cpu().numpy()
+    q0 = to_f64(c["q"])[:, :, 0]
+    others = np.concatenate([lens[r] - (cu[r + 1] - cu[r]) + np.arange(cu[r + 1] - cu[r]) for r in range(2)])
+    w = np.exp(-q0) * others[:, None]
+    want = (w / (1 + w))[..., None]
+    e = np.abs(out - want) / want
+    log(f"  {columns}: {e.max():.2e}")
+    assert (e <= 2.0 ** -10 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -16).all()
