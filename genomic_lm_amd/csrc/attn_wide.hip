@@ -311,7 +311,10 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
   float ahead_ks = 0.0f, ahead_vs = 0.0f;
   auto look_ahead = [&](int from) {
     ahead_from = from;
-    const int tok = (from + lane / RUNS) * AT_TILE + (lane % RUNS) * 16, j = tok >> lg;
+    // tiles past the request's last count as the one behind it: a table may hold
+    // all but 1024 of 2^31 tokens, and 64 tiles further would wrap
+    const int tile = min(from + lane / RUNS, (w.len + AT_TILE - 1) / AT_TILE);
+    const int tok = tile * AT_TILE + (lane % RUNS) * 16, j = tok >> lg;
     const int p = tok < w.len && j < a.max_pages ? table[j] : -1;
     ahead_page = p >= 0 && p < a.num_pages ? p : -1;
     const int64_t si = static_cast<int64_t>(max(ahead_page, 0)) * a.Hkv + head;

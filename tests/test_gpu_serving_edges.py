@@ -115,3 +115,26 @@ def test_attn_small_weights_add_up(columns):
     e = np.abs(out - want) / want
     log(f"  {columns}: {e.max():.2e}")
     assert (e <= 2.0 ** -10 + 2.0 ** -11 + 2.0 ** -8 + 2.0 ** -16).all()
+
+
+# ------------------------------------------------------------------ lengths and positions
+@pytest.mark.parametrize("Hq", [1, 40])
+def test_attn_longest_table(Hq):
+    """A table as long as one may be (all but 1024 of 2^31 tokens), the same page everywhere: the average
+    over it is the average over one page, for one column and for as many as share tiles.  The
+    sums are long: a lane adds up to 2^18 terms in fp32, each 2^-24 off at most, in the numerator and
+    in the divisor."""
+    P, DH = 64, 64
+    width = (2 ** 31 - 1 - 1024) // P
+    one = attn_case([P - 1], [1], Hq, 1, DH, P, BF, seed=5)
+    p = int(one["table"][0, 0])
+    want, mag, _ = ref.attention(to_f64(one["q"]), codes(one["k"]), codes(one["v"]), to_f64(one["ks"]),
+                                 to_f64(one["vs"]), np.array([[p]]), [P], [0, 1], DH ** -0.5, P)
+    c = dict(one)
+    c["table"] = torch.full((1, width), p, dtype=I32, device=dev())
+    c["lens"] = tensor(np.array([width * P]), I32)
+    log(f"  {width * P} tokens, {Hq} columns")
+    e = np.abs(to_f64(attend(c)) - want)
+    lim = mag * (2 * 2.0 ** -6 + 2.0 ** -11) + 2.0 ** -8 * np.abs(want) * 1.01
+    log(f"  worst error / bound {(e / lim).max():.3f}")
+    assert (e <= lim).all()
