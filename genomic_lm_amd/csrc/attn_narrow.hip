@@ -36,7 +36,7 @@ __device__ __forceinline__ int unit_tiles(int queries, int len, int group, int l
 }
 
 __device__ __forceinline__ void set_request(const AttnArgs& a, int limit, int r, Place& p) {
-  const int end = min(scalar(a.cu + r + 1), a.T);
+  const int end = min(max(scalar(a.cu + r + 1), 0), a.T);
   p.r = r;
   p.tok0 = max(scalar(a.cu + r), 0);
   p.queries = min(max(end - p.tok0, 0), a.max_q);

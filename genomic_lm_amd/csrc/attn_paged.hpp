@@ -33,9 +33,9 @@ constexpr int AT_NARROW = 16;             // columns up to which a request is na
 constexpr int AT_NARROW2 = 32;            // and in bf16 calls that hold no wider one
 
 // Request r: first query token, queries, cached tokens (each cut to what
-// exists).
+// exists; the end of the queries at 0 first, so that no difference wraps).
 __device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, int& queries, int& len) {
-  const int c0 = a.cu[r], c1 = min(a.cu[r + 1], a.T);
+  const int c0 = a.cu[r], c1 = min(max(a.cu[r + 1], 0), a.T);
   tok0 = max(c0, 0);
   queries = min(max(c1 - tok0, 0), a.max_q);
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_lg;

@@ -138,3 +138,21 @@ def test_attn_longest_table(Hq):
     lim = mag * (2 * 2.0 ** -6 + 2.0 ** -11) + 2.0 ** -8 * np.abs(want) * 1.01
     log(f"  worst error / bound {(e / lim).max():.3f}")
     assert (e <= lim).all()
+
+
+@pytest.mark.parametrize("most", [1, 40])
+def test_attn_offsets_that_descend(most):
+    """Query offsets that go back below 0 give no request queries: nothing is written."""
+    low = -2 ** 31
+    for cu in ([3, low], [4, low, 0], [5] + [low] * 70, [1, -1], [2 ** 31 - 1, low]):
+        R = len(cu) - 1
+        c = attn_case([300] * R, [1] * R, 4, 2, 64, 64, BF, seed=6)
+        c["q"] = c["q"][:1].expand(5, 4, 64).contiguous()
+        c["cu"] = torch.tensor(cu, dtype=I32, device=dev())
+        c["max_q"] = most
+        if R > 1:
+            c["cu"][2:] = 0                            # (a request of one's own would write its rows)
+        log(f"  {cu[:4]}, up to {most} queries")
+        out = torch.full_like(c["q"], 9.0)
+        attend(c, out=out)
+        assert (out == 9).all()
