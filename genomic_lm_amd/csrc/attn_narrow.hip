@@ -36,13 +36,12 @@ __device__ __forceinline__ int unit_tiles(int queries, int len, int group, int l
 }
 
 __device__ __forceinline__ void set_request(const AttnArgs& a, int limit, int r, Place& p) {
-  const int end = min(max(scalar(a.cu + r + 1), 0), a.T);
+  const Request q = request_of(a, scalar(a.cu + r), scalar(a.cu + r + 1), scalar(a.lens + r));
   p.r = r;
-  p.tok0 = max(scalar(a.cu + r), 0);
-  p.queries = min(max(end - p.tok0, 0), a.max_q);
-  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_lg;
-  p.len = static_cast<int>(min<int64_t>(max(scalar(a.lens + r), 0), cap));
-  p.ahead = p.len - (end - p.tok0);
+  p.tok0 = q.tok0;
+  p.queries = q.queries;
+  p.len = q.len;
+  p.ahead = q.ahead;
   p.tiles = unit_tiles(p.queries, p.len, a.Hq / a.Hkv, limit);
 }
 
@@ -69,9 +68,8 @@ __device__ __forceinline__ long long find_share(const AttnArgs& a, int limit, in
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int group = a.Hq / a.Hkv;
   auto weight = [&](int r) {
-    int t, q, n;
-    request_of(a, r, t, q, n);
-    return static_cast<long long>(unit_tiles(q, n, group, limit)) * a.Hkv;
+    const Request q = request_of(a, r);
+    return static_cast<long long>(unit_tiles(q.queries, q.len, group, limit)) * a.Hkv;
   };
   // With more than AN_PAIR columns two tiles at least: a piece of one tile would
   // write and read again as many bytes as the tile (1 x 65536 tokens of one head,

@@ -6,7 +6,7 @@
 // Request r owns query tokens cu[r] .. cu[r+1] and lens[r] cached tokens, its
 // queries being the last of them; query head h reads K/V head h / G.  With c =
 // scale * k_scale * log2 e per block and query i at position
-// pos = lens - (queries) + i,
+// pos = lens - (cu[r+1] - cu[r]) + i,
 //     s_j = c q.k_j (j <= pos),  m = max (s_j + log2 v_scale),  l = sum 2^(s_j - m),
 //     o = sum 2^(s_j - m) v_scale v_j / l,   0 where no token is seen.
 //
@@ -32,14 +32,28 @@ constexpr int AT_TILE = 64;               // cached tokens per tile
 constexpr int AT_NARROW = 16;             // columns up to which a request is narrow
 constexpr int AT_NARROW2 = 32;            // and in bf16 calls that hold no wider one
 
-// Request r: first query token, queries, cached tokens (each cut to what
-// exists; the end of the queries at 0 first, so that no difference wraps).
-__device__ __forceinline__ void request_of(const AttnArgs& a, int r, int& tok0, int& queries, int& len) {
-  const int c0 = a.cu[r], c1 = min(max(a.cu[r + 1], 0), a.T);
-  tok0 = max(c0, 0);
-  queries = min(max(c1 - tok0, 0), a.max_q);
-  const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_lg;
-  len = static_cast<int>(min<int64_t>(max(a.lens[r], 0), cap));
+// A request: first query token, queries, cached tokens, position of the first
+// query.  Queries past T or max_q and tokens past the table are not there; the
+// positions of the others do not depend on that, so they come from the offsets
+// and the length as given.  Tokens behind the last query's position are dropped
+// too: none sees them, and where queries are missing theirs may not have been
+// written.  A request without a query in the table counts as cut to it.
+struct Request {
+  int tok0, queries, len, ahead;
+};
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int c0, int c1, int lens) {
+  Request q;
+  q.tok0 = max(c0, 0);
+  const int brings = max(max(c1, 0) - q.tok0, 0);          // (the end at 0 first: no difference wraps)
+  q.queries = min(max(min(max(c1, 0), a.T) - q.tok0, 0), a.max_q);
+  const int cap = a.max_pages << a.page_lg;                // below 2^31
+  const int first = max(lens, 0) - brings;
+  q.ahead = first < cap ? first : cap - brings;
+  q.len = max(min(min(max(lens, 0), cap), q.ahead + q.queries), 0);
+  return q;
+}
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int r) {
+  return request_of(a, a.cu[r], a.cu[r + 1], a.lens[r]);
 }
 
 // ---------------------------------------------------------------- operands

@@ -81,24 +81,23 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
   };
 
   if (a.R == 1) {
-    int t, q, n;
-    request_of(a, 0, t, q, n);
-    const int u = units_of(q);
-    tiles = piece_tiles(static_cast<unsigned long long>(u) * tiles_of(n));
-    const int p = pieces_of(n);
+    const Request q = request_of(a, 0);
+    const int u = units_of(q.queries);
+    tiles = piece_tiles(static_cast<unsigned long long>(u) * tiles_of(q.len));
+    const int p = pieces_of(q.len);
     splits = p > 1 ? u : 0;
     if (item >= u * p) return false;
     w.r = w.slot = w.split = 0;
     at = item;
   } else if (a.R <= 64) {
-    int t, q = 0, n = 0;
-    if (lane < a.R) request_of(a, lane, t, q, n);
-    const int u = units_of(q);
-    unsigned long long work = static_cast<unsigned long long>(u) * tiles_of(n);
+    Request q{};
+    if (lane < a.R) q = request_of(a, lane);
+    const int u = units_of(q.queries);
+    unsigned long long work = static_cast<unsigned long long>(u) * tiles_of(q.len);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o);
     tiles = piece_tiles(work);
-    const int p = pieces_of(n), items = u * p, slots = p > 1 ? items : 0, split = p > 1 ? u : 0;
+    const int p = pieces_of(q.len), items = u * p, slots = p > 1 ? items : 0, split = p > 1 ? u : 0;
     int items_in = items, slots_in = slots, split_in = split;
     wave_scan3(items_in, slots_in, split_in);
     splits = __shfl(split_in, 63);
@@ -113,9 +112,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     const int r0 = min(tid * run, a.R), r1 = min(r0 + run, a.R);
     unsigned long long work = 0;
     for (int r = r0; r < r1; ++r) {
-      int t, q, n;
-      request_of(a, r, t, q, n);
-      work += static_cast<unsigned long long>(units_of(q)) * tiles_of(n);
+      const Request q = request_of(a, r);
+      work += static_cast<unsigned long long>(units_of(q.queries)) * tiles_of(q.len);
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) work += __shfl_xor(work, o);
@@ -128,9 +126,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     tiles = piece_tiles(work);
     int items = 0, slots = 0, split = 0;
     for (int r = r0; r < r1; ++r) {
-      int t, q, n;
-      request_of(a, r, t, q, n);
-      const int u = units_of(q), p = pieces_of(n);
+      const Request q = request_of(a, r);
+      const int u = units_of(q.queries), p = pieces_of(q.len);
       items += u * p;
       if (p > 1) {
         slots += u * p;
@@ -160,9 +157,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
     }
     if (item >= before && item < before + items) {
       for (int r = r0; r < r1; ++r) {
-        int t, q, n;
-        request_of(a, r, t, q, n);
-        const int u = units_of(q), p = pieces_of(n);
+        const Request q = request_of(a, r);
+        const int u = units_of(q.queries), p = pieces_of(q.len);
         if (item < before + u * p) {
           sh.found[0] = r;
           sh.found[1] = item - before;
@@ -189,11 +185,11 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
   w.r = uni(w.r);
   at = uni(at);
   w.tiles = uni(tiles);
-  request_of(a, w.r, w.tok0, w.queries, w.len);
-  w.tok0 = uni(w.tok0);
-  w.queries = uni(w.queries);
-  w.len = uni(w.len);
-  w.ahead = w.len - (min(scalar(a.cu + w.r + 1), a.T) - w.tok0);
+  const Request q = request_of(a, scalar(a.cu + w.r), scalar(a.cu + w.r + 1), scalar(a.lens + w.r));
+  w.tok0 = q.tok0;
+  w.queries = q.queries;
+  w.len = q.len;
+  w.ahead = q.ahead;
   w.pieces = uni(pieces_of(w.len));
   w.unit = uni(at / w.pieces);
   w.piece = at - w.unit * w.pieces;
@@ -262,8 +258,9 @@ __global__ __launch_bounds__(64 * W, 2) void attn_wide_kernel(AttnArgs a, int lo
     pos[b] = live[b] ? w.ahead + qi[b] : -1;
   }
   const int first_pos = uni(w.ahead + wc / group);           // of the wave's first column
-  const int wave_seen = wc < cols ? max(w.ahead + (min(wc + 32 * CW, cols) - 1) / group + 1, 0) : 0;
-  const int seen = max(w.ahead + (min(c0 + WNT, cols) - 1) / group + 1, 0);
+  auto seen_by = [&](int end) { return min(max(w.ahead + (min(end, cols) - 1) / group + 1, 0), w.len); };
+  const int wave_seen = wc < cols ? seen_by(wc + 32 * CW) : 0;
+  const int seen = seen_by(c0 + WNT);
   const int t_begin = w.piece * w.tiles;
   const int t_end = uni(min((seen + AT_TILE - 1) / AT_TILE, t_begin + w.tiles));
   const int t_wave = uni(min((wave_seen + AT_TILE - 1) / AT_TILE, t_end));

@@ -245,8 +245,9 @@ def attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu,
                    scale=None, out=None, workspace=None):
     """Causal attention of q (T, Hq, DH) over the paged cache, ragged requests:
     request r has query tokens cu[r] .. cu[r + 1] - 1 and lens[r] cached tokens,
-    the last of which are the queries' own.  max_q: no request has more queries.
-    scale defaults to 1 / sqrt(DH).  Returns out (T, Hq, DH)."""
+    the last of which are the queries' own; cu may run past T (the queries there are
+    left out), and rows of out past cu[R] are not written.  max_q: no request has
+    more queries.  scale defaults to 1 / sqrt(DH).  Returns out (T, Hq, DH)."""
     qp, qt, qh = _heads("q", q)
     T, Hq, DH = q.shape
     dev = q.get_device()

@@ -562,11 +562,15 @@ hyena_status_t hyena_kv_append_fp8(const void* k, int64_t k_tok_stride, int64_t 
  *   Hq a multiple of Hkv; query head h reads K/V head h / (Hq / Hkv)
  *   caches and scales : as hyena_kv_append_fp8 writes them, H = Hkv
  *   block_table : (R, max_pages) int32, row stride table_stride; entries out of
- *                 [0, num_pages) hide their tokens; lens beyond the table are
- *                 cut to it
+ *                 [0, num_pages) hide their tokens, and so does the table's
+ *                 end; the positions of the others stay.  (A request whose
+ *                 queries all stand past the end, pos >= max_pages * page_size,
+ *                 counts as if lens were cut to it.)
  *   cu (R + 1), lens (R) : int32
  *   max_q : no request has more queries (rows past it are not written)
- * Rows of q past cu[R] are not read, nor written in out.  Softmax statistics
+ * T may be less than cu[R] (hyena_page_map with a fixed T): the queries past it
+ * are not there, the others keep their positions and need no token behind
+ * them.  Rows of q past cu[R] are not read, nor written in out.  Softmax statistics
  * and sums are fp32; for bf16 activations the weights are rounded to 11 bits for
  * the second product, for fp32 both products carry fp32.  Nothing past a
  * request's length reaches the result, whatever the cache holds there.

@@ -156,3 +156,83 @@ def test_attn_offsets_that_descend(most):
         out = torch.full_like(c["q"], 9.0)
         attend(c, out=out)
         assert (out == 9).all()
+
+
+def by_formula(c, T, scale):
+    """out (T, Hq, DH) and its bound, row by row from the definition: query i of request r at position
+    lens[r] - (cu[r + 1] - cu[r]) + i sees the tokens up to there whose page the table holds.  For
+    requests that have a query within the table."""
+    q, kc, vc = to_f64(c["q"]), codes(c["k"]), codes(c["v"])
+    ks, vs = to_f64(c["ks"]), to_f64(c["vs"])
+    cu, lens, table, P = c["cu"].tolist(), c["lens"].tolist(), c["table"].tolist(), c["P"]
+    Hq, G = q.shape[1], q.shape[1] // kc.shape[1]
+    out, lim = np.zeros(q.shape), np.zeros(q.shape)
+    for r in range(len(lens)):
+        for t in range(cu[r], min(cu[r + 1], T)):
+            pos = lens[r] - (cu[r + 1] - cu[r]) + t - cu[r]
+            see = [(table[r][j // P], j % P) for j in range(pos + 1)
+                   if j // P < len(table[r]) and 0 <= table[r][j // P] < len(kc)]
+            if not see:
+                continue
+            p, o = np.array(see).T
+            for h in range(Hq):
+                K = ref.decode(kc[p, h // G, o]) * ks[p, h // G][:, None]
+                V = ref.decode(vc[p, h // G, :, o]) * vs[p, h // G][:, None]
+                s = K @ q[t, h] * scale
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                out[t, h] = w @ V
+                reach = (np.abs(K) @ np.abs(q[t, h])).max() * abs(scale)
+                rel = 2 * (q.shape[2] + 8) * 2.0 ** -24 * reach + 2.0 ** -21 + len(see) * 2.0 ** -24
+                half, weight = (2.0 ** -8, 2.0 ** -11) if c["dtype"] == BF else (2.0 ** -24, 2.0 ** -22)
+                floor = len(see) * 2.0 ** -32 * 448 * vs[p].max() if c["dtype"] == BF else 0.0
+                lim[t, h] = w @ np.abs(V) * (rel + weight) + floor + half * np.abs(out[t, h]) * 1.01
+    return out, lim
+
+
+def check_formula(c, T, label):
+    q = c["q"]
+    want, lim = by_formula(c, T, c["DH"] ** -0.5)
+    c = dict(c, q=q[:T].contiguous())
+    out = to_f64(attend(c))
+    e = np.abs(out - want[:T])
+    log(f"  {label} {c['dtype']}: worst error / bound {(e / np.maximum(lim[:T], 1e-300)).max():.3f}")
+    assert np.isfinite(out).all() and (e <= lim[:T] + 1e-30).all()
+
+
+# (old, new, T): the last request that has rows is cut by T
+CUT = {"few": ([90, 200, 30], [2, 4, 3], 4), "many": ([90, 200, 30], [20, 60, 5], 47),
+       "one": ([100], [90], 50), "requests": ([40] * 70, [1] * 60 + [30] * 10, 75)}
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", list(CUT))
+def test_attn_fewer_rows_than_queries(kind, dtype):
+    """T below cu[R], as after a page map with a fixed T: the queries that have rows keep their
+    positions, and the tokens of the others, which got places but were never appended, are not read
+    (their places hold NaN codes).  Tolerance: as the attention's with 11-bit weights."""
+    old, new, T = CUT[kind]
+    for P, DH, Hq, Hkv in ((16, 64, 4, 2), (64, 128, 2, 1)):
+        c = attn_case(old, new, Hq, Hkv, DH, P, dtype, seed=7)
+        k, v = codes(c["k"]).copy(), codes(c["v"]).copy()
+        cu, table = c["cu"].tolist(), c["table"].tolist()
+        for r in range(len(old)):
+            for t in range(max(cu[r], T), cu[r + 1]):
+                page, at = divmod(old[r] + t - cu[r], P)
+                k[table[r][page], :, at] = 0x7F
+                v[table[r][page], :, :, at] = 0x7F
+        set_codes(c["k"], k)
+        set_codes(c["v"], v)
+        check_formula(c, T, f"{kind} P={P}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("new", [2, 7, 40])
+def test_attn_chunk_past_the_table(new, dtype):
+    """A chunk that begins in its table and ends past it: its tokens in the table are seen where they
+    stand, the others are not there."""
+    for P, DH, Hq, Hkv, width in ((16, 64, 4, 2, 3), (64, 128, 2, 1, 2), (64, 64, 4, 1, 8)):
+        cap = P * width
+        c = attn_case([cap - 1, 5, cap - max(new // 2, 1)], [new, 1, new], Hq, Hkv, DH, P, dtype, seed=8)
+        c["table"] = c["table"][:, :width].contiguous()
+        check_formula(c, c["q"].shape[0], f"{new} new, table of {cap}")
