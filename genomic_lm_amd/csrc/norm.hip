@@ -107,23 +107,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(s[v][e], s[v][e], ss);
   ss = row_sum<W, LR>(ss, sh, wave);
-  float inv;
-  if (ss < 0x1p126f) {
-    inv = rsqrtf(ss / static_cast<float>(D) + eps);
-  } else {
-    // the squares leave fp32 (|s| around 1e18 and more, infinities, NaN): the
-    // same with the row scaled by 2^-64, which a finite row then survives
-    float t = 0.0f;
+  // Where the squares or eps leave fp32 (|s| around 1e18 and more): the same with
+  // the row scaled.  By 2^-96 every finite row's squares stay below 2^64 each.
+  float unit = 1.0f, eps_in = eps;
+  if (!(fmaxf(ss, eps) < 0x1p126f)) unit = 0x1p-96f;
+  if (unit != 1.0f) {
+    ss = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = s[v][e] * 0x1p-64f;
-        t = fmaf(z, z, t);
+        const float z = s[v][e] * unit;
+        ss = fmaf(z, z, ss);
       }
-    t = row_sum<W, LR>(t, sh, wave);
-    inv = rsqrtf(t / static_cast<float>(D)) * 0x1p-64f;
+    ss = row_sum<W, LR>(ss, sh, wave);
+    eps_in = eps * unit * unit;
   }
+  const float inv = rsqrtf(ss / static_cast<float>(D) + eps_in);
 
   if (residual_out) {
     IO* ro = residual_out + row * residual_out_stride;
@@ -132,6 +132,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
       const int c = ((v * W + wave) * 64 + lane) * 8;
       store8(ro + c, static_cast<int64_t>(D) - c, s[v]);
     }
+  }
+  if (unit != 1.0f) {                   // (not into inv, which would leave the normal range)
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[v][e] *= unit;
   }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {

@@ -467,8 +467,10 @@ size_t hyena_chunk_tokmajor_workspace_size(int64_t B, int64_t D, int64_t L, int6
  *   residual_out : T rows of D `io`, or NULL (not kept); may be residual or x
  *                  (rows of equal stride); needs a residual
  *   eps          : finite, >= 0
- * Rows whose squares leave fp32 (|s| ~ 1e18 and more) are scaled first; a NaN
- * or infinity makes its own row NaN.  D <= HYENA_MAX_NORM_DIM.
+ * Rows whose squares leave fp32 (|s| ~ 1e18 and more) are scaled first, up to
+ * the largest finite s.  A NaN makes its own row NaN; an infinity makes its own
+ * column NaN and the rest of its row 0, as the formula has it.
+ * D <= HYENA_MAX_NORM_DIM.
  */
 hyena_status_t hyena_add_rmsnorm(const void* x, int64_t x_stride, const void* residual,
                                  int64_t residual_stride, const float* weight, float eps, void* y,

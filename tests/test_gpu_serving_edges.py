@@ -8,7 +8,7 @@ import torch
 import genomic_lm_amd as G
 from tests import serving_ref as ref
 from tests.gpu_util import dev, log, to_f64
-from tests.test_gpu_serving import BF, F32, I32, attend, attn_case, codes, tensor
+from tests.test_gpu_serving import BF, F32, I32, attend, attn_case, check_norm, codes, tensor
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +236,39 @@ def test_attn_chunk_past_the_table(new, dtype):
         c = attn_case([cap - 1, 5, cap - max(new // 2, 1)], [new, 1, new], Hq, Hkv, DH, P, dtype, seed=8)
         c["table"] = c["table"][:, :width].contiguous()
         check_formula(c, c["q"].shape[0], f"{new} new, table of {cap}")
+
+
+# ------------------------------------------------------------------ norm
+def check_norms(x, r, w, eps, dtype):
+    """All three outputs, with the tolerances of test_gpu_serving."""
+    y, ro = G.add_rmsnorm(x, w, r, eps=eps)
+    check_norm(x, r, w, eps, y, ro, dtype)
+    for group in (0, 128):
+        q, sc, ro = G.add_rmsnorm_fp8(x, w, r, eps=eps, group=group)
+        check_norm(x, r, w, eps, None, ro, dtype, q, sc, group)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [8, 64, 200, 512, 1000, 2048, 4096, 8192, 32768])
+def test_norm_largest_rows(D, dtype):
+    """Finite rows up to the type's largest value, with and without a residual, and an eps that counts
+    beside them; an infinity by the formula: NaN in its column, 0 in the others."""
+    rng = np.random.default_rng(D)
+    sign = rng.choice([-1.0, 1.0], (6, D))
+    size = np.array([1e18, 1e19, 1e36, 1e37, 1e38, 3.3e38])[:, None]
+    x = tensor(sign * size * rng.uniform(0.25, 1.0, (6, D)), dtype)
+    w = tensor(1 + 0.1 * rng.standard_normal(D))
+    for eps in (1e-6, 3e38):
+        check_norms(x, None, w, eps, dtype)
+        check_norms(x[:5], x[:5].roll(1, 1), w, eps, dtype)
+    check_norms(tensor(rng.standard_normal((3, D)), dtype), None, None, 3.4e38, dtype)
+    x = tensor(rng.standard_normal((3, D)), dtype)
+    x[1, D // 2] = float("inf")
+    y, _ = G.add_rmsnorm(x, w)
+    want = torch.zeros(D, device=dev())
+    want[D // 2] = float("nan")
+    assert torch.equal(y[1].isnan(), want.isnan()) and (y[1].nan_to_num() == 0).all()
+    assert torch.isfinite(y[[0, 2]].float()).all()
+    q, sc, _ = G.add_rmsnorm_fp8(x, w, group=128)
+    c = codes(q)[1] & 0x7F
+    assert c[D // 2] == 0x7F and (np.delete(c, D // 2) == 0).all() and (sc[1] == 1).all()
