@@ -107,10 +107,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(s[v][e], s[v][e], ss);
   ss = row_sum<W, LR>(ss, sh, wave);
-  // Where the squares or eps leave fp32 (|s| around 1e18 and more): the same with
-  // the row scaled.  By 2^-96 every finite row's squares stay below 2^64 each.
+  // Where the squares or eps leave fp32 (|s| around 1e18 and more), or the squares
+  // fall below its normal range (|s| around 1e-17 and less) and eps does not cover
+  // them: the same with the row scaled.  By 2^-96 every finite row's squares stay
+  // below 2^64 each, by 2^96 those of the smallest values above 2^-106.
   float unit = 1.0f, eps_in = eps;
   if (!(fmaxf(ss, eps) < 0x1p126f)) unit = 0x1p-96f;
+  else if (ss < 0x1p-100f && eps < 0x1p-64f) unit = 0x1p96f;
   if (unit != 1.0f) {
     ss = 0.0f;
 #pragma unroll

@@ -467,8 +467,9 @@ size_t hyena_chunk_tokmajor_workspace_size(int64_t B, int64_t D, int64_t L, int6
  *   residual_out : T rows of D `io`, or NULL (not kept); may be residual or x
  *                  (rows of equal stride); needs a residual
  *   eps          : finite, >= 0
- * Rows whose squares leave fp32 (|s| ~ 1e18 and more) are scaled first, up to
- * the largest finite s.  A NaN makes its own row NaN; an infinity makes its own
+ * Rows whose squares leave fp32 (|s| ~ 1e18 and more, or 1e-17 and less with an
+ * eps that does not cover them) are scaled first: every finite row has its norm,
+ * but for zeros with eps = 0 (0 / 0).  A NaN makes its own row NaN; an infinity makes its own
  * column NaN and the rest of its row 0, as the formula has it.
  * D <= HYENA_MAX_NORM_DIM.
  */

@@ -272,3 +272,21 @@ def test_norm_largest_rows(D, dtype):
     q, sc, _ = G.add_rmsnorm_fp8(x, w, group=128)
     c = codes(q)[1] & 0x7F
     assert c[D // 2] == 0x7F and (np.delete(c, D // 2) == 0).all() and (sc[1] == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [1, 8, 64, 200, 512, 1000, 2048, 4096, 8192, 32768])
+def test_norm_smallest_rows(D, dtype):
+    """Rows whose squares fall out of fp32's range, down to its smallest values, with no eps or one
+    that does not cover them, beside rows that are not small; and with one that does."""
+    rng = np.random.default_rng(D)
+    sign = rng.choice([-1.0, 1.0], (9, D))
+    size = np.array([1.0, 1e-12, 1e-17, 1e-19, 1e-23, 1e-30, 1e-37, 1e-40, 2.0 ** -133])[:, None]
+    x = tensor(sign * size * rng.uniform(0.6, 1.0, (9, D)), dtype)
+    assert (x != 0).all()
+    w = tensor(1 + 0.1 * rng.standard_normal(D))
+    for eps in (0.0, 1e-45, 1e-38, 1e-30):
+        eps = float(np.float32(eps))
+        check_norms(x, None, w, eps, dtype)
+        check_norms(x, x.clone(), None, eps, dtype)
+    check_norms(x[:6], None, w, 1e-6, dtype)
