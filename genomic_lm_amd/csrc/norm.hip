@@ -6,7 +6,7 @@
 // 'blocks.N.projections').  Per row of D columns
 //     s = x + r,   y = s / sqrt(mean(s^2) + eps) * w,   r' = round(s)
 // and for the 8-bit output, over the row or over runs of `group` columns,
-//     scale = max|y| / 448 (1 where y is 0),   q = e4m3(y / scale).
+//     scale = max(max|y| / 448, 2^-140) (1 where y is 0),   q = e4m3(y / scale).
 // The norm reads the unrounded sum: y is rounded once.
 //
 // Every element is read once and written once, ~10 vector operations each:
@@ -191,7 +191,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void add_rmsnorm_kernel(
     for (int v = 0; v < NV; ++v) {
       const int c = ((v * W + wave) * 64 + lane) * 8;
       const float a = __uint_as_float(top[v]);
-      const float scale = a > 0.0f ? a / FP8_MAX : 1.0f;     // NaN: 1, its codes say NaN
+      // NaN: 1, its codes say NaN.  Not below 2^-140: a smaller quotient has too few
+      // bits, and y / scale could pass 464, e4m3's end, or be x / 0
+      const float scale = a > 0.0f ? fmaxf(a / FP8_MAX, 0x1p-140f) : 1.0f;
       if constexpr (OUT == 1) {
         if (v == 0 && lane == 0 && wave == 0) q_scale[row] = scale;
       } else {

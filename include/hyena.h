@@ -483,7 +483,7 @@ hyena_status_t hyena_add_rmsnorm(const void* x, int64_t x_stride, const void* re
  * hyena_add_rmsnorm_fp8 -- the same with y in e4m3 and scales, the form an
  * 8-bit in_proj takes (evo2_flash README, layer_names table:
  * 'blocks.N.projections').
- *   scale = max|y| / 448 over the run (1 where that is 0 or NaN),
+ *   scale = max|y| / 448 over the run, at least 2^-140 (1 where max|y| is 0 or NaN),
  *   q = e4m3(y / scale),  y ~ q * scale.
  *   q       : (T, D) e4m3, contiguous
  *   q_scale : fp32; group = 0: one run per row, (T); group = HYENA_NORM_GROUP:

@@ -290,3 +290,22 @@ def test_norm_smallest_rows(D, dtype):
         check_norms(x, None, w, eps, dtype)
         check_norms(x, x.clone(), None, eps, dtype)
     check_norms(x[:6], None, w, 1e-6, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 256, 1001])
+def test_norm_codes_of_subnormal_values(D):
+    """Weights that make y a number below fp32's normal range, down to its smallest: codes are numbers,
+    and code * scale is y within e4m3's rounding (2^-4 of the value, half a subnormal step: 2^-10 of the
+    scale) and fp32's there (2^-149, twice: y and the scale times 448)."""
+    rng = np.random.default_rng(D)
+    x = tensor(rng.standard_normal((4, D)), F32)
+    for size in (1.4e-45, 1e-44, 1e-43, 3e-43, 9e-43, 4e-42, 1e-40, 1e-38):
+        w = tensor(size * rng.uniform(0.5, 2.0, D))
+        _, want = ref.rmsnorm(to_f64(x), None, to_f64(w), 1e-6)
+        for group in (0, 128):
+            q, sc, _ = G.add_rmsnorm_fp8(x, w, eps=1e-6, group=group)
+            c, s = ref.decode(codes(q)), np.repeat(to_f64(sc).reshape(4, -1), group or D, 1)[:, :D]
+            assert np.isfinite(c).all() and (s >= 2.0 ** -140).all(), size
+            e = np.abs(c * s - want)
+            lim = 2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -8) + 2.0 ** -10 * s + 2 * 2.0 ** -149
+            assert (e <= lim).all(), (size, (e / lim).max())
