@@ -9,8 +9,9 @@
 //
 // For the tokens that a call writes into a block, a = their largest magnitude:
 //     s1 = 2^ceil(log2(a / 448)),   s = s1 in a fresh block, else max(s0, s1)
-// old codes times s0 / s, new codes e4m3(x / s).  A block is fresh when its
-// first place is written by the call.  Scales are powers of two: a block whose
+// old codes (those of the places before the lowest that the call writes) times
+// s0 / s, new codes e4m3(x / s).  A block is fresh when its first place is
+// written by the call.  Scales are powers of two: a block whose
 // scale grows is moved without a second rounding (only codes that fall below
 // e4m3's normal range lose bits), and a power of two costs a floating format
 // no precision.
@@ -83,7 +84,7 @@ struct Append {
   struct Run {
     int64_t t;                                     // first token
     int64_t blk;                                   // block of the cache
-    int n0, n;                                     // first place, tokens from the first to the last
+    int n0, n;                                     // lowest place, tokens from the first to the last
     bool straight;                                 // place n0 + j for token j
     const int64_t* slots;                          // of the run's tokens
     int64_t page0, pages;                          // first slot of the page, slots of the cache
@@ -349,6 +350,15 @@ __global__ __launch_bounds__(KA_T, sizeof(IO) == 2 ? 4 : 2) void kv_append_kerne
     u.blk = page * H + head;
     u.kb = kp.cache + u.blk * static_cast<int64_t>(P) * DH;
     u.vb = vp.cache + u.blk * static_cast<int64_t>(P) * DH;
+    if (!u.straight) {
+      // places in any order: the older codes are those before the lowest
+      int over = 0;                      // P - place
+      for (int j = lane; j < u.n; j += 64) {
+        const int at = u.place(j);
+        if (at >= 0) over = max(over, P - at);
+      }
+      u.n0 = P - static_cast<int>(max64(static_cast<uint32_t>(over)));
+    }
     if (u.n <= KA_SHORT) {
       if ((turn++ & (KA_T / 64 - 1)) == wave) A::by_wave(kp, vp, ks, vs, u, P);
     } else {

@@ -537,13 +537,13 @@ hyena_status_t hyena_page_map(const int32_t* old_lens, const int32_t* new_lens, 
  * Per block, with a = the largest finite magnitude of the tokens that the call
  * writes into it and s1 = 2^ceil(log2(a / 448)) (at least 2^-96): the scale
  * becomes s1 where the call writes place 0, else max(scale, s1), the codes of
- * the places before the first token's times old / new scale; new codes are
+ * the places before the lowest that it writes times old / new scale; new codes are
  * e4m3(x / scale).  A token with a non-finite key or value gets a NaN key and
  * zeros for its non-finite values: it makes NaN of the queries that see it and
  * of no others.
  * The tokens of one page must stand together in the call (as hyena_page_map
- * gives them), with fewer than 63 tokens without a slot between two of them,
- * each in a place of its own; two requests must not share a page that is
+ * gives them), in any order, with fewer than 63 tokens without a slot between
+ * two of them, each in a place of its own; two requests must not share a page that is
  * written.  DH 64 or 128.
  */
 hyena_status_t hyena_kv_append_fp8(const void* k, int64_t k_tok_stride, int64_t k_head_stride,

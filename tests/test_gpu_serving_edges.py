@@ -8,7 +8,8 @@ import torch
 import genomic_lm_amd as G
 from tests import serving_ref as ref
 from tests.gpu_util import dev, log, to_f64
-from tests.test_gpu_serving import BF, F32, I32, attend, attn_case, check_norm, codes, tensor
+from tests.test_gpu_serving import (BF, F32, I32, attend, attn_case, check_norm, codes, host_cache, random_cache,
+                                    tensor)
 
 pytestmark = pytest.mark.gpu
 
@@ -309,3 +310,66 @@ def test_norm_codes_of_subnormal_values(D):
             e = np.abs(c * s - want)
             lim = 2.0 ** -4 * np.abs(want) * (1 + 2.0 ** -8) + 2.0 ** -10 * s + 2 * 2.0 ** -149
             assert (e <= lim).all(), (size, (e / lim).max())
+
+
+# ------------------------------------------------------------------ append
+def append_by_page(k, v, slots, kc, vc, ks, vs, P):
+    """The header's formulas page by page, over all tokens of the call that a page takes, wherever they
+    stand in it and in whatever order; codes and scales are changed in place."""
+    pages = {}
+    for t, s in enumerate(slots.tolist()):
+        if 0 <= s < len(kc) * P:
+            pages.setdefault(s // P, []).append((t, s % P))
+    for page, tokens in pages.items():
+        t, o = np.array(tokens).T
+        low = o.min()
+        for h in range(k.shape[1]):
+            a, b = k[t, h], v[t, h]
+            for x, c, sc in ((a, kc[page, h], ks), (b, vc[page, h].T, vs)):
+                scale = ref.block_scale(np.abs(x).max())
+                if low > 0:
+                    scale = max(scale, sc[page, h])
+                    c[:low] = ref.encode(ref.decode(c[:low]) * (sc[page, h] / scale))
+                sc[page, h] = scale
+                c[o] = ref.encode(x / scale)
+
+
+def check_pages(slots, N, H, P, DH, dtype, seed, big=()):
+    """big: tokens whose values are larger than all others'."""
+    rng = np.random.default_rng(seed)
+    T = len(slots)
+    k, v = (rng.uniform(-1, 1, (T, H, DH)) for _ in range(2))
+    for t in big:
+        k[t], v[t] = k[t] * 40, v[t] * 90
+    k, v = tensor(k, dtype), tensor(v, dtype)
+    cache = random_cache(N, H, P, DH, seed)
+    for sc in cache[2:]:
+        sc[: N // 2] = float("nan")                # of pages never written: not read by a fresh block
+    want = host_cache(cache)
+    append_by_page(to_f64(k), to_f64(v), slots, *want, P)
+    G.kv_append_fp8(k, v, tensor(slots, torch.int64), *cache)
+    used = np.unique(slots[slots >= 0] // P)
+    for name, g, w in zip(("k_cache", "v_cache", "k_scale", "v_scale"), host_cache(cache), want):
+        for page in used:
+            assert (g[page] == w[page]).all(), (name, int(page), int((g[page] != w[page]).sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pad", [0, 4300])
+@pytest.mark.parametrize("P,DH", [(16, 64), (64, 128), (256, 64)])
+def test_append_places_in_any_order(P, DH, pad, dtype):
+    """A page's places from the last to the first, shuffled, and with place 0 in the middle, in fresh
+    pages (whose scales hold NaN) and in pages with older tokens, in runs of a wave's and of the
+    workgroup's size.  Exact."""
+    rng = np.random.default_rng(P + pad)
+    N = 16
+    old = N // 2                                   # pages from here on have a scale
+    n = min(P, 70)
+    here = [np.array([1, 0]), np.array([2, 0, 1]), np.arange(4)[::-1], rng.permutation(n), np.arange(n)[::-1],
+            np.concatenate([np.arange(5, n), np.arange(5)])]
+    late = [np.array([P - 1, P - 2]), 3 + rng.permutation(4), P - 1 - np.arange(min(P - 5, 66)),
+            5 + rng.permutation(P - 5)[:60]]
+    slots = np.concatenate([np.full(pad, -1)] + [i * P + o for i, o in enumerate(here)] +
+                           [(old + i) * P + o for i, o in enumerate(late)]).astype(np.int64)
+    big = rng.choice(np.arange(pad, len(slots)), 12, replace=False)
+    check_pages(slots, N, 2, P, DH, dtype, P, big)
