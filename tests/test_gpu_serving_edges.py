@@ -348,7 +348,7 @@ def check_pages(slots, N, H, P, DH, dtype, seed, big=()):
     want = host_cache(cache)
     append_by_page(to_f64(k), to_f64(v), slots, *want, P)
     G.kv_append_fp8(k, v, tensor(slots, torch.int64), *cache)
-    used = np.unique(slots[slots >= 0] // P)
+    used = np.unique(slots[(slots >= 0) & (slots < N * P)] // P)
     for name, g, w in zip(("k_cache", "v_cache", "k_scale", "v_scale"), host_cache(cache), want):
         for page in used:
             assert (g[page] == w[page]).all(), (name, int(page), int((g[page] != w[page]).sum()))
@@ -373,3 +373,25 @@ def test_append_places_in_any_order(P, DH, pad, dtype):
                            [(old + i) * P + o for i, o in enumerate(late)]).astype(np.int64)
     big = rng.choice(np.arange(pad, len(slots)), 12, replace=False)
     check_pages(slots, N, 2, P, DH, dtype, P, big)
+
+
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("gap", [1, 3, 32, 61, 62])
+def test_append_largest_value_after_a_gap(gap, long):
+    """Up to 62 tokens without a slot between two of one page, at every position against the 64 tokens
+    that are looked at together: one scale for all of the page's tokens, taken from the last of them, in
+    fresh pages and behind older tokens.  Exact."""
+    H, DH, P, N = 1, 64, 64, 40
+    rng = np.random.default_rng(gap)
+    none = [-1, -7, N * P, 1 << 40]
+    slots, big, fresh, held = [-1] * (4200 if long else 0), [], iter(range(N // 2)), iter(range(N // 2, N))
+    for i in range(36):
+        page, o = (next(fresh), 0) if i % 2 else (next(held), int(rng.integers(1, 20)))
+        before, after = (1, 1) if i < 12 else (int(rng.integers(1, 22)), int(rng.integers(1, 22)))
+        for at in range(before + after):
+            if at == before or (i >= 24 and at and rng.random() < 0.2):
+                slots += [none[int(x)] for x in rng.integers(0, 4, gap if at == before else 2)]
+            slots.append(page * P + o + at)
+        big.append(len(slots) - 1)
+        slots += [-1] * int(rng.integers(0, 9))
+    check_pages(np.array(slots, dtype=np.int64), N, H, P, DH, BF, gap, big)
