@@ -61,6 +61,13 @@ __global__ __launch_bounds__(PM_T) void page_map_kernel(
   auto cached = [&](int r) { return max(old_lens[r], 0); };
   auto brings = [&](int r, int o) { return min(max(new_lens[r], 0), 0x7FFFFFFF - o); };
 
+  // the page that request r's first new token shares with its last cached one, -1
+  // if the table holds none (an earlier step found no page for it); 0 if it begins one
+  auto shared_page = [&](int r, int o) {
+    const int j = o >> lg;
+    return (o & mask) && j < max_pages ? block_table[r * table_stride + j] : 0;
+  };
+
   // every thread sums its run of requests, then a scan over the threads
   const int run = (R + PM_T - 1) / PM_T;
   const int r0 = min(tid * run, R), r1 = min(r0 + run, R);
@@ -105,6 +112,7 @@ __global__ __launch_bounds__(PM_T) void page_map_kernel(
       const int64_t room = static_cast<int64_t>(have + got) << lg;
       const int64_t from = room > o ? room : o;
       if (o + n > from) unplaced = add_sat(unplaced, static_cast<int>(o + n - from));
+      if (n > 0 && shared_page(r, o) < 0) unplaced = add_sat(unplaced, min(n, mask + 1 - (o & mask)));
     }
     a = add_sat(a, n);
     b = add_sat(b, want - have);

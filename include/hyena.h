@@ -512,7 +512,8 @@ hyena_status_t hyena_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void
  *   positions    : (T) int32, written, or NULL;  slots : (T) int64, written
  *   status       : (2) int32, written: the free list's new head, and the count
  *                  of new tokens that found no page (free list or table at its
- *                  end; their slots are -1)
+ *                  end, or a part-filled page that an earlier step did not
+ *                  get; their slots are -1)
  * T is the size of positions and slots: entries past cu[R] get -1 (a fixed T
  * can be captured in a graph), tokens past T get none.  Outputs must not
  * overlap the inputs.  Negative lengths count as 0.  R <= HYENA_MAX_REQUESTS.

@@ -395,3 +395,35 @@ def test_append_largest_value_after_a_gap(gap, long):
         big.append(len(slots) - 1)
         slots += [-1] * int(rng.integers(0, 9))
     check_pages(np.array(slots, dtype=np.int64), N, H, P, DH, BF, gap, big)
+
+
+# ------------------------------------------------------------------ page map
+@pytest.mark.parametrize("R", [1, 5, 300])
+def test_page_map_after_a_shortage(R):
+    """Steps that go on after the free list ran out: status counts every new token whose slot is -1, those
+    in a part-filled page that the earlier step did not get among them.  Exact."""
+    rng = np.random.default_rng(R)
+    P, width = 16, 8
+    i32 = lambda a: tensor(np.array(a), I32)  # noqa: E731
+    table = torch.full((R, width), -1, dtype=I32, device=dev())
+    lens = torch.zeros(R, dtype=I32, device=dev())
+    free, head = i32(rng.permutation(3 * R)), i32([0])
+    lost = 0
+    for step in range(14):
+        new = rng.integers(0, 25 if step < 4 else 4, R)
+        new[0] = 9
+        T = int(new.sum())
+        cu, after, pos, slots, status = G.page_map(lens, i32(new), table, free, head, P, T)
+        want = np.full(T, -1)
+        t = 0
+        rows = table.cpu().numpy()
+        for r in range(R):
+            for p in range(int(lens[r]), int(after[r])):
+                if p // P < width and rows[r, p // P] >= 0:
+                    want[t] = rows[r, p // P] * P + p % P
+                t += 1
+        assert (slots.cpu().numpy() == want).all(), step
+        assert status.tolist() == [min(3 * R, int(status[0])), int((want < 0).sum())], step
+        lost += int(status[1])
+        lens, head = after, status[:1].clone()
+    assert lost > 0
