@@ -44,10 +44,10 @@ def _rows(name, t, like=None):
         if t.stride(1) == 1 or D == 1:
             return t.data_ptr(), t.stride(0)
     elif D == 1 or t.stride(-1) == 1:
-        step = t.stride(-2)
-        if all(t.shape[i] == 1 or t.stride(i) == t.stride(i + 1) * t.shape[i + 1]
-               for i in range(t.dim() - 2)):
-            return t.data_ptr(), step
+        # axes of one row have no say, such as the last token of each sequence, x[:, -1:]
+        axes = [(n, s) for n, s in zip(t.shape[:-1], t.stride()) if n != 1]
+        if all(s == s2 * n2 for (_, s), (n2, s2) in zip(axes, axes[1:])):
+            return t.data_ptr(), axes[-1][1] if axes else D
     raise ValueError(f"{name} must have a contiguous last axis and rows at one stride")
 
 

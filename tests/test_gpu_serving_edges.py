@@ -312,6 +312,22 @@ def test_norm_codes_of_subnormal_values(D):
             assert (e <= lim).all(), (size, (e / lim).max())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_rows_of_single_axes(dtype):
+    """Rows at one stride under axes of size one: the last token of each sequence, in and out."""
+    x = torch.randn((3, 7, 40), device=dev()).to(dtype)
+    want, _ = G.add_rmsnorm(x[:, -1].contiguous())
+    whole = torch.full_like(x, 9.0)
+    for a, b in ((x[:, -1:], whole[:, 2:3]), (x[:, -1:, None], whole[:, 3:4, None]), (x[None, :, None, -1], None)):
+        y, _ = G.add_rmsnorm(a, out=b)
+        assert y.shape == a.shape and torch.equal(y.reshape(3, 40), want)
+    assert (whole[:, [0, 1, 4, 5, 6]] == 9).all()
+    y, _ = G.add_rmsnorm(x[1:2, 3:4, 5:30])
+    assert torch.equal(y, G.add_rmsnorm(x[1:2, 3:4, 5:30].contiguous())[0])
+    with pytest.raises(ValueError):
+        G.add_rmsnorm(x[:, 1:3])
+
+
 # ------------------------------------------------------------------ append
 def append_by_page(k, v, slots, kc, vc, ks, vs, P):
     """The header's formulas page by page, over all tokens of the call that a page takes, wherever they
