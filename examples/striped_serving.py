@@ -57,6 +57,7 @@ class StripedServer:
         self.head = torch.zeros(1, dtype=torch.int32, device=device)
         self.table = torch.full((requests, per), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(requests, dtype=torch.int32, device=device)
+        self.unplaced = torch.zeros(1, dtype=torch.int32, device=device)
         self.caches = {i: serving.new_cache(self.pages, heads, page, dim // heads, device)
                        for i, kind in enumerate(pattern) if kind == "a"}
         self.states = {i: torch.zeros((requests, dim, modes), device=device)
@@ -100,6 +101,7 @@ class StripedServer:
             x = y @ self.w_out[i].t()
         hidden, _ = G.add_rmsnorm(x, self.norms[-1], res)
         self.lens, self.head = lens, status[:1].clone()
+        self.unplaced += status[1:]           # tokens without a page: looked at when the host next waits
         return hidden, hidden[(cu[1:] - 1).clamp(min=0).long()] @ self.embed.t()
 
     def finish(self, r):
@@ -155,7 +157,8 @@ def main(argv=None):
     a = ap.parse_args(argv)
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(4, 512, (n,), generator=g).tolist() for n in a.prompts]
-    most = max(a.prompts) + a.steps
+    rounds = 20
+    most = max(max(a.prompts) + a.steps + 1, a.page + 3) + rounds
     build = lambda: StripedServer(dim=a.dim, heads=a.heads, requests=len(prompts), max_len=most, page=a.page)  # noqa: E731
     server = build()
     seqs, hidden = serve(server, prompts, a.steps, a.chunk)
@@ -176,12 +179,12 @@ def main(argv=None):
 
     torch.cuda.synchronize()
     began = time.perf_counter()
-    rounds = 20
     for _ in range(rounds):
-        server.lens -= 1                      # the same position again: nothing grows
         server.step(ids[:len(prompts)], [1] * len(prompts))
     torch.cuda.synchronize()
     ms = (time.perf_counter() - began) / rounds * 1e3
+    if int(server.unplaced) or int(whole.unplaced):
+        raise RuntimeError("tokens without a page: the pool is too small")
     print(f"{len(prompts)} requests, {len(server.pattern)} blocks of {a.dim}: {ms:.3f} ms per decode step")
     print("served against one prefill, relative difference per request:",
           " ".join(f"{x:.3f}" for x in far))

@@ -1,6 +1,9 @@
 """The serving operators at the edges of what they accept, against 64-bit formulas.
 
 Tolerances are stated with each test, before its first run."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -443,3 +446,26 @@ def test_page_map_after_a_shortage(R):
         lost += int(status[1])
         lens, head = after, status[:1].clone()
     assert lost > 0
+
+
+# ------------------------------------------------------------------ example
+@pytest.mark.parametrize("args", [["--prompts", "1", "1", "--steps", "3", "--page", "64"],
+                                  ["--prompts", "40", "9", "--steps", "24", "--page", "64"],
+                                  ["--prompts", "29", "9", "--steps", "2", "--page", "16"]])
+def test_example_places_every_token(args, monkeypatch):
+    """The serving example at lengths that end with a page, and with prompts shorter than one: no step
+    leaves a token without a page."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    monkeypatch.syspath_prepend(os.path.join(root, "examples"))
+    import striped_serving
+    seen, page_map = [], G.page_map
+
+    def watched(*a):
+        out = page_map(*a)
+        seen.append(out[4])
+        return out
+
+    monkeypatch.setattr(striped_serving.G, "page_map", watched)
+    far, finite = striped_serving.main(["--dim", "256", "--heads", "4", "--chunk", "48", *args])
+    assert finite and max(far) < 0.05, far
+    assert seen and not torch.stack(seen)[:, 1].any()
