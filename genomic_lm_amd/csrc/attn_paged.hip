@@ -10,7 +10,9 @@
 // K/V head, or four tokens of 8.  32 columns over 64 x 8192 tokens of 8 K/V
 // heads of 128: 142 us there, 214 us as wide units, which are laid out for 128;
 // one request of 65536 tokens on one K/V head: 22 against 65 us.  fp32 heads
-// of 128 use 251 of 256 registers for one set, so fp32 keeps to 16.
+// of 128 use 253 of 256 registers for one set, so fp32 keeps to 16.  A call that
+// holds a wider request keeps to 16 too, so single tokens of 32 heads on one K/V
+// head are wide units there.
 #include "attn_paged.hpp"
 
 namespace hyena {

@@ -288,7 +288,8 @@ inline size_t wide_bytes(int nt, int waves, int DH) {
 // of 32 columns (2.26 -> 2.13 ms for a 4096-token chunk at 32768); 64 columns
 // per wave need more registers than two waves per SIMD have (2.57 ms).  Heads
 // of 64: four waves of 64 columns (1.31 -> 1.20 ms).  fp32's operands fill the
-// registers: 32 columns per wave.
+// registers: 32 columns per wave, and heads of 128 spill 9 of them (13 with pages
+// under 64 tokens).
 struct WideForm {
   int nt, waves;
 };

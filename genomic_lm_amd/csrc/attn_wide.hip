@@ -13,6 +13,8 @@
 // more than AT_SLACK.  Scores of the next tile ahead of this one's softmax (2.29
 // ms), fixed orders of matrix and vector instructions (2.32 to 2.50) and
 // accumulators in the other register file (2.29) were slower than the plain order.
+// Heads of 64 take 1.20 ms for half the products: the softmax costs the same per
+// score, 12.3 vector instructions to an MFMA there against 7.7.
 #include "attn_paged.hpp"
 
 namespace hyena {
@@ -209,9 +211,9 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lo, int item, A
 // bf16 and kept in LDS for the W waves of 32 CW columns each, in two buffers:
 // tile t + 1, in flight from HBM since tile t - 1, is written to the other buffer
 // beside tile t's scores.  16-byte pieces of a row are permuted by the row's
-// number so that lanes on consecutive rows read different banks: 16-byte reads
-// run at 188 bytes a cycle and CU; V's rows, two of which span all banks, are
-// permuted by half their number (by their number: 123).
+// number so that lanes on consecutive rows read different banks; V's rows, two of
+// which span all banks, by half their number.  Bank conflicts are a sixth of the
+// cycles in which LDS works (chunk of 4096 at 32768, heads of 128).
 constexpr float AT_SLACK = 8.0f;      // how far (log2) scores may pass the reference before O is rescaled
 
 template <typename IO, int DH, bool BIG, int CW, int W>

@@ -22,10 +22,10 @@
 // Scales are taken over finite values.
 //
 // Reads 2 DH (2 or 4) bytes per token and head and writes 2 DH: HBM bound for
-// chunks (13624 tokens of 32 heads of 128, bf16: 79 us, 4.2 TB/s).  For single
+// chunks (13624 tokens of 32 heads of 128, bf16: 78 us, 4.3 TB/s).  For single
 // tokens the writes to V are DH single bytes, each in a 64-byte row of its own,
 // and a row is what memory reads and writes for it: 128 tokens of 32 heads take
-// 10.8 us and move 36 MB out and 28 MB in for 3.1 MB of data.  The attention, for
+// 10.8 us and move 33 MB out and 28 MB in for 3.1 MB of data.  The attention, for
 // which V lies so, reads every row thousands of times for that one write.
 #include "fp8.hpp"
 #include "serving.hpp"
@@ -277,8 +277,9 @@ struct Append {
   }
 };
 
-// Four waves per SIMD for bf16 (128 VGPRs): 81 us against 86 us at three and 104
-// us at five (spills) for 13624 tokens of 32 heads of 128; fp32 would spill.
+// Four waves per SIMD for bf16 (128 VGPRs; heads of 128 spill one): 81 us against
+// 86 us at three and 104 us at five (more spills) for 13624 tokens of 32 heads of
+// 128; fp32 would spill.
 template <typename IO, int DH>
 __global__ __launch_bounds__(KA_T, sizeof(IO) == 2 ? 4 : 2) void kv_append_kernel(KvPtr kp, KvPtr vp,
                                                          const int64_t* __restrict__ slots,
@@ -368,7 +369,12 @@ __global__ __launch_bounds__(KA_T, sizeof(IO) == 2 ? 4 : 2) void kv_append_kerne
 }
 
 // Tokens per workgroup: few, so that single tokens spread over the chip; 64 in
-// long calls, where most tokens continue a run and open none.
+// long calls, where most tokens continue a run and open none.  With 4 and with 64,
+// 32 heads of 128 in bf16 (fp32): 256 single tokens 26 and 52 us (28 and 44), 64
+// runs of 16 29 and 33 (32 and 33); but one chunk of 512 13.3 and 12.7 (12.8 and
+// 13.1), of 1024 17 and 14 (20 and 14), of 4096 50 and 29 (62 and 40).  The number of
+// tokens, all that the host knows, is the rule: it favours single tokens, at the
+// cost of chunks of 1024 to 4096.
 static int tokens_per_group(int64_t T) { return T <= 4096 ? 4 : 64; }
 static int64_t append_grid(int64_t T, int64_t H) {
   const int per = tokens_per_group(T);

@@ -18,7 +18,7 @@
 // 32768 x 4096 bf16 with residual, e4m3 per 128 columns: 166 us, 5.7 TB/s of the
 // 944 MB it cannot do without (a 4 GiB copy: 4.75 TB/s counting both ways; three
 // of five bytes here are reads).  5000 x 1001 fp32: 17.7 us, 4.5 TB/s.  16 x
-// 4096: 4.2 us, a launch and the chain above.
+// 4096: 4.5 us, a launch and the chain above.
 #include "fp8.hpp"
 #include "serving.hpp"
 

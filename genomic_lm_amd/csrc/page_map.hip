@@ -12,8 +12,8 @@
 // The data is small (12 bytes a token), so the cost is the latency of a
 // launch; one launch does everything.  The prefix sums over the requests are
 // repeated by every workgroup (R loads from L2, one scan) instead of being
-// handed from a first launch to a second: the kernel takes 5.5 us for 16 decoding
-// requests and 7.9 us for 512 requests with 139701 tokens, so the scan costs
+// handed from a first launch to a second: the kernel takes 5.6 us for 16 decoding
+// requests and 7.7 us for 512 requests with 139701 tokens, so the scan costs
 // less than the ~4 us that the shortest dependent launch takes.
 #include "serving.hpp"
 

@@ -575,8 +575,9 @@ hyena_status_t hyena_kv_append_fp8(const void* k, int64_t k_tok_stride, int64_t 
  * T may be less than cu[R] (hyena_page_map with a fixed T): the queries past it
  * are not there, the others keep their positions and need no token behind
  * them.  Rows of q past cu[R] are not read, nor written in out.  Softmax statistics
- * and sums are fp32; for bf16 activations the weights are rounded to 11 bits for
- * the second product, for fp32 both products carry fp32.  Nothing past a
+ * and sums are fp32; for bf16 activations the weights are rounded to 11 bits (the
+ * smallest to 2^-32 of the largest) for the second product, for fp32 both products
+ * carry fp32.  Nothing past a
  * request's length reaches the result, whatever the cache holds there.
  * Workspace (device, 16-byte aligned, no initial contents) of
  * hyena_attn_paged_workspace_size bytes; NULL, short or misaligned when one is
