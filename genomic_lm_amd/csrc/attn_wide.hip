@@ -3,8 +3,8 @@
 // against 2 DH bytes per cached token, so from some tens of columns on the
 // matrix cores and the softmax's vector work bound it.
 //
-// 4096 tokens at the end of 32768 of 32 heads of 128, bf16: 1.98 ms,
-// 1.04 PFLOP/s of the 2.06 TFLOP under the mask; the library's square product of 16384
+// 4096 tokens at the end of 32768 of 32 heads of 128, bf16: 1.97 to 2.07
+// ms by card, up to 1.04 PFLOP/s of the 2.06 TFLOP under the mask; the library's square product of 16384
 // reaches 1.34 and one of 8192 1.20.  Power bounds both: with cache and queries
 // all zero, the same instructions take 1.83 ms where random ones took 2.25 (128
 // columns per unit then), and the product of 8192 runs at 1.72 PFLOP/s.  So what
