@@ -34,6 +34,16 @@ The serving step around the mixers (submodule serving):
   attn_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu,
                  max_q, scale=None)                                   -> out
 
+The 8-bit projections around them and the rotary positions (submodule projection):
+  linear_fp8(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16)  -> y
+  gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act="gelu",
+                   dtype=torch.bfloat16)                  -> h, or (q, scale) in e4m3
+  quantize_fp8(x, group=0)                                -> (q, scale)
+  quantize_weight_fp8(w)                                  -> (q, scale)
+  rotary_inv_freq(rotary_dim, base=10000.0, factor=1.0)   -> inv_freq
+  qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=None)
+                                                          -> (q_out, k_out)
+
 Every function is also available under the C name (hyena_fftconv_fwd, ...),
 and the submodule hyena_op gives the four core calls the short names
 fftconv, fir, chunk and modal_filter.
@@ -41,6 +51,7 @@ fftconv, fir, chunk and modal_filter.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -54,6 +65,7 @@ __all__ = [
     "chunk_fwd_tokmajor", "chunk_tokmajor_workspace_size", "fir_fwd_tokmajor",
     "add_rmsnorm", "add_rmsnorm_fp8", "page_map", "kv_append_fp8",
     "attn_paged_fp8", "attn_paged_workspace_size",
+    "linear_fp8", "gated_linear_fp8", "quantize_fp8", "quantize_weight_fp8", "rotary_inv_freq", "qk_norm_rope",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_LAUNCH",
     "F32", "BF16", "ALGOS", "EXPORTS",
 ]
@@ -119,6 +131,17 @@ EXPORTS = {
                                     _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, ctypes.c_float,
                                     _p, _int, _p, _size, _p]),
     "hyena_attn_paged_workspace_size": (_size, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "hyena_linear_fp8": (_int, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _int,
+                                _p]),
+    "hyena_gated_linear_fp8": (_int, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _int, _p, _i64, _i64,
+                                      _i64, _i64, _int, _p]),
+    "hyena_gated_linear_fp8_quant": (_int, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _int, _p, _p, _i64,
+                                            _i64, _i64, _p]),
+    "hyena_quantize_fp8": (_int, [_p, _i64, _p, _p, _i64, _i64, _i64, _int, _p]),
+    "hyena_quantize_weight_fp8": (_int, [_p, _i64, _p, _p, _i64, _i64, _int, _p]),
+    "hyena_qk_norm_rope": (_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, ctypes.c_int32,
+                                  ctypes.c_int32, ctypes.c_float, _p, _p, _p, _i64, _i64, _p, _i64, _i64,
+                                  _i64, _i64, _i64, _i64, _int, _p]),
 }
 
 
@@ -586,6 +609,8 @@ def fir_fwd_tokmajor(xin, taps, skip=None, window_in=None, pos=(0, 1, 2), out=No
 
 from .serving import (add_rmsnorm, add_rmsnorm_fp8, page_map, kv_append_fp8,  # noqa: E402
                       attn_paged_fp8, attn_paged_workspace_size)
+from .projection import (linear_fp8, gated_linear_fp8, quantize_fp8, quantize_weight_fp8,  # noqa: E402
+                         rotary_inv_freq, qk_norm_rope)
 
 # The same functions under the names of the C entry points they call
 # (chunk_fwd / chunk_fwd_cpx call the *_algo entry point when algo is not
@@ -611,6 +636,12 @@ hyena_page_map = page_map
 hyena_kv_append_fp8 = kv_append_fp8
 hyena_attn_paged_fp8 = attn_paged_fp8
 hyena_attn_paged_workspace_size = attn_paged_workspace_size
+hyena_linear_fp8 = linear_fp8
+hyena_gated_linear_fp8 = gated_linear_fp8
+hyena_gated_linear_fp8_quant = functools.partial(gated_linear_fp8, dtype=torch.float8_e4m3fn)
+hyena_quantize_fp8 = quantize_fp8
+hyena_quantize_weight_fp8 = quantize_weight_fp8
+hyena_qk_norm_rope = qk_norm_rope
 __all__ += [n for n in list(globals()) if n.startswith("hyena_") and callable(globals()[n])]
 
 from . import hyena_op  # noqa: E402,F401  (short names of the four core calls)

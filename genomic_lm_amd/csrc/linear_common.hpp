@@ -1,0 +1,105 @@
+// linear_common.hpp -- device pieces of the block-scaled e4m3 products
+// (linear_tile.hip, linear_few.hip).
+#pragma once
+
+#include "fp8.hpp"
+#include "projection.hpp"
+
+namespace hyena {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int RUN = 128;      // columns of K that share a scale
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// One operand of a 16 x 16 tile of a run: lane l holds 32 codes of row l % 16;
+// which 32 of the run's 128 columns is free as long as both operands agree.  The
+// product gives the lane rows 4 (l / 16) .. + 3 of a (weights) by column l % 16 (tokens).
+//
+// The matrix unit adds the products of e4m3 codes in groups of eight columns, cut
+// below 2^-13 of the group's largest (measured: 2^16 + 2^2 gives 2^16 where both stand
+// in one group, and all of it where they do not, on every e4m3 instruction);
+// that is 1.5e-5 of a sum of normally distributed codes, whatever K, against the
+// 1.7e-3 of an output rounded to bf16.  For outputs that hold more, fp32 and the scales of 8-bit
+// ones, the codes are widened to bf16 (exact), whose products the unit adds
+// without loss in fp32, at half the rate.
+template <bool WIDE> struct Frag;
+template <> struct Frag<false> {
+  i32x8 v;
+  __device__ __forceinline__ void set(i32x8 codes) { v = codes; }
+};
+template <> struct Frag<true> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(i32x8 codes) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = static_cast<uint32_t>(codes[2 * i]), hi = static_cast<uint32_t>(codes[2 * i + 1]);
+      const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+      const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+      const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+      const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+      v[i] = bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+    }
+  }
+};
+__device__ __forceinline__ f32x4 mfma_run(const Frag<false>& a, const Frag<false>& b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_run(const Frag<true>& a, const Frag<true>& b) {
+  f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ i32x8 pair16(i32x4 lo, i32x4 hi) {
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 16 codes at p, of which n (at most 16, maybe none) exist; zero beyond.
+__device__ __forceinline__ i32x4 codes16(const uint8_t* p, int n) {
+  i32x4 v = {0, 0, 0, 0};
+  if (n >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    for (int e = 0; e < n; ++e) v[e >> 2] |= static_cast<int>(p[e]) << (8 * (e & 3));
+  }
+  return v;
+}
+
+// act(g) * u.  Forms without a difference of near equals: the gelu as g erfc(-g / sqrt 2) / 2,
+// its tanh form as g / (1 + exp(-2 z)).
+__device__ __forceinline__ float gate(float g, float u, int act) {
+  if (act == ACT_GELU) g = 0.5f * g * erfcf(g * -0.70710678118654752f);
+  else if (act == ACT_GELU_TANH)
+    g = g / (1.0f + expf(-1.5957691216057308f * fmaf(0.044715f * g * g, g, g)));
+  else if (act == ACT_SILU) g = g / (1.0f + expf(-g));
+  return g * u;
+}
+
+// The scale of a run whose largest magnitude has the bits `top`, and codes of
+// its values, by the rules of hyena_add_rmsnorm_fp8.
+__device__ __forceinline__ float run_scale(uint32_t top) {
+  const float a = __uint_as_float(top);
+  return a > 0.0f ? fmaxf(a / FP8_MAX, 0x1p-140f) : 1.0f;
+}
+template <int N>
+__device__ __forceinline__ void to_codes(const float (&x)[N], float scale, uint32_t (&w)[N / 4]) {
+  float z[N];
+  if (scale >= 0x1p-100f) {
+    const float is = 1.0f / scale;
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] = x[e] * is;
+  } else {                              // 1 / scale may overflow
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] = x[e] / scale;
+  }
+#pragma unroll
+  for (int e = 0; e < N; e += 4) w[e / 4] = fp8x4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+}
+
+}  // namespace hyena

@@ -111,6 +111,16 @@ typedef enum hyena_chunk_algo {
 #define HYENA_MAX_PAGE 256               /* [HYENA_MIN_PAGE, HYENA_MAX_PAGE] */
 #define HYENA_MAX_REQUESTS 4096          /* requests per serving step */
 #define HYENA_MAX_HEADS 1024             /* attention heads */
+#define HYENA_MAX_PROJ_DIM (1 << 20)     /* N and K of the 8-bit projections */
+#define HYENA_MAX_ROPE_DIM 256           /* DH of hyena_qk_norm_rope */
+
+/* Activation of the gated projection. */
+typedef enum hyena_act {
+    HYENA_ACT_NONE = 0,
+    HYENA_ACT_GELU = 1,          /* g * (1 + erf(g / sqrt 2)) / 2 */
+    HYENA_ACT_GELU_TANH = 2,     /* g * (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+    HYENA_ACT_SILU = 3,          /* g / (1 + exp(-g)) */
+} hyena_act_t;
 
 int hyena_abi_version(void);
 const char* hyena_status_string(hyena_status_t status);
@@ -594,6 +604,119 @@ hyena_status_t hyena_attn_paged_fp8(const void* q, int64_t q_tok_stride, int64_t
                                     hipStream_t stream);
 size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int64_t max_pages,
                                        int64_t page_size, int64_t Hq, int64_t Hkv, int64_t DH);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit projections of a block (in_proj, out_proj and the gated MLP's l1, l2,
+ * l3: evo2_flash README, layer_names table; in_proj in fp8: Evo2-7B-262K model
+ * card, Implementation Notes, 'TELinear'), the quantisation of their operands,
+ * and the rotary positions of the striped attention blocks.
+ *
+ * An operand is e4m3 codes with fp32 scales; a code stands for code * scale.
+ *   activations x (T, K): rows at stride x_stride >= 0, x_group = 0: a scale per
+ *     row; x_group = HYENA_NORM_GROUP: a scale per row and run of 128 columns (the
+ *     last run shorter), scales of a row contiguous; x_scale_stride: floats
+ *     between the scales of two rows (>= 0).  The forms that
+ *     hyena_add_rmsnorm_fp8 and hyena_quantize_fp8 write.
+ *   weights w (N, K) contiguous, w_scale (ceil(N / 128), ceil(K / 128)) contiguous,
+ *     a scale per block of 128 x 128 (the last ones smaller), the form that
+ *     hyena_quantize_weight_fp8 writes.
+ * Codes need no alignment; rows of 16-byte alignment load fastest.  N and K up to
+ * HYENA_MAX_PROJ_DIM.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * hyena_linear_fp8 -- y = x w^T + bias.
+ *   y[t, n] = sum_b (x_scale[t, b] * w_scale[n / 128, b]) * sum_{k in run b} x[t, k] w[n, k] + bias[n]
+ * Products and sums are fp32, the two scales are multiplied first; y is rounded
+ * once.  K = 0 gives the bias.
+ *   bias : (N) fp32, or NULL (0);  y : T rows of N `io`, row stride y_stride >= N
+ * The order of the sums is fixed for a T: a call repeated gives the same bits.
+ */
+hyena_status_t hyena_linear_fp8(const uint8_t* x, int64_t x_stride, const float* x_scale,
+                                int64_t x_scale_stride, int64_t x_group, const uint8_t* w,
+                                const float* w_scale, const float* bias, void* y,
+                                int64_t y_stride, int64_t T, int64_t N, int64_t K,
+                                hyena_dtype_t io, hipStream_t stream);
+
+/*
+ * hyena_gated_linear_fp8 -- the first half of the gated MLP in one pass:
+ *   h = act(x w_gate^T) * (x w_up^T)
+ * with both products as hyena_linear_fp8 has them, unrounded; h is rounded once.
+ *   w_gate, w_up : (I, K) with their scales;  act : hyena_act_t
+ *   h : T rows of I `io`, row stride h_stride >= I
+ */
+hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const float* x_scale,
+                                      int64_t x_scale_stride, int64_t x_group,
+                                      const uint8_t* w_gate, const float* gate_scale,
+                                      const uint8_t* w_up, const float* up_scale, hyena_act_t act,
+                                      void* h, int64_t h_stride, int64_t T, int64_t I, int64_t K,
+                                      hyena_dtype_t io, hipStream_t stream);
+
+/*
+ * hyena_gated_linear_fp8_quant -- the same with h in e4m3 and a scale per row and
+ * 128 columns, the operand of the MLP's last projection; scales and codes by the
+ * rules of hyena_add_rmsnorm_fp8.
+ *   q : (T, I) e4m3, contiguous;  q_scale : (T, ceil(I / 128)) fp32
+ */
+hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
+                                            const float* x_scale, int64_t x_scale_stride,
+                                            int64_t x_group, const uint8_t* w_gate,
+                                            const float* gate_scale, const uint8_t* w_up,
+                                            const float* up_scale, hyena_act_t act, uint8_t* q,
+                                            float* q_scale, int64_t T, int64_t I, int64_t K,
+                                            hipStream_t stream);
+
+/*
+ * hyena_quantize_fp8 -- activations to e4m3 with scales (a mixer's output in front
+ * of out_proj); hyena_quantize_weight_fp8 -- a weight, with a scale per block of
+ * 128 rows by 128 columns.
+ *   scale = max|x| / 448 over the run or block, at least 2^-140 (1 where max|x| is
+ *   0 or NaN),  q = e4m3(x / scale),  x ~ q * scale.
+ * An infinity makes its run's scale infinite: its own code NaN, the others 0.
+ *   x : T rows of D `io`, row stride x_stride >= 0;  q : (T, D), contiguous
+ *   group = 0: q_scale (T), D <= HYENA_MAX_NORM_DIM;  group = HYENA_NORM_GROUP:
+ *   q_scale (T, ceil(D / 128))
+ *   w : N rows of K `io`;  scale : (ceil(N / 128), ceil(K / 128))
+ */
+hyena_status_t hyena_quantize_fp8(const void* x, int64_t x_stride, uint8_t* q, float* q_scale,
+                                  int64_t group, int64_t T, int64_t D, hyena_dtype_t io,
+                                  hipStream_t stream);
+hyena_status_t hyena_quantize_weight_fp8(const void* w, int64_t w_stride, uint8_t* q, float* scale,
+                                         int64_t N, int64_t K, hyena_dtype_t io,
+                                         hipStream_t stream);
+
+/*
+ * hyena_qk_norm_rope -- the norms of query and key heads and their rotation in one
+ * pass (MHA with rotary embedding, base 10000, positions scaled 32-fold for 262K:
+ * Evo2-7B-262K model card, Architecture; frequencies and multiply in fp32:
+ * Implementation Notes, 'Custom rotary embedding').  Per head of DH columns:
+ *   norm != 0:  x' = x / sqrt(mean(x^2) + eps) * weight, else x' = x
+ *   for i < rotary_dim / 2, f = positions[t] * inv_freq[i], (a, b) = columns
+ *   (i, i + rotary_dim / 2), or (2i, 2i + 1) where interleaved != 0:
+ *     a' = a cos f - b sin f,   b' = b cos f + a sin f;   the rest stays.
+ * f and its reduction are taken in 64 bits from the fp32 inv_freq, so far
+ * positions keep their angle; outputs are rounded once.
+ *   q (T, Hq, DH), k (T, Hk, DH) `io`, token and head strides >= 0
+ *   q_out, k_out : written, with strides of their own; may be q and k (equal
+ *                  strides), and must not overlap them otherwise
+ *   positions : (T) int32; rows with a negative position (hyena_page_map gives
+ *               them to tokens past the last) are neither read nor written.
+ *               NULL with rotary_dim = 0 only.
+ *   inv_freq  : (rotary_dim / 2) fp32; scaled positions have it divided
+ *   q_weight, k_weight : (DH) fp32, or NULL (1);  eps : finite, >= 0
+ * rotary_dim even, 0 (no rotation) to DH <= HYENA_MAX_ROPE_DIM; Hq, Hk >= 0, each
+ * <= HYENA_MAX_HEADS (0: that pointer may be NULL).  Rows whose squares leave fp32
+ * have their norm as in hyena_add_rmsnorm.
+ */
+hyena_status_t hyena_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                  const void* k, int64_t k_tok_stride, int64_t k_head_stride,
+                                  const int32_t* positions, const float* inv_freq,
+                                  int64_t rotary_dim, int32_t interleaved, int32_t norm, float eps,
+                                  const float* q_weight, const float* k_weight, void* q_out,
+                                  int64_t qo_tok_stride, int64_t qo_head_stride, void* k_out,
+                                  int64_t ko_tok_stride, int64_t ko_head_stride, int64_t T,
+                                  int64_t Hq, int64_t Hk, int64_t DH, hyena_dtype_t io,
+                                  hipStream_t stream);
 
 #ifdef __cplusplus
 }
