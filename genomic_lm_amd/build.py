@@ -48,6 +48,7 @@ EXTRA_FLAGS = {
     "attn_wide.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "chunk_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fftconv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "linear_dma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "linear_few.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "linear_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fir_mfma.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],

@@ -38,6 +38,8 @@ bool linear_fits(int64_t T, int64_t N);               // whether the launch grid
 hipError_t launch_linear(const LinearArgs& a);
 hipError_t launch_linear_few(const LinearArgs& a);    // T <= LINEAR_FEW_ROWS
 hipError_t launch_linear_tile(const LinearArgs& a);
+bool linear_dma_takes(const LinearArgs& a);            // alignment and strides
+hipError_t launch_linear_dma(const LinearArgs& a);
 constexpr int LINEAR_FEW_ROWS = 16;
 
 // Codes and scales of T rows: a scale per row (group 0), per 128 columns
