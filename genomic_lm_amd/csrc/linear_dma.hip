@@ -6,108 +6,163 @@ namespace hyena {
 
 typedef __attribute__((address_space(3))) void lds_ptr;
 
-// 16 bytes (4) per lane from base + off straight into LDS, lane l at dst + 16 l (4 l).
-// Written as assembly so that the compiler, which cannot tell the two halves of the LDS
-// buffer apart, does not make every LDS read of one half wait for the loads into the
-// other; the kernel waits for them itself (dma_sync).  They write no vector registers;
-// m0 is the compiler's only where it sets it itself, just before the use.
+// A wave's value where the compiler has not seen that it is one.
+__device__ __forceinline__ uint64_t scalar(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
+  return lo | (static_cast<uint64_t>(hi) << 32);
+}
+// 16 bytes (4) per lane from base + off straight into LDS, lane l at dst + 16 l (4 l);
+// base and dst are the wave's.  Written as assembly so that the compiler, which cannot tell
+// the halves of the LDS buffer apart, does not make every LDS read of one half wait for the
+// loads into the other; the kernels wait for them themselves.  They write no vector
+// registers; m0 is the compiler's only where it sets it itself, just before the use.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(off), "s"(scalar(base))
                : "memory");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(dst), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(off), "s"(scalar(base))
                : "memory");
 }
-// This wave's loads have arrived; then every wave is here.
+// All but N of this wave's loads have arrived, and its LDS reads; then every wave is here.
+template <int N>
 __device__ __forceinline__ void dma_sync() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  static_assert(N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// WT x WN waves, each with MT x MN tiles of 16 tokens by 16 columns.
-template <int WT, int WN, int MT, int MN, bool GATED, int OUT>
-__global__ __launch_bounds__(WT * WN * 64) void linear_dma_kernel(LinearArgs a, int tiles_t, int tiles_n) {
-  constexpr int NW = WT * WN;
-  constexpr int BT = WT * MT * 16, BN = WN * MN * 16;
-  constexpr int CN = GATED ? BN / 2 : BN;
-  constexpr int MC = GATED ? MN / 2 : MN;
-  constexpr bool WIDE = OUT != OUT_BF16;                 // Frag says why
-  constexpr int RX = BT / (NW * 8), RW = BN / (NW * 8);  // loads of a wave, eight rows each
-  static_assert(BT % (NW * 8) == 0 && BN % (NW * 8) == 0 && BT % 64 == 0 && BT / 64 <= NW, "whole loads");
+// What a wave of WT x WN, each with MT x MN tiles of 16 x 16, loads of each run of K: codes of
+// the tokens and of the weights (a gated wave's first MN / 2 tiles from w0, the others from w1),
+// the tokens' scales, those of w0 and of w1, in this order in LDS.
+template <int WT, int WN, int MT, int MN, bool GATED>
+struct Loads {
+  static constexpr int NW = WT * WN;
+  static constexpr int BT = WT * MT * 16, BN = WN * MN * 16;
+  static constexpr int CN = GATED ? BN / 2 : BN, MC = GATED ? MN / 2 : MN;   // columns of the output
+  static constexpr int RX = BT / (NW * 8), RW = BN / (NW * 8);               // loads of eight rows each
+  static constexpr int XW = BT / 64;                                         // waves for the tokens' scales
+  static_assert(BT % (NW * 8) == 0 && BN % (NW * 8) == 0 && BT % 64 == 0, "whole loads");
+  static_assert(NW > XW + (GATED ? 1 : 0), "waves for all scales");
   static_assert(RUN % (MC * 16) == 0, "a wave's columns lie in one block of the scales");
-  constexpr int XB = BT * RUN, WB = BN * RUN, BUF = XB + WB + BT * 4;   // codes, codes, scales
-  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * BUF];
-  const uint32_t sh0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr*)(sh)));
+  static_assert(NW % 2 == 0, "a wave's eight rows are all even or all odd ones");
+  static constexpr int XB = BT * RUN, SB = XB + BN * RUN, BUF = SB + BT * 4 + 512;
 
-  const int tid = static_cast<int>(threadIdx.x);
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint8_t* bx;
+  const uint8_t* bw[RW];
+  const float* bs;
+  uint32_t ox[RX], ow[RW], os, ds;
+  int step, wave;
+  int chunk;        // a load's lane l fills place l % 8 of row l / 8: the chunk that belongs there (slot)
+
+  __device__ __forceinline__ Loads(const LinearArgs& a, int64_t t0, int n0, int wave, int lane) : wave(wave) {
+    const int lrow = lane >> 3;
+    chunk = ((lane & 7) ^ lrow ^ (wave & 1)) * 16;
+    const int64_t rows = a.T - t0;                       // rows past the end repeat the last one
+    bx = a.x + t0 * a.x_stride;
+#pragma unroll
+    for (int i = 0; i < RX; ++i) {
+      const int r = (i * NW + wave) * 8 + lrow;
+      ox[i] = static_cast<uint32_t>(r < rows ? r : rows - 1) * static_cast<uint32_t>(a.x_stride) + chunk;
+      asm volatile("" : "+v"(ox[i]));                    // 32 bits, not the 64 of the product
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const int r = (i * NW + wave) * 8;                 // first of the eight
+      int n = r;
+      bw[i] = a.w0;
+      if constexpr (GATED) {
+        const int rr = r % (MN * 16);
+        n = r / (MN * 16) * (MC * 16) + rr % (MC * 16);
+        if (rr >= MC * 16) bw[i] = a.w1;
+      }
+      bw[i] += static_cast<int64_t>(n0) * a.K;
+      n += lrow;
+      ow[i] = static_cast<uint32_t>(n < a.N - n0 ? n : a.N - n0 - 1) * static_cast<uint32_t>(a.K) + chunk;
+      asm volatile("" : "+v"(ow[i]));
+    }
+    // Scales come through LDS too: a scalar load in the loop would be waited for with every
+    // LDS read (both count in lgkmcnt, scalar ones out of order).
+    if (wave < XW) {
+      const int r = wave * 64 + lane;
+      bs = a.x_scale + t0 * a.xs_row;
+      os = static_cast<uint32_t>(r < rows ? r : rows - 1) * static_cast<uint32_t>(a.xs_row) * 4u;
+      step = a.xs_run;
+      ds = SB + wave * 256;
+    } else {                                             // of the block of each wave column
+      const int which = GATED ? (wave - XW) & 1 : 0;
+      const int c = n0 + lane % WN * (MC * 16);
+      bs = which ? a.s1 : a.s0;
+      os = static_cast<uint32_t>((c < a.N ? c : a.N - 1) / RUN) *
+           static_cast<uint32_t>((a.K + RUN - 1) / RUN) * 4u;
+      step = 1;
+      ds = SB + (XW + which) * 256;
+    }
+  }
+  __device__ __forceinline__ void scales(int kb, uint32_t to) const {
+    dma4(bs + static_cast<int64_t>(kb) * step, os, to + ds);
+  }
+  __device__ __forceinline__ void tokens(int kb, uint32_t to) const {
+#pragma unroll
+    for (int i = 0; i < RX; ++i) dma16(bx + kb * RUN, ox[i], to + (i * NW + wave) * 1024);
+  }
+  template <int FIRST, int EVERY>
+  __device__ __forceinline__ void weights(int kb, uint32_t to) const {
+#pragma unroll
+    for (int i = FIRST; i < RW; i += EVERY) dma16(bw[i] + kb * RUN, ow[i], to + XB + (i * NW + wave) * 1024);
+  }
+  // the lane's chunks of a run that K does not reach (it is a multiple of 16): zeros
+  __device__ __forceinline__ void clear(uint8_t* buf, int lane) const {
+    const i32x4 zero = {0, 0, 0, 0};
+    i32x4* const z = reinterpret_cast<i32x4*>(buf + wave * 1024) + lane;
+#pragma unroll
+    for (int i = 0; i < RX + RW; ++i) z[i * NW * 64] = zero;
+  }
+};
+
+// A lane's two chunks of row lane % 16 of a tile of 16 rows.
+__device__ __forceinline__ i32x8 tile_codes(const uint8_t* tile, int lane) {
+  const int r = lane & 15, c = (lane >> 4) * 2, swz = (r & 7) ^ (r >> 3);
+  return pair16(*reinterpret_cast<const i32x4*>(tile + r * RUN + (c ^ swz) * 16),
+                *reinterpret_cast<const i32x4*>(tile + r * RUN + ((c + 1) ^ swz) * 16));
+}
+
+// KG groups of WT x WN waves share a tile and take turns at the runs of K.
+template <int WT, int WN, int MT, int MN, int KG, bool GATED, int OUT>
+__global__ __launch_bounds__(WT * WN * KG * 64) void linear_dma_kernel(LinearArgs a, int tiles_t, int tiles_n) {
+  using L = Loads<WT, WN, MT, MN, GATED>;
+  constexpr int NW = L::NW, MC = L::MC, BUF = L::BUF;
+  constexpr bool WIDE = OUT != OUT_BF16;                 // Frag says why
+  constexpr int JOIN = (KG - 1) * NW * MN * MT * 1024;   // the other groups' sums
+  constexpr int TOPS = OUT == OUT_FP8 ? WN * L::BT * 4 : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * KG * BUF > JOIN + TOPS ? 2 * KG * BUF : JOIN + TOPS];
+
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave_of_all = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int kg = wave_of_all / NW, wave = wave_of_all % NW;
   const int wt = wave / WN, wn = wave % WN;
+  uint8_t* const mine = sh + kg * 2 * BUF;
+  const uint32_t mine0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr*)(mine)));
   int ti, ni;
   tile_of(tiles_t, tiles_n, ti, ni);
-  const int64_t t0 = static_cast<int64_t>(ti) * BT;
-  const int n0 = ni * CN;
-  const int K = a.K, N = a.N;
+  const int64_t t0 = static_cast<int64_t>(ti) * L::BT;
+  const int n0 = ni * L::CN;
+  const int K = a.K;
   const int blocks = (K + RUN - 1) / RUN;
-
-  // A load of a wave fills eight rows of 128 bytes, lane l place l % 8 of row l / 8;
-  // the chunk that belongs there (slot) is the same for all of a lane's loads.
-  static_assert(NW % 2 == 0, "a wave's eight rows are all even or all odd ones");
-  const int lrow = lane >> 3;
-  const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ lrow ^ (wave & 1)) * 16;
-  const int64_t rows = a.T - t0;                          // rows past the end repeat the last one
-  const uint8_t* const bx = a.x + t0 * a.x_stride;
-  const uint8_t* bw[RW];
-  uint32_t ox[RX], ow[RW];
-#pragma unroll
-  for (int i = 0; i < RX; ++i) {
-    const int r = (i * NW + wave) * 8 + lrow;
-    ox[i] = static_cast<uint32_t>(r < rows ? r : rows - 1) * static_cast<uint32_t>(a.x_stride) + chunk;
-  }
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    const int r = (i * NW + wave) * 8;                   // first of the eight
-    int n = r;
-    bw[i] = a.w0;
-    if constexpr (GATED) {
-      const int rr = r % (MN * 16);
-      n = r / (MN * 16) * (MC * 16) + rr % (MC * 16);
-      if (rr >= MC * 16) bw[i] = a.w1;
-    }
-    bw[i] += static_cast<int64_t>(n0) * K;
-    n += lrow;
-    ow[i] = static_cast<uint32_t>(n < N - n0 ? n : N - n0 - 1) * static_cast<uint32_t>(K) + chunk;
-  }
-  const int sr = wave * 64 + lane;                       // scales: the first BT / 64 waves
-  const uint32_t os = static_cast<uint32_t>(sr < rows ? sr : rows - 1) * static_cast<uint32_t>(a.xs_row) * 4u;
-  const float* const bs = a.x_scale + t0 * a.xs_row;
-
-  auto stage = [&](int kb, int buf) {
-    const int k = kb * RUN;
-    const uint32_t to = sh0 + buf * BUF + wave * 1024;
-    if (wave < BT / 64) dma4(bs + static_cast<int64_t>(kb) * a.xs_run, os, sh0 + buf * BUF + XB + WB + wave * 256);
-    if (k + static_cast<int>(chunk) < K) {               // K is a multiple of 16
-#pragma unroll
-      for (int i = 0; i < RX; ++i) dma16(bx + k, ox[i], to + i * (NW * 1024));
-#pragma unroll
-      for (int i = 0; i < RW; ++i) dma16(bw[i] + k, ow[i], to + XB + i * (NW * 1024));
-    } else {                                             // the last, shorter run: zeros beyond K
-      const i32x4 zero = {0, 0, 0, 0};
-      i32x4* const z = reinterpret_cast<i32x4*>(sh + buf * BUF + wave * 1024) + lane;
-#pragma unroll
-      for (int i = 0; i < RX + RW; ++i) z[i * NW * 64] = zero;
+  const L from(a, t0, n0, wave, lane);
+  auto stage = [&](int kb, int buf) __attribute__((always_inline)) {
+    const uint32_t to = mine0 + buf * BUF;
+    from.scales(kb, to);
+    if (kb * RUN + from.chunk < K) {
+      from.tokens(kb, to);
+      from.template weights<0, 1>(kb, to);
+    } else {
+      from.clear(mine + buf * BUF, lane);
     }
   };
-
-  const int fr = lane & 15, fc = lane >> 4;
-  const int swz = (fr & 7) ^ (fr >> 3);
-  // byte places of the lane's two chunks in a tile of 16 rows
-  const int f0 = fr * RUN + ((2 * fc) ^ swz) * 16, f1 = fr * RUN + ((2 * fc + 1) ^ swz) * 16;
-  const int ncol = n0 + wn * (MC * 16);
-  const int64_t sbase = static_cast<int64_t>((ncol < N ? ncol : N - 1) / RUN) * blocks;
-  typedef const __attribute__((address_space(4))) float* cptr;
-  const cptr ps0 = (cptr)(a.s0 + sbase);
-  const cptr ps1 = (cptr)(GATED ? a.s1 + sbase : a.s0);
 
   f32x4 acc[MN][MT];
 #pragma unroll
@@ -115,48 +170,204 @@ __global__ __launch_bounds__(WT * WN * 64) void linear_dma_kernel(LinearArgs a, 
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  if (blocks > 0) stage(0, 0);
-  dma_sync();
-  for (int kb = 0; kb < blocks; ++kb) {
-    if (kb + 1 < blocks) stage(kb + 1, (kb + 1) & 1);
-    const uint8_t* const b = sh + (kb & 1) * BUF;
+  if (kg < blocks) stage(kg, 0);
+  dma_sync<0>();
+  int buf = 0;
+  for (int k0 = 0; k0 < blocks; k0 += KG) {
+    const int kb = k0 + kg;
+    if (kb + KG < blocks) stage(kb + KG, buf ^ 1);
+    if (KG == 1 || kb < blocks) {
+      const uint8_t* const b = mine + buf * BUF;
+      const float* const st = reinterpret_cast<const float*>(b + L::SB) + wt * MT * 16 + (lane & 15);
+      const float* const sw = reinterpret_cast<const float*>(b + L::SB + L::XW * 256) + wn;
+      const float w0 = sw[0], w1 = GATED ? sw[64] : 0.0f;
+      Frag<WIDE> fx[MT];
+      float sx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        fx[j].set(tile_codes(b + (wt * MT + j) * 2048, lane));
+        sx[j] = st[j * 16];
+      }
+#pragma unroll
+      for (int i = 0; i < MN; ++i) {
+        Frag<WIDE> fw;
+        fw.set(tile_codes(b + L::XB + (wn * MN + i) * 2048, lane));
+        const float s = GATED && i >= MC ? w1 : w0;
+        // keeps the compiler from widening several operands ahead, for which no registers are left
+        if constexpr (WIDE) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const f32x4 p = mfma_run(fw, fx[j]);
+          const float f = sx[j] * s;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], f, acc[i][j][e]);
+        }
+      }
+    }
+    buf ^= 1;
+    dma_sync<0>();
+  }
+  if constexpr (KG > 1) {                                // the groups' sums, in their order
+    f32x4* const join = reinterpret_cast<f32x4*>(sh) + wave * (MN * MT * 64) + lane;
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < MN; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) join[((kg - 1) * NW * MN * MT + i * MT + j) * 64] = acc[i][j];
+    }
+    tile_sync();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < MN; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] += join[(g * NW * MN * MT + i * MT + j) * 64];
+  }
+  tile_epilogue<WT, WN, MT, MN, GATED, OUT>(a, acc, t0, n0 + wn * (MC * 16), wt, wn, lane, sh + JOIN);
+}
+
+// The largest products with bf16 outputs: 256 x 256 tiles, eight waves of 64 x 128 in two halves
+// that take turns, one reading its operands of half a run while the other multiplies (the
+// two waves of a SIMD belong to different halves).  Time goes by in slots that end with a barrier;
+// of run r the first half reads in slots 4r and 4r + 2 and multiplies in 4r + 1 and 4r + 3, the
+// second does the same a slot later.  A read slot also asks for what it may overwrite: in its
+// first the other columns of the next run, in its second the tokens and first columns of the run
+// after; so a run's worth of loads (FLY) stays on its way, each for about six slots.
+// A shorter last run goes first, where its zeros can be written in peace.
+template <bool GATED>
+__global__ __launch_bounds__(512) void linear_turns_kernel(LinearArgs a, int tiles_t, int tiles_n) {
+  constexpr int WT = 4, WN = 2, MT = 4, MN = 8;
+  using L = Loads<WT, WN, MT, MN, GATED>;
+  constexpr int BUF = L::BUF, FLY = L::RX + L::RW + 1;
+  static_assert(L::NW == 8 && L::RW == 4, "the even loads are the waves' first halves");
+  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * BUF];
+  const uint32_t sh0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr*)(sh)));
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+  const bool second = wave >= 4;
+  int ti, ni;
+  tile_of(tiles_t, tiles_n, ti, ni);
+  const int64_t t0 = static_cast<int64_t>(ti) * L::BT;
+  const int n0 = ni * L::CN;
+  const int full = a.K / RUN, tail = a.K % RUN ? 1 : 0, blocks = full + tail;   // full >= 1
+  const L from(a, t0, n0, wave, lane);
+  // Step `it` takes run it - tail, the first of a tail run `full`.  Past the end the last full run
+  // is loaded again, so that every step has as many loads on their way.
+  auto run_of = [&](int it) {
+    const int kb = it - tail < full ? it - tail : full - 1;
+    return kb < 0 ? full : kb;
+  };
+  auto ask0 = [&](int it) __attribute__((always_inline)) {
+    const int kb = run_of(it);
+    const uint32_t to = sh0 + (it & 1) * BUF;
+    from.scales(kb, to);
+    from.tokens(kb, to);
+    from.template weights<0, 2>(kb, to);
+  };
+  auto ask1 = [&](int it) __attribute__((always_inline)) {
+    from.template weights<1, 2>(run_of(it), sh0 + (it & 1) * BUF);
+  };
+  // nothing but the loads and reads moves from one slot to another
+  auto slot_end = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_end = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    dma_sync<FLY>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  f32x4 acc[MN][MT];
+#pragma unroll
+  for (int i = 0; i < MN; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  Frag<false> fx[MT], fw[MN / 2];
+  float sx[MT];
+  // products of half H's columns; each is scaled and added two products later, when it is there
+  auto multiply = [&](auto half, float sw) __attribute__((always_inline)) {
+    constexpr int H = decltype(half)::value, Q = MN / 2 * MT;
+    float s[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) s[j] = sx[j] * sw;
+    f32x4 p[3];
+    auto add = [&](int q) __attribute__((always_inline)) {
+      f32x4& c = acc[H * MN / 2 + q / MT][q % MT];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = fmaf(p[q % 3][e], s[q % MT], c[e]);
+    };
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      p[q % 3] = mfma_run(fw[q / MT], fx[q % MT]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (q > 1) add(q - 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(Q - 2);
+    add(Q - 1);
+  };
+
+  {
+    const int first = run_of(0);
+    const bool on = first * RUN + from.chunk < a.K;
+    if (on) {
+      ask0(0);
+      ask1(0);
+    } else {
+      from.scales(first, sh0);
+      from.clear(sh, lane);
+    }
+    ask0(1);
+  }
+  // (the scales of lanes that are not `on` were asked for in a branch of their own, so fewer
+  // loads than FLY may follow the first run's: all of them are waited for)
+  dma_sync<0>();
+  if (second) slot_end();
+  for (int it = 0; it < blocks; ++it) {
+    const uint8_t* const b = sh + (it & 1) * BUF;
     const uint8_t* const xt = b + wt * MT * 2048;
-    const uint8_t* const wp = b + XB + wn * MN * 2048;
-    const float* const st = reinterpret_cast<const float*>(b + XB + WB) + wt * MT * 16 + fr;
-    const float w0 = ps0[kb], w1 = GATED ? ps1[kb] : 0.0f;
-    Frag<WIDE> fx[MT];
-    float sx[MT];
+    const uint8_t* const wp = b + L::XB + wn * MN * 2048;
+    const float* const st = reinterpret_cast<const float*>(b + L::SB) + wt * MT * 16 + (lane & 15);
+    const float* const sw = reinterpret_cast<const float*>(b + L::SB + L::XW * 256) + wn;
+    const float w0 = sw[0], w1 = GATED ? sw[64] : w0;
+    ask1(it + 1);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-      fx[j].set(pair16(*reinterpret_cast<const i32x4*>(xt + j * 2048 + f0),
-                       *reinterpret_cast<const i32x4*>(xt + j * 2048 + f1)));
+      fx[j].set(tile_codes(xt + j * 2048, lane));
       sx[j] = st[j * 16];
     }
 #pragma unroll
-    for (int i = 0; i < MN; ++i) {
-      Frag<WIDE> fw;
-      fw.set(pair16(*reinterpret_cast<const i32x4*>(wp + i * 2048 + f0),
-                    *reinterpret_cast<const i32x4*>(wp + i * 2048 + f1)));
-      const float sw = GATED && i >= MC ? w1 : w0;
+    for (int i = 0; i < MN / 2; ++i) fw[i].set(tile_codes(wp + i * 2048, lane));
+    read_end();
+    multiply(std::integral_constant<int, 0>{}, w0);
+    slot_end();
+    ask0(it + 2);
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const f32x4 p = mfma_run(fw, fx[j]);
-        const float s = sx[j] * sw;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
-      }
-    }
-    dma_sync();
+    for (int i = 0; i < MN / 2; ++i) fw[i].set(tile_codes(wp + (MN / 2 + i) * 2048, lane));
+    read_end();
+    multiply(std::integral_constant<int, 1>{}, w1);
+    slot_end();
   }
-  tile_epilogue<WT, WN, MT, MN, GATED, OUT>(a, acc, t0, ncol, wt, wn, lane, sh);
+  if (!second) slot_end();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // no load outlives its workgroup's LDS
+  tile_epilogue<WT, WN, MT, MN, GATED, OUT_BF16>(a, acc, t0, n0 + wn * (L::MC * 16), wt, wn, lane, sh);
 }
 
-template <int WT, int WN, int MT, int MN, bool GATED, int OUT>
+template <int BT, int CN>
+static int64_t tiles(const LinearArgs& a) {
+  return (a.T + BT - 1) / BT * ((a.N + CN - 1) / CN);
+}
+
+template <int WT, int WN, int MT, int MN, int KG, bool GATED, int OUT>
 static void dma_go(const LinearArgs& a) {
   constexpr int BT = WT * MT * 16, CN = WN * MN * 16 / (GATED ? 2 : 1);
-  const int64_t tt = (a.T + BT - 1) / BT, tn = (a.N + CN - 1) / CN;
-  linear_dma_kernel<WT, WN, MT, MN, GATED, OUT><<<static_cast<unsigned>(tt * tn), WT * WN * 64, 0, a.stream>>>(
-      a, static_cast<int>(tt), static_cast<int>(tn));
+  linear_dma_kernel<WT, WN, MT, MN, KG, GATED, OUT>
+      <<<static_cast<unsigned>(tiles<BT, CN>(a)), WT * WN * KG * 64, 0, a.stream>>>(
+          a, static_cast<int>((a.T + BT - 1) / BT), static_cast<int>((a.N + CN - 1) / CN));
 }
 
 // whole 16-byte chunks, and 32-bit offsets within a tile
@@ -166,14 +377,45 @@ bool linear_dma_takes(const LinearArgs& a) {
          a.x_stride < (1 << 23) && a.xs_row < (1 << 21);
 }
 
+// The largest tiles where they fill most of the 256 CUs, each with one workgroup; smaller ones,
+// whose K two or four groups of waves share, where they do not.  Measured (us, bf16 outputs, the
+// tile that is taken against the next): 8192 x 12288 x 4096 256 x 256 384, 128 x 128 486; 1024 x
+// 12288 (192 tiles) 72, 91; 512 x 12288 (384 tiles of 128 x 128) 54 by one group, 62 by two, 59 by
+// 256 x 256; 512 x 4096 (128) 41, 32 by two groups, 37 by 64 x 64; 256 x 4096 (64) 28, 64 x 64 by
+// four groups 26; 64 x 4096 25, 15.
+template <bool GATED, int OUT>
+static void dma_pick(const LinearArgs& a) {
+  const int64_t n256 = tiles<256, GATED ? 128 : 256>(a), n128 = tiles<128, GATED ? 64 : 128>(a);
+  if constexpr (OUT == OUT_FP8) {
+    // a workgroup has whole runs of 128 columns: 8192 x 11008 x 4096 256 rows 1269, 128 rows 1500;
+    // 1000 x 10928 (344 tiles) 241, 231; 64 x 11008 128 rows 74, 64 rows 54
+    if (n256 >= 400) dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
+    else if (a.T > 64) dma_go<4, 2, 2, 8, 1, GATED, OUT>(a);
+    else dma_go<4, 2, 1, 8, 1, GATED, OUT>(a);
+  } else if (n256 >= 128 && (OUT != OUT_BF16 || a.K >= RUN)) {
+    if constexpr (OUT == OUT_BF16)
+      linear_turns_kernel<GATED><<<static_cast<unsigned>(n256), 512, 0, a.stream>>>(
+          a, static_cast<int>((a.T + 255) / 256), static_cast<int>(n256 / ((a.T + 255) / 256)));
+    else dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
+  } else if (a.T > 64 && n128 > 256) {
+    dma_go<2, 2, 4, 4, 1, GATED, OUT>(a);
+  } else if (a.T > 64 && n128 >= 90) {
+    dma_go<2, 2, 4, 4, 2, GATED, OUT>(a);
+  } else if constexpr (GATED) {
+    dma_go<2, 2, 2, 4, 2, GATED, OUT>(a);
+  } else {
+    dma_go<2, 2, 2, 2, 4, GATED, OUT>(a);
+  }
+}
+
 hipError_t launch_linear_dma(const LinearArgs& a) {
   if (a.w1) {
-    if (a.out == OUT_BF16) dma_go<4, 2, 4, 8, true, OUT_BF16>(a);
-    else if (a.out == OUT_F32) dma_go<4, 2, 4, 4, true, OUT_F32>(a);
-    else dma_go<2, 4, 4, 4, true, OUT_FP8>(a);
+    if (a.out == OUT_BF16) dma_pick<true, OUT_BF16>(a);
+    else if (a.out == OUT_F32) dma_pick<true, OUT_F32>(a);
+    else dma_pick<true, OUT_FP8>(a);
   } else {
-    if (a.out == OUT_BF16) dma_go<4, 2, 4, 8, false, OUT_BF16>(a);
-    else dma_go<4, 2, 4, 4, false, OUT_F32>(a);
+    if (a.out == OUT_BF16) dma_pick<false, OUT_BF16>(a);
+    else dma_pick<false, OUT_F32>(a);
   }
   return hipGetLastError();
 }

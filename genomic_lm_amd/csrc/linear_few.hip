@@ -172,7 +172,7 @@ bool linear_fits(int64_t T, int64_t N) { return (T + 63) / 64 * ((N + 63) / 64) 
 
 hipError_t launch_linear(const LinearArgs& a) {
   if (a.T <= LINEAR_FEW_ROWS) return launch_linear_few(a);
-  return a.T > 256 && linear_dma_takes(a) ? launch_linear_dma(a) : launch_linear_tile(a);
+  return linear_dma_takes(a) ? launch_linear_dma(a) : launch_linear_tile(a);
 }
 
 }  // namespace hyena

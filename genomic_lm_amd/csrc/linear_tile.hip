@@ -148,14 +148,21 @@ static void tile_go(const LinearArgs& a) {
   auto go = [&](auto kernel) {
     kernel<<<grid, WT * WN * 64, 0, a.stream>>>(a, static_cast<int>(tt), static_cast<int>(tn));
   };
-  if (a.out == OUT_F32) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_F32>);
-  else if (a.out == OUT_BF16) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_BF16>);
-  else if constexpr (GATED && CN % RUN == 0) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_FP8>);
+  if constexpr (GATED && CN % RUN == 0) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_FP8>);
+  else if (a.out == OUT_F32) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_F32>);
+  else go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_BF16>);
 }
 
 hipError_t launch_linear_tile(const LinearArgs& a) {
-  if (a.w1) tile_go<2, 4, 4, 4, true>(a);
-  else tile_go<2, 2, 4, 4, false>(a);
+  const int64_t n128 = (a.T + 127) / 128 * ((a.N + 127) / 128) * (a.w1 ? 2 : 1);
+  if (a.out == OUT_FP8) tile_go<4, 2, 2, 8, true>(a);
+  else if (a.w1) {
+    if (n128 >= 256) tile_go<2, 2, 4, 4, true>(a);
+    else tile_go<2, 2, 2, 4, true>(a);
+  } else {
+    if (n128 >= 256) tile_go<2, 2, 4, 4, false>(a);
+    else tile_go<2, 2, 2, 2, false>(a);
+  }
   return hipGetLastError();
 }
 

@@ -33,6 +33,19 @@ __device__ __forceinline__ void tile_of(int tiles_t, int tiles_n, int& ti, int& 
   ni = in / high;
 }
 
+// Exchanges the odd 16-lane rows of a with the even ones of b, and the upper half of
+// a with the lower half of b.
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
 // The tile's sums to the output: a wave's lane holds columns 4 (l / 16) .. + 3 of
 // token l % 16 in each of its MT x MN tiles, the gate's in the first half of
 // the MN and the other weight's in the second.  sh: LDS that nobody reads any more.
@@ -44,7 +57,7 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
   const int N = a.N;
   const int cg = 4 * (lane >> 4);
   if constexpr (OUT == OUT_FP8) {
-    static_assert(GATED, "codes come from the gated product");
+    static_assert(GATED && MC % 4 == 0, "codes come from the gated product");
     float* top = reinterpret_cast<float*>(sh);          // [WN][BT]
     constexpr int GW = RUN / (MC * 16);                 // waves that share a run of columns
     float h[MC][MT][4];
@@ -79,48 +92,75 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
         m = o > m ? o : m;
       }
       const float scale = run_scale(m);
-      if (t >= a.T) continue;
-      if (wn % GW == 0 && lane < 16 && ncol < N) a.q_scale[t * runs + ncol / RUN] = scale;
+      if (wn % GW == 0 && lane < 16 && ncol < N && t < a.T) a.q_scale[t * runs + ncol / RUN] = scale;
       uint8_t* row = static_cast<uint8_t*>(a.y) + t * a.y_stride;
 #pragma unroll
-      for (int i = 0; i < MC; ++i) {
-        uint32_t w[1];
-        to_codes<4>(h[i][j], scale, w);
-        const int n = ncol + i * 16 + cg;
-        if (n + 4 <= N) __builtin_memcpy(row + n, w, 4);
+      for (int i = 0; i < MC; i += 4) {
+        // lane group g holds words g of four tiles; afterwards the four words of tile g
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t c[1];
+          to_codes<4>(h[i + q][j], scale, c);
+          w[q] = c[0];
+        }
+        swap16(w[0], w[1]);
+        swap16(w[2], w[3]);
+        swap32(w[0], w[2]);
+        swap32(w[1], w[3]);
+        const int n = ncol + (i + (lane >> 4)) * 16;
+        if (t >= a.T || n >= N) continue;
+        if (n + 16 <= N) __builtin_memcpy(row + n, w, 16);
         else
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) row[n + e] = static_cast<uint8_t>(w[0] >> (8 * e));
+          for (int e = 0; n + e < N; ++e) row[n + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
       }
     }
   } else {
     using O = typename std::conditional<OUT == OUT_BF16, bf16_t, float>::type;
+    static_assert(MC % 2 == 0 || OUT == OUT_F32, "tiles in pairs");
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const int64_t t = t0 + (wt * MT + j) * 16 + (lane & 15);
-      if (t >= a.T) continue;
       O* row = static_cast<O*>(a.y) + t * a.y_stride;
 #pragma unroll
-      for (int i = 0; i < MC; ++i) {
-        const int n = ncol + i * 16 + cg;
-        float o[4];
+      for (int i = 0; i < MC; i += 2) {
+        float o[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (GATED) o[e] = gate(acc[i][j][e], acc[i + MC][j][e], a.act);
-          else o[e] = acc[i][j][e] + (a.bias && n + e < N ? a.bias[n + e] : 0.0f);
-        }
-        if (n + 4 <= N) {
-          if constexpr (OUT == OUT_BF16) {
-            const uint32_t w[2] = {
-                static_cast<uint32_t>(f32_to_bf16(o[0])) | (static_cast<uint32_t>(f32_to_bf16(o[1])) << 16),
-                static_cast<uint32_t>(f32_to_bf16(o[2])) | (static_cast<uint32_t>(f32_to_bf16(o[3])) << 16)};
-            __builtin_memcpy(row + n, w, 8);
-          } else {
-            __builtin_memcpy(row + n, o, 16);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = ncol + (i + q) * 16 + cg + e;
+            if constexpr (GATED) o[q][e] = gate(acc[i + q][j][e], acc[i + q + MC][j][e], a.act);
+            else o[q][e] = acc[i + q][j][e] + (a.bias && n < N ? a.bias[n] : 0.0f);
           }
+        if constexpr (OUT == OUT_BF16) {
+          // 16-byte stores: even lane groups g take columns 4g .. 4g + 7 of the first
+          // tile, odd ones 4(g - 1) .. of the second
+          uint32_t w[2][2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              w[q][e] = static_cast<uint32_t>(f32_to_bf16(o[q][2 * e])) |
+                        (static_cast<uint32_t>(f32_to_bf16(o[q][2 * e + 1])) << 16);
+          swap16(w[0][0], w[1][0]);
+          swap16(w[0][1], w[1][1]);
+          const uint32_t v[4] = {w[0][0], w[0][1], w[1][0], w[1][1]};
+          const int g = lane >> 4, n = ncol + (i + (g & 1)) * 16 + (g >> 1) * 8;
+          if (t >= a.T || n >= N) continue;
+          if (n + 8 <= N) __builtin_memcpy(row + n, v, 16);
+          else
+            for (int e = 0; n + e < N; ++e) row[n + e] = static_cast<bf16_t>(v[e >> 1] >> (16 * (e & 1)));
         } else {
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) Io<O>::st(row, n + e, o[e]);
+          if (t >= a.T) continue;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int n = ncol + (i + q) * 16 + cg;
+            if (n + 4 <= N) __builtin_memcpy(row + n, o[q], 16);
+            else
+              for (int e = 0; e < 4; ++e)
+                if (n + e < N) row[n + e] = o[q][e];
+          }
         }
       }
     }

@@ -109,6 +109,20 @@ def test_linear(T, K, N, group, dtype, bias):
     assert (e <= tol + half(dtype) * (np.abs(want) + tol)).all(), (e - tol).max()
 
 
+@pytest.mark.parametrize("T,K,N", [
+    (2100, 128, 3700), (2100, 272, 3700), (2100, 400, 3800), (2060, 112, 3800),    # the largest tiles, one to four runs
+    (2100, 272, 2100), (700, 1040, 2000), (700, 1024, 2000), (130, 1168, 520), (40, 528, 640)])  # shared K
+@pytest.mark.parametrize("group,dtype", [(128, BF), (0, F32)])
+def test_linear_tiles(T, K, N, group, dtype):
+    rng = np.random.default_rng(T + K + N)
+    x, xs, ws = operands(rng, T, K, N, group)
+    y = G.linear_fp8(*to_gpu(x, xs, ws), dtype=dtype)
+    want, size = ref.product(x, xs, *ws[0])
+    tol = sum_error(K, size, dtype)
+    e = np.abs(to_f64(y) - want)
+    assert (e <= tol + half(dtype) * (np.abs(want) + tol)).all(), (e - tol).max()
+
+
 def check_gated(x, xs, ws, act, got, dtype):
     K = x.shape[1]
     g, gsize = ref.product(x, xs, *ws[0])
@@ -151,6 +165,16 @@ def test_gated(T, K, N, act, dtype, group):
     xs = xs / f32(60 * math.sqrt(K))
     got = G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=dtype or F8)
     check_gated(x, xs, ws, act, got, dtype)
+
+
+@pytest.mark.parametrize("T,K,N,act,dtype", [
+    (2100, 400, 1900, "none", BF), (2100, 272, 1900, "silu", F32), (5200, 144, 2500, "gelu", None),
+    (700, 1040, 1000, "gelu", BF), (700, 1040, 1000, "gelu", None), (2000, 128, 1100, "silu", BF)])
+def test_gated_tiles(T, K, N, act, dtype):
+    rng = np.random.default_rng(T + K + N)
+    x, xs, ws = operands(rng, T, K, N, 128, 2)
+    xs = xs / f32(60 * math.sqrt(K))
+    check_gated(x, xs, ws, act, G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=dtype or F8), dtype)
 
 
 @pytest.mark.parametrize("T", [3, 40, 600])
