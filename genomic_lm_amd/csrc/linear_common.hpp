@@ -102,4 +102,48 @@ __device__ __forceinline__ void to_codes(const float (&x)[N], float scale, uint3
   for (int e = 0; e < N; e += 4) w[e / 4] = fp8x4(z[e], z[e + 1], z[e + 2], z[e + 3]);
 }
 
+// LDS place of 16-byte chunk c of row r: any 8 and any 16 consecutive rows have
+// their chunks c in different banks.
+__device__ __forceinline__ int slot(int r, int c) {
+  return r * 8 + (c ^ (r & 7) ^ ((r >> 3) & 1));
+}
+
+// A lane's two chunks of row lane % 16 of a tile of 16 rows.
+__device__ __forceinline__ i32x8 tile_codes(const uint8_t* tile, int lane) {
+  const int r = lane & 15, c = (lane >> 4) * 2, swz = (r & 7) ^ (r >> 3);
+  return pair16(*reinterpret_cast<const i32x4*>(tile + r * RUN + (c ^ swz) * 16),
+                *reinterpret_cast<const i32x4*>(tile + r * RUN + ((c + 1) ^ swz) * 16));
+}
+
+typedef __attribute__((address_space(3))) void lds_ptr;
+
+// A wave's value where the compiler has not seen that it is one.
+__device__ __forceinline__ uint64_t scalar(const void* p) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
+  return lo | (static_cast<uint64_t>(hi) << 32);
+}
+// 16 bytes (4) per lane from base + off straight into LDS, lane l at dst + 16 l (4 l);
+// base and dst are the wave's.  Written as assembly so that the compiler, which cannot tell
+// the halves of the LDS buffer apart, does not make every LDS read of one half wait for the
+// loads into the other; the kernels wait for them themselves.  They write no vector
+// registers; m0 is the compiler's only where it sets it itself, just before the use.
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(off), "s"(scalar(base))
+               : "memory");
+}
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+               "v"(off), "s"(scalar(base))
+               : "memory");
+}
+// All but N of this wave's loads have arrived.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 }  // namespace hyena

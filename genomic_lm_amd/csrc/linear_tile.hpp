@@ -12,12 +12,6 @@ __device__ __forceinline__ void tile_sync() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// LDS place of 16-byte chunk c of row r: any 8 and any 16 consecutive rows have
-// their chunks c in different banks.
-__device__ __forceinline__ int slot(int r, int c) {
-  return r * 8 + (c ^ (r & 7) ^ ((r >> 3) & 1));
-}
-
 // Tile (row, column) of this workgroup.  Workgroups of one XCD (every eighth)
 // take neighbouring tiles, in groups of up to 8 tile rows, so that they share
 // operands in its L2.
@@ -57,7 +51,7 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
   const int N = a.N;
   const int cg = 4 * (lane >> 4);
   if constexpr (OUT == OUT_FP8) {
-    static_assert(GATED && MC % 4 == 0, "codes come from the gated product");
+    static_assert(GATED, "codes come from the gated product");
     float* top = reinterpret_cast<float*>(sh);          // [WN][BT]
     constexpr int GW = RUN / (MC * 16);                 // waves that share a run of columns
     float h[MC][MT][4];
@@ -94,25 +88,38 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
       const float scale = run_scale(m);
       if (wn % GW == 0 && lane < 16 && ncol < N && t < a.T) a.q_scale[t * runs + ncol / RUN] = scale;
       uint8_t* row = static_cast<uint8_t*>(a.y) + t * a.y_stride;
+      if constexpr (MC % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < MC; i += 4) {
-        // lane group g holds words g of four tiles; afterwards the four words of tile g
-        uint32_t w[4];
+        for (int i = 0; i < MC; i += 4) {
+          // lane group g holds words g of four tiles; afterwards the four words of tile g
+          uint32_t w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t c[1];
-          to_codes<4>(h[i + q][j], scale, c);
-          w[q] = c[0];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t c[1];
+            to_codes<4>(h[i + q][j], scale, c);
+            w[q] = c[0];
+          }
+          swap16(w[0], w[1]);
+          swap16(w[2], w[3]);
+          swap32(w[0], w[2]);
+          swap32(w[1], w[3]);
+          const int n = ncol + (i + (lane >> 4)) * 16;
+          if (t >= a.T || n >= N) continue;
+          if (n + 16 <= N) __builtin_memcpy(row + n, w, 16);
+          else
+            for (int e = 0; n + e < N; ++e) row[n + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
         }
-        swap16(w[0], w[1]);
-        swap16(w[2], w[3]);
-        swap32(w[0], w[2]);
-        swap32(w[1], w[3]);
-        const int n = ncol + (i + (lane >> 4)) * 16;
-        if (t >= a.T || n >= N) continue;
-        if (n + 16 <= N) __builtin_memcpy(row + n, w, 16);
-        else
-          for (int e = 0; n + e < N; ++e) row[n + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+      } else if (t < a.T) {
+#pragma unroll
+        for (int i = 0; i < MC; ++i) {
+          uint32_t w[1];
+          to_codes<4>(h[i][j], scale, w);
+          const int n = ncol + i * 16 + cg;
+          if (n + 4 <= N) __builtin_memcpy(row + n, w, 4);
+          else
+            for (int e = 0; e < 4; ++e)
+              if (n + e < N) row[n + e] = static_cast<uint8_t>(w[0] >> (8 * e));
+        }
       }
     }
   } else {
