@@ -221,10 +221,11 @@ static void few_dma_go(const LinearArgs& a) {
   linear_few_dma_kernel<WK, MT, NI, GATED, OUT>
       <<<static_cast<unsigned>((a.N + NI * 16 - 1) / (NI * 16)), WK * 64, 0, a.stream>>>(a);
 }
-// Eight waves to a workgroup where there are few; four, with more workgroups to a CU, and then two
-// tiles of columns for each reading of more than 16 tokens, where there are many.  Measured (us):
+// Eight waves to a workgroup where there are few; four, with more workgroups to a CU, and two
+// tiles of columns for each reading of the tokens, where there are many.  Measured (us, weights
+// from the last-level cache unless said):
 // 16 x 11008 to 4096 (256 workgroups) 10.0 with eight waves, 11.1 with four; 1 x 4096 to 12288
-// (768) 11.0, 9.2; 32 x 4096 to 12288 13.5 with one tile of columns, 12.0 with two, to 4096 6.5, 7.4;
+// from HBM 12.9 with two tiles, 13.9 with one, 14.0 with eight waves; 32 x 4096 to 12288 13.5 with one tile of columns, 12.0 with two, to 4096 6.5, 7.4;
 // 64 x 4096 to 12288 22.6, 20.4, to 4096 8.6, 10.5.
 template <bool GATED, int OUT>
 static void few_pick(const LinearArgs& a) {
@@ -232,7 +233,8 @@ static void few_pick(const LinearArgs& a) {
   if (!linear_dma_takes(a))
     linear_few_kernel<8, 1, 4, GATED, OUT><<<static_cast<unsigned>((a.N + 15) / 16), 512, 0, a.stream>>>(a);
   else if (a.T <= 16) {
-    if (many) few_dma_go<4, 1, 1, GATED, OUT>(a);
+    if (!GATED && many) few_dma_go<4, 1, 2, false, OUT>(a);
+    else if (many) few_dma_go<4, 1, 1, GATED, OUT>(a);
     else few_dma_go<8, 1, 1, GATED, OUT>(a);
   } else if (a.T <= 32) {
     if (!GATED && many) few_dma_go<4, 2, 2, false, OUT>(a);

@@ -12,6 +12,8 @@ per block of 128 x 128, as quantize_weight_fp8 gives them.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _ACT_DTYPES, BF16, F32, _check, _io, _stream, lib
@@ -47,17 +49,15 @@ def _operand(x, x_scale):
     rows, K = x.shape[:-1], x.shape[-1]
     runs = (K + NORM_GROUP - 1) // NORM_GROUP
     if x_scale.shape == (*rows, runs):
-        step, group = _one_stride("x_scale", x_scale), NORM_GROUP
+        step, group = runs if x_scale.is_contiguous() else _one_stride("x_scale", x_scale), NORM_GROUP
     elif x_scale.shape == rows:
         # one scale per row: rows at one stride
         step = 1 if x_scale.is_contiguous() else _one_stride("x_scale", x_scale[..., None])
         group = 0
     else:
         raise ValueError(f"x_scale must have shape {tuple(rows)} or {(*rows, runs)}, got {tuple(x_scale.shape)}")
-    T = 1
-    for n in rows:
-        T *= n
-    return (x.data_ptr(), _one_stride("x", x), x_scale.data_ptr(), step, group), T, K, rows
+    T = rows[0] if len(rows) == 1 else math.prod(rows)
+    return (x.data_ptr(), K if x.is_contiguous() else _one_stride("x", x), x_scale.data_ptr(), step, group), T, K, rows
 
 
 def _weight(name, w, scale, K, dev, N=None):
@@ -75,7 +75,7 @@ def _out(name, out, x, rows, N, dtype):
     if out is None:
         if dtype not in _ACT_DTYPES:
             raise TypeError("dtype must be bfloat16 or float32")
-        out = torch.empty((*rows, N), dtype=dtype, device=x.device)
+        out = x.new_empty((*rows, N), dtype=dtype)
         return out.data_ptr(), N, F32 if dtype is torch.float32 else BF16, out
     p, s = _rows(name, out)
     if tuple(out.shape) != (*rows, N) or out.get_device() != x.get_device():
@@ -113,12 +113,16 @@ def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = 
     up, _ = _weight("w_up", w_up, up_scale, K, dev, N)
     if dtype in _FP8:
         sshape = (*rows, (N + NORM_GROUP - 1) // NORM_GROUP)
-        if out is None:
-            out = torch.empty((*rows, N), dtype=dtype, device=x.device)
+        if out is None:                    # what is made here needs no check
+            out = x.new_empty((*rows, N), dtype=dtype)
+            qp = out.data_ptr()
+        else:
+            qp = _vec("out", out, out.dtype if getattr(out, "dtype", None) in _FP8 else dtype, (*rows, N), dev)
         if scale is None:
-            scale = torch.empty(sshape, dtype=torch.float32, device=x.device)
-        qp = _vec("out", out, out.dtype if getattr(out, "dtype", None) in _FP8 else dtype, (*rows, N), dev)
-        sp = _vec("scale", scale, torch.float32, sshape, dev)
+            scale = x.new_empty(sshape, dtype=torch.float32)
+            sp = scale.data_ptr()
+        else:
+            sp = _vec("scale", scale, torch.float32, sshape, dev)
         _check("hyena_gated_linear_fp8_quant", lib().hyena_gated_linear_fp8_quant(
             *head, *gp, *up, ACTS[act], qp, sp, T, N, K, _stream(x)))
         return out, scale
@@ -217,15 +221,15 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=No
         raise ValueError("q_weight and k_weight go with a norm: give eps")
     qw = None if q_weight is None else _vec("q_weight", q_weight, torch.float32, (DH,), dev)
     kw = None if k_weight is None else _vec("k_weight", k_weight, torch.float32, (DH,), dev)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if q_out is None:                      # what is made here needs no check
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qo = (q_out.data_ptr(), Hq * DH, DH)
     else:
         qo = _same("q_out", q_out, q)
     ko = (None, 0, 0)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
             ko = (k_out.data_ptr(), Hk * DH, DH)
         else:
             ko = _same("k_out", k_out, k)
