@@ -1,15 +1,19 @@
 """A small striped stack served with a paged 8-bit cache.
 
 Runs the library's operators together the way a server of a StripedHyena 2 model
-uses them (random weights, no rotary embedding, one mixer per block):
+uses them (random weights, one mixer per block), every projection in 8 bits:
 
-    page_map                     once per step: tables and slots of the new tokens
+    page_map                     once per step: tables, slots and positions of the new tokens
     per block:
       add_rmsnorm_fp8            residual addition, norm, 8-bit input of in_proj
-      in_proj                    a matrix product (torch)
+      linear_fp8                 in_proj
       h: chunk_fwd_tokmajor      the modal Hyena mixer, its state carried per request
-      a: kv_append_fp8 + attn_paged_fp8   attention over the cache
-      out_proj                   a matrix product (torch)
+      a: qk_norm_rope            norms of the query and key heads, rotary positions, in place
+         kv_append_fp8 + attn_paged_fp8   attention over the cache
+      quantize_fp8 + linear_fp8  out_proj
+      add_rmsnorm_fp8            residual addition, norm, 8-bit input of the MLP
+      gated_linear_fp8           both projections, gelu and product, 8-bit output
+      linear_fp8                 the MLP's last projection
     add_rmsnorm                  final norm, then the unembedding (torch)
 
 Prompts of different lengths are prefilled in chunks, then all requests decode
@@ -43,9 +47,16 @@ class StripedServer:
         rand = lambda *s, scale=1.0: (torch.randn(s, generator=g) * scale).to(device)  # noqa: E731
         self.pattern, self.dim, self.heads, self.page, self.device = pattern, dim, heads, page, device
         self.embed = rand(vocab, dim).to(BF)
-        self.norms = [1 + rand(dim, scale=0.1) for _ in range(len(pattern) + 1)]
-        self.w_in = [rand(3 * dim, dim, scale=dim ** -0.5).to(BF) for _ in pattern]
-        self.w_out = [rand(dim, dim, scale=dim ** -0.5).to(BF) for _ in pattern]
+        self.norms = [1 + rand(dim, scale=0.1) for _ in range(2 * len(pattern) + 1)]
+        inner = -(-11 * dim // 64) * 16                 # 2.75 dim, in whole 16 columns
+        # weights in 8 bits with their scales, quantised once
+        weight = lambda *s: G.quantize_weight_fp8(rand(*s, scale=s[1] ** -0.5))  # noqa: E731
+        self.w_in = [weight(3 * dim, dim) for _ in pattern]
+        self.w_out = [weight(dim, dim) for _ in pattern]
+        self.w_gate, self.w_up = ([weight(inner, dim) for _ in pattern] for _ in range(2))
+        self.w_down = [weight(dim, inner) for _ in pattern]
+        self.head_norms = [[1 + rand(dim // heads, scale=0.1) for _ in "qk"] for _ in pattern]
+        self.inv_freq = G.rotary_inv_freq(dim // heads, device=device)
         # poles with memories of one to a thousand tokens
         self.log_poles = [-torch.exp(torch.rand((dim, modes), generator=g) * -6.9).to(device) for _ in pattern]
         self.residues = [rand(dim, modes, scale=modes ** -0.5) for _ in pattern]
@@ -78,8 +89,9 @@ class StripedServer:
             at += n
         return out
 
-    def _attention(self, i, proj, cu, lens, slots, most):
+    def _attention(self, i, proj, cu, lens, positions, slots, most):
         q, k, v = proj.view(-1, 3, self.heads, self.dim // self.heads).unbind(1)
+        G.qk_norm_rope(q, k, positions, self.inv_freq, *self.head_norms[i], eps=1e-6, q_out=q, k_out=k)
         G.kv_append_fp8(k, v, slots, *self.caches[i])
         o = G.attn_paged_fp8(q, *self.caches[i], self.table, lens, cu, most)
         return o.view(-1, self.dim)
@@ -89,16 +101,20 @@ class StripedServer:
         Returns the normed hidden state of every new token and the logits of each last one."""
         tokens = sum(new)
         brings = torch.tensor(new, dtype=torch.int32).to(self.device)
-        cu, lens, _, slots, status = G.page_map(self.lens, brings, self.table, self.free, self.head,
-                                                self.page, tokens)
+        cu, lens, positions, slots, status = G.page_map(self.lens, brings, self.table, self.free, self.head,
+                                                        self.page, tokens)
         x, res = self.embed[ids], None
         for i, kind in enumerate(self.pattern):
-            q, scale, summed = G.add_rmsnorm_fp8(x, self.norms[i], res)
+            q, scale, summed = G.add_rmsnorm_fp8(x, self.norms[2 * i], res, group=128)
             res = x if summed is None else summed
-            proj = ((q.to(BF) @ self.w_in[i].t()) * scale[:, None]).to(BF)
+            proj = G.linear_fp8(q, scale, *self.w_in[i])
             y = (self._hyena(i, proj, new) if kind == "h"
-                 else self._attention(i, proj, cu, lens, slots, max(new)))
-            x = y @ self.w_out[i].t()
+                 else self._attention(i, proj, cu, lens, positions, slots, max(new)))
+            x = G.linear_fp8(*G.quantize_fp8(y, group=128), *self.w_out[i])
+            q, scale, res = G.add_rmsnorm_fp8(x, self.norms[2 * i + 1], res, group=128)
+            q, scale = G.gated_linear_fp8(q, scale, *self.w_gate[i], *self.w_up[i], act="gelu",
+                                          dtype=torch.float8_e4m3fn)
+            x = G.linear_fp8(q, scale, *self.w_down[i])
         hidden, _ = G.add_rmsnorm(x, self.norms[-1], res)
         self.lens, self.head = lens, status[:1].clone()
         self.unplaced += status[1:]           # tokens without a page: looked at when the host next waits
