@@ -71,13 +71,34 @@ __device__ __forceinline__ i32x4 codes16(const uint8_t* p, int n) {
   return v;
 }
 
-// act(g) * u.  Forms without a difference of near equals: the gelu as g erfc(-g / sqrt 2) / 2,
-// its tanh form as g / (1 + exp(-2 z)).
+// act(g) * u, in forms without a difference of near equals.
+//
+// The gelu is g Phi(g), Phi(-|g|) = exp(-g^2 / 2) erfcx(|g| / sqrt 2) / 2, where erfcx(z) =
+// exp(z^2) erfc(z) = t q(t), t = 1 / (1 + 0.35 z), with a polynomial q fitted over all z >= 0 to
+// a relative 2.4e-8 (least squares at Chebyshev points, reweighted towards the largest error).  About
+// 20 instructions; the device library's erfc, ten times that, took a fifth of the time of a gated
+// product of 8192 x 4096 to 11008.
 __device__ __forceinline__ float gate(float g, float u, int act) {
-  if (act == ACT_GELU) g = 0.5f * g * erfcf(g * -0.70710678118654752f);
-  else if (act == ACT_GELU_TANH)
-    g = g / (1.0f + expf(-1.5957691216057308f * fmaf(0.044715f * g * g, g, g)));
-  else if (act == ACT_SILU) g = g / (1.0f + expf(-g));
+  if (act == ACT_GELU) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.24748737341529164f, 1.0f));
+    float q = 0.007330488879233599f;
+    q = fmaf(q, t, 0.005140664987266064f);
+    q = fmaf(q, t, -0.10037992149591446f);
+    q = fmaf(q, t, 0.13765418529510498f);
+    q = fmaf(q, t, -0.02970522828400135f);
+    q = fmaf(q, t, 0.11713682115077972f);
+    q = fmaf(q, t, 0.12056729942560196f);
+    q = fmaf(q, t, 0.16200152039527893f);
+    q = fmaf(q, t, 0.18532025814056396f);
+    q = fmaf(q, t, 0.19746758043766022f);
+    q = fmaf(q, t, 0.19746634364128113f);
+    const float h = 0.5f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f) * (q * t);
+    g *= g < 0.0f ? h : 1.0f - h;
+  } else if (act == ACT_GELU_TANH) {           // g / (1 + exp(-2 z)); 2 sqrt(2 / pi) log2 e
+    g *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-2.3022081982148305f * fmaf(0.044715f * g * g, g, g)));
+  } else if (act == ACT_SILU) {
+    g *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+  }
   return g * u;
 }
 
