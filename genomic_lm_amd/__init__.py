@@ -65,7 +65,8 @@ __all__ = [
     "chunk_fwd_tokmajor", "chunk_tokmajor_workspace_size", "fir_fwd_tokmajor",
     "add_rmsnorm", "add_rmsnorm_fp8", "page_map", "kv_append_fp8",
     "attn_paged_fp8", "attn_paged_workspace_size",
-    "linear_fp8", "gated_linear_fp8", "quantize_fp8", "quantize_weight_fp8", "rotary_inv_freq", "qk_norm_rope",
+    "linear_fp8", "gated_linear_fp8", "gated_linear_fp8_workspace_size", "quantize_fp8",
+    "quantize_weight_fp8", "rotary_inv_freq", "qk_norm_rope",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_WORKSPACE", "ERR_LAUNCH",
     "F32", "BF16", "ALGOS", "EXPORTS",
 ]
@@ -136,7 +137,8 @@ EXPORTS = {
     "hyena_gated_linear_fp8": (_int, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _int, _p, _i64, _i64,
                                       _i64, _i64, _int, _p]),
     "hyena_gated_linear_fp8_quant": (_int, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _int, _p, _p, _i64,
-                                            _i64, _i64, _p]),
+                                            _i64, _i64, _p, _size, _p]),
+    "hyena_gated_linear_fp8_workspace_size": (_size, [_i64, _i64, _i64]),
     "hyena_quantize_fp8": (_int, [_p, _i64, _p, _p, _i64, _i64, _i64, _int, _p]),
     "hyena_quantize_weight_fp8": (_int, [_p, _i64, _p, _p, _i64, _i64, _int, _p]),
     "hyena_qk_norm_rope": (_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, ctypes.c_int32,
@@ -609,8 +611,8 @@ def fir_fwd_tokmajor(xin, taps, skip=None, window_in=None, pos=(0, 1, 2), out=No
 
 from .serving import (add_rmsnorm, add_rmsnorm_fp8, page_map, kv_append_fp8,  # noqa: E402
                       attn_paged_fp8, attn_paged_workspace_size)
-from .projection import (linear_fp8, gated_linear_fp8, quantize_fp8, quantize_weight_fp8,  # noqa: E402
-                         rotary_inv_freq, qk_norm_rope)
+from .projection import (linear_fp8, gated_linear_fp8, gated_linear_fp8_workspace_size,  # noqa: E402
+                         quantize_fp8, quantize_weight_fp8, rotary_inv_freq, qk_norm_rope)
 
 # The same functions under the names of the C entry points they call
 # (chunk_fwd / chunk_fwd_cpx call the *_algo entry point when algo is not
@@ -639,6 +641,7 @@ hyena_attn_paged_workspace_size = attn_paged_workspace_size
 hyena_linear_fp8 = linear_fp8
 hyena_gated_linear_fp8 = gated_linear_fp8
 hyena_gated_linear_fp8_quant = functools.partial(gated_linear_fp8, dtype=torch.float8_e4m3fn)
+hyena_gated_linear_fp8_workspace_size = gated_linear_fp8_workspace_size
 hyena_quantize_fp8 = quantize_fp8
 hyena_quantize_weight_fp8 = quantize_weight_fp8
 hyena_qk_norm_rope = qk_norm_rope

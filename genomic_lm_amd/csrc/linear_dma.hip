@@ -19,10 +19,10 @@ struct Loads {
   static constexpr int NW = WT * WN;
   static constexpr int BT = WT * MT * 16, BN = WN * MN * 16;
   static constexpr int CN = GATED ? BN / 2 : BN, MC = GATED ? MN / 2 : MN;   // columns of the output
-  static constexpr int RX = (BT + NW * 8 - 1) / (NW * 8), RW = BN / (NW * 8);   // loads of eight rows each
-  static constexpr int XW = (BT + 63) / 64;                                  // waves for the tokens' scales
+  static constexpr int RX = BT / (NW * 8), RW = BN / (NW * 8);               // loads of eight rows each
+  static constexpr int XW = BT / 64;                                         // waves for the tokens' scales
   static constexpr int LOADS = RX + RW + 1;                                  // of a wave and run
-  static_assert((BT % (NW * 8) == 0 || NW % (BT / 8) == 0) && BN % (NW * 8) == 0, "whole loads");
+  static_assert(BT % (NW * 8) == 0 && BN % (NW * 8) == 0 && BT % 64 == 0, "whole loads");
   static_assert(NW > XW + (GATED ? 1 : 0), "waves for all scales");
   static_assert(RUN % (MC * 16) == 0, "a wave's columns lie in one block of the scales");
   static_assert(NW % 2 == 0, "a wave's eight rows are all even or all odd ones");
@@ -42,7 +42,7 @@ struct Loads {
     bx = a.x + t0 * a.x_stride;
 #pragma unroll
     for (int i = 0; i < RX; ++i) {
-      const int r = token_rows(i) + lrow;
+      const int r = (i * NW + wave) * 8 + lrow;
       ox[i] = static_cast<uint32_t>(r < rows ? r : rows - 1) * static_cast<uint32_t>(a.x_stride) + chunk;
       asm volatile("" : "+v"(ox[i]));                    // 32 bits, not the 64 of the product
     }
@@ -79,14 +79,12 @@ struct Loads {
       ds = SB + (XW + which) * 256;
     }
   }
-  // first row of the wave's load i; few tokens are loaded by several waves
-  __device__ __forceinline__ int token_rows(int i) const { return (i * NW + wave) % (BT / 8) * 8; }
   __device__ __forceinline__ void scales(int kb, uint32_t to) const {
     dma4(bs + static_cast<int64_t>(kb) * step, os, to + ds);
   }
   __device__ __forceinline__ void tokens(int kb, uint32_t to) const {
 #pragma unroll
-    for (int i = 0; i < RX; ++i) dma16(bx + kb * RUN, ox[i], to + token_rows(i) * RUN);
+    for (int i = 0; i < RX; ++i) dma16(bx + kb * RUN, ox[i], to + (i * NW + wave) * 1024);
   }
   template <int FIRST, int EVERY>
   __device__ __forceinline__ void weights(int kb, uint32_t to) const {
@@ -96,30 +94,27 @@ struct Loads {
   // the lane's chunks of a run that K does not reach (it is a multiple of 16): zeros
   __device__ __forceinline__ void clear(uint8_t* buf, int lane) const {
     const i32x4 zero = {0, 0, 0, 0};
-    i32x4* const z = reinterpret_cast<i32x4*>(buf) + lane;
+    i32x4* const z = reinterpret_cast<i32x4*>(buf + wave * 1024) + lane;
 #pragma unroll
-    for (int i = 0; i < RX; ++i) z[token_rows(i) * 8] = zero;
-#pragma unroll
-    for (int i = 0; i < RW; ++i) z[XB / 16 + (i * NW + wave) * 64] = zero;
+    for (int i = 0; i < RX + RW; ++i) z[i * NW * 64] = zero;
   }
 };
 
-// KG groups of WT x WN waves share a tile and take turns at the runs of K, of which each group has
-// S in LDS.
-template <int WT, int WN, int MT, int MN, int KG, int S, bool GATED, int OUT>
+// KG groups of WT x WN waves share a tile and take turns at the runs of K.
+template <int WT, int WN, int MT, int MN, int KG, bool GATED, int OUT>
 __global__ __launch_bounds__(WT * WN * KG * 64) void linear_dma_kernel(LinearArgs a, int tiles_t, int tiles_n) {
   using L = Loads<WT, WN, MT, MN, GATED>;
   constexpr int NW = L::NW, MC = L::MC, BUF = L::BUF;
   constexpr bool WIDE = OUT != OUT_BF16;                 // Frag says why
   constexpr int JOIN = (KG - 1) * NW * MN * MT * 1024;   // the other groups' sums
   constexpr int TOPS = OUT == OUT_FP8 ? WN * L::BT * 4 : 0;
-  __shared__ __attribute__((aligned(16))) uint8_t sh[S * KG * BUF > JOIN + TOPS ? S * KG * BUF : JOIN + TOPS];
+  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * KG * BUF > JOIN + TOPS ? 2 * KG * BUF : JOIN + TOPS];
 
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave_of_all = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int kg = wave_of_all / NW, wave = wave_of_all % NW;
   const int wt = wave / WN, wn = wave % WN;
-  uint8_t* const mine = sh + kg * S * BUF;
+  uint8_t* const mine = sh + kg * 2 * BUF;
   const uint32_t mine0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr*)(mine)));
   int ti, ni;
   tile_of(tiles_t, tiles_n, ti, ni);
@@ -145,17 +140,12 @@ __global__ __launch_bounds__(WT * WN * KG * 64) void linear_dma_kernel(LinearArg
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // the last S - 2 runs asked for may still be on their way
-  constexpr int FLY = (S - 2) * L::LOADS;
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i)
-    if (kg + i * KG < blocks) stage(kg + i * KG, i);
-  if (S > 2 && kg + (S - 2) * KG < blocks) dma_sync<FLY>();
-  else dma_sync<0>();
+  if (kg < blocks) stage(kg, 0);
+  dma_sync<0>();
   int buf = 0;
   for (int k0 = 0; k0 < blocks; k0 += KG) {
-    const int kb = k0 + kg, ask = kb + (S - 1) * KG;
-    if (ask < blocks) stage(ask, S == 2 ? buf ^ 1 : buf == 0 ? S - 1 : buf - 1);
+    const int kb = k0 + kg;
+    if (kb + KG < blocks) stage(kb + KG, buf ^ 1);
     if (KG == 1 || kb < blocks) {
       const uint8_t* const b = mine + buf * BUF;
       const float* const st = reinterpret_cast<const float*>(b + L::SB) + wt * MT * 16 + (lane & 15);
@@ -184,27 +174,11 @@ __global__ __launch_bounds__(WT * WN * KG * 64) void linear_dma_kernel(LinearArg
         }
       }
     }
-    buf = S == 2 ? buf ^ 1 : buf == S - 1 ? 0 : buf + 1;
-    if (S > 2 && ask < blocks) dma_sync<FLY>();
-    else dma_sync<0>();
+    buf ^= 1;
+    dma_sync<0>();
   }
-  if constexpr (KG > 1) {                                // the groups' sums, in their order
-    f32x4* const join = reinterpret_cast<f32x4*>(sh) + wave * (MN * MT * 64) + lane;
-    if (kg > 0) {
-#pragma unroll
-      for (int i = 0; i < MN; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) join[((kg - 1) * NW * MN * MT + i * MT + j) * 64] = acc[i][j];
-    }
-    tile_sync();
-    if (kg > 0) return;
-#pragma unroll
-    for (int g = 0; g < KG - 1; ++g)
-#pragma unroll
-      for (int i = 0; i < MN; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) acc[i][j] += join[(g * NW * MN * MT + i * MT + j) * 64];
-  }
+  if constexpr (KG > 1) join_groups<KG, NW, MT, MN>(acc, sh, kg, wave, lane);
+  if (kg > 0) return;
   tile_epilogue<WT, WN, MT, MN, GATED, OUT>(a, acc, t0, n0 + wn * (MC * 16), wt, wn, lane, sh + JOIN);
 }
 
@@ -343,10 +317,10 @@ static int64_t tiles(const LinearArgs& a) {
   return (a.T + BT - 1) / BT * ((a.N + CN - 1) / CN);
 }
 
-template <int WT, int WN, int MT, int MN, int KG, int S, bool GATED, int OUT>
+template <int WT, int WN, int MT, int MN, int KG, bool GATED, int OUT>
 static void dma_go(const LinearArgs& a) {
   constexpr int BT = WT * MT * 16, CN = WN * MN * 16 / (GATED ? 2 : 1);
-  linear_dma_kernel<WT, WN, MT, MN, KG, S, GATED, OUT>
+  linear_dma_kernel<WT, WN, MT, MN, KG, GATED, OUT>
       <<<static_cast<unsigned>(tiles<BT, CN>(a)), WT * WN * KG * 64, 0, a.stream>>>(
           a, static_cast<int>((a.T + BT - 1) / BT), static_cast<int>((a.N + CN - 1) / CN));
 }
@@ -358,35 +332,31 @@ bool linear_dma_takes(const LinearArgs& a) {
          a.x_stride < (1 << 23) && a.xs_row < (1 << 21);
 }
 
-// The largest tiles where they fill most of the 256 CUs, each with one workgroup; smaller ones,
-// whose K two or four groups of waves share, where they do not.  Measured (us, bf16 outputs, the
-// tile that is taken against the next): 8192 x 12288 x 4096 256 x 256 384, 128 x 128 486; 1024 x
-// 12288 (192 tiles) 72, 91; 512 x 12288 (384 tiles of 128 x 128) 54 by one group, 62 by two, 59 by
-// 256 x 256; 512 x 4096 (128) 41, 32 by two groups, 37 by 64 x 64; 256 x 4096 (64) 28, 64 x 64 by
-// four groups 26; 64 x 4096 25, 15.
+// Tiles by the rounds of workgroups that they make on 256 CUs: one of 256 x 256 to a CU, two of 128 x
+// 128, whose round takes 0.68 of the time of one of the former.  Where there is less than a round,
+// two or four groups of waves share the K of a tile.  Measured (us, bf16 outputs, the tile that
+// is taken against the next): 8192 x 12288 x 4096 256 x 256 384, 128 x 128 486; 1024 x 12288 (192 and
+// 768 tiles) 72, 91; 512 x 12288 (96, 384) 128 x 128 54, 59; 512 x 4096 (128 of 128 x 128) 32 by two
+// groups, 41 by one, 37 by 64 x 64; 256 x 4096 (64) 28, 64 x 64 by four groups 26.
 template <bool GATED, int OUT>
 static void dma_pick(const LinearArgs& a) {
   const int64_t n256 = tiles<256, GATED ? 128 : 256>(a), n128 = tiles<128, GATED ? 64 : 128>(a);
   if constexpr (OUT == OUT_FP8) {
-    // a workgroup has whole runs of 128 columns: 8192 x 11008 x 4096 256 rows 1269, 128 rows 1500;
-    // 1000 x 10928 (344 tiles) 241, 231; 64 x 11008 128 rows 74, 64 rows 54
-    if (n256 >= 400) dma_go<4, 2, 4, 8, 1, 2, GATED, OUT>(a);
-    else if (a.T > 64) dma_go<4, 2, 2, 8, 1, 2, GATED, OUT>(a);
-    else if (a.T > 16) dma_go<4, 2, 1, 8, 1, 3, GATED, OUT>(a);
-    else dma_go<1, 8, 1, 2, 1, 4, GATED, OUT>(a);
-  } else if (n256 >= 128 && (OUT != OUT_BF16 || a.K >= RUN)) {
+    dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
+  } else if (n128 > 256 && 100 * ((n256 + 255) / 256) <= 68 * ((n128 + 511) / 512) &&
+             (OUT != OUT_BF16 || a.K >= RUN)) {
     if constexpr (OUT == OUT_BF16)
       linear_turns_kernel<GATED><<<static_cast<unsigned>(n256), 512, 0, a.stream>>>(
           a, static_cast<int>((a.T + 255) / 256), static_cast<int>(n256 / ((a.T + 255) / 256)));
-    else dma_go<4, 2, 4, 8, 1, 2, GATED, OUT>(a);
-  } else if (a.T > 64 && n128 > 256) {
-    dma_go<2, 2, 4, 4, 1, 2, GATED, OUT>(a);
-  } else if (a.T > 64 && n128 >= 90) {
-    dma_go<2, 2, 4, 4, 2, 2, GATED, OUT>(a);
+    else dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
+  } else if (n128 > 256) {
+    dma_go<2, 2, 4, 4, 1, GATED, OUT>(a);
+  } else if (n128 >= 90) {
+    dma_go<2, 2, 4, 4, 2, GATED, OUT>(a);
   } else if constexpr (GATED) {
-    dma_go<2, 2, 2, 4, 2, 2, GATED, OUT>(a);
+    dma_go<2, 2, 2, 4, 2, GATED, OUT>(a);
   } else {
-    dma_go<2, 2, 2, 2, 4, 2, GATED, OUT>(a);
+    dma_go<2, 2, 2, 2, 4, GATED, OUT>(a);
   }
 }
 

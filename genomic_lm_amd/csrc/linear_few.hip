@@ -1,4 +1,5 @@
-// linear_few.hip -- block-scaled e4m3 products of up to 64 rows (decode steps).
+// linear_few.hip -- block-scaled e4m3 products of few rows (decode steps) or few outputs, and the
+// choice among the products.
 #include "linear_common.hpp"
 
 namespace hyena {
@@ -37,6 +38,16 @@ __device__ __forceinline__ void few_join(const LinearArgs& a, const f32x4 (&acc)
   }
 }
 
+// The rows of the workgroup: R of them from R blockIdx.y on.
+template <int R, int OUT>
+__device__ __forceinline__ void few_rows(LinearArgs& a) {
+  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * R;
+  a.x += t0 * a.x_stride;
+  a.x_scale += t0 * a.xs_row;
+  a.y = static_cast<uint8_t*>(a.y) + t0 * a.y_stride * (OUT == OUT_BF16 ? 2 : 4);
+  a.T = a.T - t0 < R ? a.T - t0 : R;
+}
+
 // For rows of whole 16-byte chunks.  A wave has NI tiles of 16 columns (of each weight) and up to
 // 16 MT tokens, and takes every WK-th run of K, through a ring of two runs in LDS of its own,
 // filled straight from memory: loads of operands to registers, 16 rows in one instruction, pass
@@ -53,6 +64,7 @@ __global__ __launch_bounds__(WK * 64) void linear_few_dma_kernel(LinearArgs a) {
   const int tid = static_cast<int>(threadIdx.x);
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  few_rows<16 * MT, OUT>(a);
   uint8_t* const ring = sh + wave * (2 * BUF);
   const uint32_t ring0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr*)(ring)));
   const int n0 = static_cast<int>(blockIdx.x) * (NI * 16);
@@ -152,6 +164,7 @@ __global__ __launch_bounds__(WK * 64) void linear_few_kernel(LinearArgs a) {
   const int tid = static_cast<int>(threadIdx.x);
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  few_rows<16, OUT>(a);
   const int n0 = static_cast<int>(blockIdx.x) * (NI * 16);
   const int K = a.K, N = a.N, T = static_cast<int>(a.T);
   const int blocks = (K + RUN - 1) / RUN, full = K / RUN;
@@ -218,21 +231,23 @@ __global__ __launch_bounds__(WK * 64) void linear_few_kernel(LinearArgs a) {
 
 template <int WK, int MT, int NI, bool GATED, int OUT>
 static void few_dma_go(const LinearArgs& a) {
-  linear_few_dma_kernel<WK, MT, NI, GATED, OUT>
-      <<<static_cast<unsigned>((a.N + NI * 16 - 1) / (NI * 16)), WK * 64, 0, a.stream>>>(a);
+  const dim3 grid(static_cast<unsigned>((a.N + NI * 16 - 1) / (NI * 16)),
+                  static_cast<unsigned>((a.T + MT * 16 - 1) / (MT * 16)));
+  linear_few_dma_kernel<WK, MT, NI, GATED, OUT><<<grid, WK * 64, 0, a.stream>>>(a);
 }
 // Eight waves to a workgroup where there are few; four, with more workgroups to a CU, and two
 // tiles of columns for each reading of the tokens, where there are many.  Measured (us, weights
-// from the last-level cache unless said):
-// 16 x 11008 to 4096 (256 workgroups) 10.0 with eight waves, 11.1 with four; 1 x 4096 to 12288
-// from HBM 12.9 with two tiles, 13.9 with one, 14.0 with eight waves; 32 x 4096 to 12288 13.5 with one tile of columns, 12.0 with two, to 4096 6.5, 7.4;
-// 64 x 4096 to 12288 22.6, 20.4, to 4096 8.6, 10.5.
+// from the last-level cache unless said): 16 x 11008 to 4096 (256 workgroups)
+// 10.0 with eight waves, 11.1 with four; 1 x 4096 to 12288 from HBM 12.9 with two tiles, 13.9 with one,
+// 14.0 with eight waves; 32 x 4096 to 12288 13.5 with one tile of columns, 12.0 with two, to 4096
+// 6.5, 7.4; 64 x 4096 to 12288 22.6, 20.4, to 4096 8.6, 10.5.
 template <bool GATED, int OUT>
 static void few_pick(const LinearArgs& a) {
   const bool many = a.N > 16 * 512;
-  if (!linear_dma_takes(a))
-    linear_few_kernel<8, 1, 4, GATED, OUT><<<static_cast<unsigned>((a.N + 15) / 16), 512, 0, a.stream>>>(a);
-  else if (a.T <= 16) {
+  if (!linear_dma_takes(a)) {
+    const dim3 grid(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>((a.T + 15) / 16));
+    linear_few_kernel<8, 1, 4, GATED, OUT><<<grid, 512, 0, a.stream>>>(a);
+  } else if (a.T <= 16) {
     if (!GATED && many) few_dma_go<4, 1, 2, false, OUT>(a);
     else if (many) few_dma_go<4, 1, 1, GATED, OUT>(a);
     else few_dma_go<8, 1, 1, GATED, OUT>(a);
@@ -259,9 +274,37 @@ hipError_t launch_linear_few(const LinearArgs& a) {
 // less than 2^32 threads in a grid of the smallest tiles (64 x 64, 256 threads)
 bool linear_fits(int64_t T, int64_t N) { return (T + 63) / 64 * ((N + 63) / 64) < (int64_t(1) << 24); }
 
+// Up to 64 rows (16 without the loads straight to LDS), and more of them as further workgroups while
+// two of those go to a CU, one without those loads: their waves split K finer than the tiles' do.  Measured
+// (us, few-row kernel, then tiles; bf16 outputs): 128 x 4096 to 512 7.4, 12.0; to 4096 (512 workgroups) 14.8,
+// 18.8; 192 x 4096 to 4096 (768) 21, 23; 256 28, 25; 512 x 11008 to 1024 (512) 30, 36; K = 4097: 48
+// rows to 1024 (192) 17, 21; 128 to 512 (256) 17, 21; 65 to 1024 (320) 24, 21.
+static bool few_takes(const LinearArgs& a, bool dma) {
+  const int64_t parts = dma ? (a.T + 63) / 64 : (a.T + 15) / 16;
+  return parts == 1 || parts * ((a.N + 15) / 16) <= (dma ? 512 : 256);
+}
+
+// A workgroup that makes e4m3 codes has runs of 128 columns whole.  Where that leaves CUs idle, less
+// than 300 tiles of 256 x 128, h goes through memory in fp32 and its codes are made in a second
+// launch.  Measured (us, one launch, then two): 4 x 4096 to 11008 25, 19; 128 72, 43; 400 144, 111; 600
+// (258 tiles) 147, 134; 1000 (344) 209, 217; 1000 x 2048 to 5504 (172) 86, 66.
+size_t linear_workspace(int64_t T, int64_t N) {
+  return (T + 255) / 256 * ((N + 127) / 128) < 300 ? static_cast<size_t>(T) * static_cast<size_t>(N) * 4 : 0;
+}
+
 hipError_t launch_linear(const LinearArgs& a) {
+  if (a.out == OUT_FP8 && linear_workspace(a.T, a.N)) {
+    LinearArgs b = a;
+    b.out = OUT_F32;
+    b.y = a.workspace;
+    b.y_stride = a.N;
+    const hipError_t e = launch_linear(b);
+    if (e != hipSuccess) return e;
+    return launch_quantize(QuantArgs{a.workspace, a.N, static_cast<uint8_t*>(a.y), a.q_scale, RUN, 1, a.T, a.N,
+                                     false, a.stream});
+  }
   const bool dma = linear_dma_takes(a);
-  if (a.T <= (dma ? LINEAR_FEW_ROWS_DMA : LINEAR_FEW_ROWS) && a.out != OUT_FP8) return launch_linear_few(a);
+  if (a.out != OUT_FP8 && few_takes(a, dma)) return launch_linear_few(a);
   return dma ? launch_linear_dma(a) : launch_linear_tile(a);
 }
 

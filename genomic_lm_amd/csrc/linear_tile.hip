@@ -1,12 +1,14 @@
-// linear_tile.hip -- block-scaled e4m3 products of many rows, on LDS tiles.
+// linear_tile.hip -- block-scaled e4m3 products of many rows at any alignment, on LDS
+// tiles that pass through registers.
 #include "linear_tile.hpp"
 
 namespace hyena {
 
-// WT x WN waves, each with MT x MN tiles of 16 tokens by 16 columns.
-template <int WT, int WN, int MT, int MN, bool GATED, int OUT>
-__global__ __launch_bounds__(WT * WN * 64) void linear_tile_kernel(LinearArgs a, int tiles_t, int tiles_n) {
-  constexpr int NT = WT * WN * 64;
+// KG groups of WT x WN waves, each wave with MT x MN tiles of 16 tokens by 16 columns.  The groups share
+// the tile and take turns at the runs of K.
+template <int WT, int WN, int MT, int MN, int KG, bool GATED, int OUT>
+__global__ __launch_bounds__(WT * WN * KG * 64) void linear_tile_kernel(LinearArgs a, int tiles_t, int tiles_n) {
+  constexpr int NW = WT * WN, NT = NW * 64;
   constexpr int BT = WT * MT * 16, BN = WN * MN * 16;    // rows of the two staged tiles
   constexpr int CN = GATED ? BN / 2 : BN;                // columns of the output tile
   constexpr int MC = GATED ? MN / 2 : MN;
@@ -15,13 +17,17 @@ __global__ __launch_bounds__(WT * WN * 64) void linear_tile_kernel(LinearArgs a,
   constexpr int RX = BT / STEP, RW = BN / STEP;
   static_assert(BT % STEP == 0 && BN % STEP == 0, "whole rows per pass");
   static_assert(RUN % (MC * 16) == 0, "a wave's columns lie in one block of the scales");
-  __shared__ __attribute__((aligned(16))) uint8_t sh[2 * (BT + BN) * RUN];
   constexpr int BUF = (BT + BN) * 8;                     // 16-byte slots
-  i32x4* lds = reinterpret_cast<i32x4*>(sh);
+  constexpr int JOIN = (KG - 1) * NW * MN * MT * 1024;   // the other groups' sums
+  constexpr int TOPS = OUT == OUT_FP8 ? WN * BT * 4 : 0;
+  __shared__ __attribute__((aligned(16)))
+  uint8_t sh[2 * KG * BUF * 16 > JOIN + TOPS ? 2 * KG * BUF * 16 : JOIN + TOPS];
 
-  const int tid = static_cast<int>(threadIdx.x);
+  const int tid = static_cast<int>(threadIdx.x) % NT;    // within the group
   const int lane = tid & 63;
+  const int kg = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / NT);
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  i32x4* const lds = reinterpret_cast<i32x4*>(sh) + kg * 2 * BUF;
   const int wt = wave / WN, wn = wave % WN;
 
   int ti, ni;
@@ -100,13 +106,21 @@ __global__ __launch_bounds__(WT * WN * 64) void linear_tile_kernel(LinearArgs a,
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  fetch(0);
-  put(0);
-  if (blocks > 1) fetch(1);
+  if (kg < blocks) {
+    fetch(kg);
+    put(0);
+  }
+  if (kg + KG < blocks) fetch(kg + KG);
   tile_sync();
   const int fr = lane & 15, fc = (lane >> 4) * 2;
-  for (int kb = 0; kb < blocks; ++kb) {
-    const i32x4* bx = lds + (kb & 1) * BUF;
+  int buf = 0;
+  for (int k0 = 0; k0 < blocks; k0 += KG, buf ^= 1) {
+    const int kb = k0 + kg;
+    if (KG > 1 && kb >= blocks) {                        // nothing left for this group
+      tile_sync();
+      continue;
+    }
+    const i32x4* bx = lds + buf * BUF;
     const i32x4* bw = bx + BT * 8;
     float sx[MT];
 #pragma unroll
@@ -132,36 +146,41 @@ __global__ __launch_bounds__(WT * WN * 64) void linear_tile_kernel(LinearArgs a,
         for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
       }
     }
-    if (kb + 1 < blocks) put((kb + 1) & 1);
-    if (kb + 2 < blocks) fetch(kb + 2);
+    if (kb + KG < blocks) put(buf ^ 1);
+    if (kb + 2 * KG < blocks) fetch(kb + 2 * KG);
     tile_sync();
   }
+  if constexpr (KG > 1) join_groups<KG, NW, MT, MN>(acc, sh, kg, wave, lane);
+  if (kg > 0) return;
 
-  tile_epilogue<WT, WN, MT, MN, GATED, OUT>(a, acc, t0, ncol, wt, wn, lane, sh);
+  tile_epilogue<WT, WN, MT, MN, GATED, OUT>(a, acc, t0, ncol, wt, wn, lane, sh + JOIN);
 }
 
-template <int WT, int WN, int MT, int MN, bool GATED>
+template <int WT, int WN, int MT, int MN, int KG, bool GATED>
 static void tile_go(const LinearArgs& a) {
   constexpr int BT = WT * MT * 16, CN = WN * MN * 16 / (GATED ? 2 : 1);
   const int64_t tt = (a.T + BT - 1) / BT, tn = (a.N + CN - 1) / CN;
   const unsigned grid = static_cast<unsigned>(tt * tn);
   auto go = [&](auto kernel) {
-    kernel<<<grid, WT * WN * 64, 0, a.stream>>>(a, static_cast<int>(tt), static_cast<int>(tn));
+    kernel<<<grid, WT * WN * KG * 64, 0, a.stream>>>(a, static_cast<int>(tt), static_cast<int>(tn));
   };
-  if constexpr (GATED && CN % RUN == 0) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_FP8>);
-  else if (a.out == OUT_F32) go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_F32>);
-  else go(linear_tile_kernel<WT, WN, MT, MN, GATED, OUT_BF16>);
+  if constexpr (GATED && CN % RUN == 0) go(linear_tile_kernel<WT, WN, MT, MN, KG, GATED, OUT_FP8>);
+  else if (a.out == OUT_F32) go(linear_tile_kernel<WT, WN, MT, MN, KG, GATED, OUT_F32>);
+  else go(linear_tile_kernel<WT, WN, MT, MN, KG, GATED, OUT_BF16>);
 }
 
+// Smaller tiles, whose K two groups of waves share, where those of 128 x 128 leave CUs idle.  Measured
+// (us, fp32 and bf16 outputs, by one group, two, four): 30 x 9662 to 384 59, 48, 45; 333 x 1001 to 1000
+// 15, 13, 14; 500 x 1001 to 4000 -, 28, 37; 700 x 301 to 2000 -, 24, 31.
 hipError_t launch_linear_tile(const LinearArgs& a) {
   const int64_t n128 = (a.T + 127) / 128 * ((a.N + 127) / 128) * (a.w1 ? 2 : 1);
-  if (a.out == OUT_FP8) tile_go<4, 2, 2, 8, true>(a);
+  if (a.out == OUT_FP8) tile_go<4, 2, 2, 8, 1, true>(a);
   else if (a.w1) {
-    if (n128 >= 256) tile_go<2, 2, 4, 4, true>(a);
-    else tile_go<2, 2, 2, 4, true>(a);
+    if (n128 >= 256) tile_go<2, 2, 4, 4, 1, true>(a);
+    else tile_go<2, 2, 2, 4, 2, true>(a);
   } else {
-    if (n128 >= 256) tile_go<2, 2, 4, 4, false>(a);
-    else tile_go<2, 2, 2, 2, false>(a);
+    if (n128 >= 256) tile_go<2, 2, 4, 4, 1, false>(a);
+    else tile_go<2, 2, 2, 2, 2, false>(a);
   }
   return hipGetLastError();
 }

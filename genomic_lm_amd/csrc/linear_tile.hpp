@@ -40,6 +40,27 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
+// The other groups' sums to group 0, in their order: acc of group 0 is the tile's afterwards.  The
+// groups are done with the LDS at sh.
+template <int KG, int NW, int MT, int MN>
+__device__ __forceinline__ void join_groups(f32x4 (&acc)[MN][MT], uint8_t* sh, int kg, int wave, int lane) {
+  f32x4* const join = reinterpret_cast<f32x4*>(sh) + wave * (MN * MT * 64) + lane;
+  if (kg > 0) {
+#pragma unroll
+    for (int i = 0; i < MN; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) join[((kg - 1) * NW * MN * MT + i * MT + j) * 64] = acc[i][j];
+  }
+  tile_sync();
+  if (kg > 0) return;
+#pragma unroll
+  for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+    for (int i = 0; i < MN; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] += join[(g * NW * MN * MT + i * MT + j) * 64];
+}
+
 // The tile's sums to the output: a wave's lane holds columns 4 (l / 16) .. + 3 of
 // token l % 16 in each of its MT x MN tiles, the gate's in the first half of
 // the MN and the other weight's in the second.  sh: LDS that nobody reads any more.
@@ -51,7 +72,7 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
   const int N = a.N;
   const int cg = 4 * (lane >> 4);
   if constexpr (OUT == OUT_FP8) {
-    static_assert(GATED, "codes come from the gated product");
+    static_assert(GATED && MC % 4 == 0, "codes come from the gated product");
     float* top = reinterpret_cast<float*>(sh);          // [WN][BT]
     constexpr int GW = RUN / (MC * 16);                 // waves that share a run of columns
     float h[MC][MT][4];
@@ -88,7 +109,7 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
       const float scale = run_scale(m);
       if (wn % GW == 0 && lane < 16 && ncol < N && t < a.T) a.q_scale[t * runs + ncol / RUN] = scale;
       uint8_t* row = static_cast<uint8_t*>(a.y) + t * a.y_stride;
-      if constexpr (MC % 4 == 0) {
+      {
 #pragma unroll
         for (int i = 0; i < MC; i += 4) {
           // lane group g holds words g of four tiles; afterwards the four words of tile g
@@ -108,17 +129,6 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
           if (n + 16 <= N) __builtin_memcpy(row + n, w, 16);
           else
             for (int e = 0; n + e < N; ++e) row[n + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
-        }
-      } else if (t < a.T) {
-#pragma unroll
-        for (int i = 0; i < MC; ++i) {
-          uint32_t w[1];
-          to_codes<4>(h[i][j], scale, w);
-          const int n = ncol + i * 16 + cg;
-          if (n + 4 <= N) __builtin_memcpy(row + n, w, 4);
-          else
-            for (int e = 0; e < 4; ++e)
-              if (n + e < N) row[n + e] = static_cast<uint8_t>(w[0] >> (8 * e));
         }
       }
     }

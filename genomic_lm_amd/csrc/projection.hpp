@@ -33,14 +33,15 @@ struct LinearArgs {
   int64_t T;
   int N, K;
   hipStream_t stream;
+  float* workspace = nullptr;   // (T, N), where linear_workspace asks for it
 };
+size_t linear_workspace(int64_t T, int64_t N);        // bytes, of OUT_FP8
 bool linear_fits(int64_t T, int64_t N);               // whether the launch grid exists
 hipError_t launch_linear(const LinearArgs& a);
-hipError_t launch_linear_few(const LinearArgs& a);    // T up to:
+hipError_t launch_linear_few(const LinearArgs& a);
 hipError_t launch_linear_tile(const LinearArgs& a);
 bool linear_dma_takes(const LinearArgs& a);            // alignment and strides
 hipError_t launch_linear_dma(const LinearArgs& a);
-constexpr int LINEAR_FEW_ROWS = 16, LINEAR_FEW_ROWS_DMA = 64;
 
 // Codes and scales of T rows: a scale per row (group 0), per 128 columns
 // (group 128, block 1) or per 128 rows by 128 columns (block 128).

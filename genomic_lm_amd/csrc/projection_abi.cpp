@@ -24,7 +24,8 @@ bool valid_io(hyena_dtype_t io) { return io == HYENA_F32 || io == HYENA_BF16; }
 size_t io_size(hyena_dtype_t io) { return io == HYENA_BF16 ? 2 : 4; }
 
 // Sizes, pointers and strides of a product; two: a second weight.
-hyena_status_t linear_impl(const hyena::LinearArgs& a, int64_t N, int64_t K, int64_t x_group, bool two) {
+hyena_status_t linear_impl(const hyena::LinearArgs& a, int64_t N, int64_t K, int64_t x_group, bool two,
+                           size_t ws_bytes = 0) {
   if (a.T < 0 || N < 0 || K < 0 || a.x_stride < 0 || a.xs_row < 0 || a.y_stride < 0 ||
       (x_group != 0 && x_group != HYENA_NORM_GROUP))
     return HYENA_ERR_INVALID_ARG;
@@ -40,6 +41,10 @@ hyena_status_t linear_impl(const hyena::LinearArgs& a, int64_t N, int64_t K, int
   if (N > HYENA_MAX_PROJ_DIM || K > HYENA_MAX_PROJ_DIM || a.T > kMaxInt || a.x_stride > kMost / a.T ||
       a.xs_row > kMost / a.T || a.y_stride > kMost / a.T || !hyena::linear_fits(a.T, N))
     return HYENA_ERR_UNSUPPORTED;
+  if (a.out == hyena::OUT_FP8) {
+    const size_t need = hyena::linear_workspace(a.T, N);
+    if (need && (!a.workspace || ws_bytes < need || !aligned_to(a.workspace, 16))) return HYENA_ERR_WORKSPACE;
+  }
   hyena::LinearArgs b = a;
   b.N = static_cast<int>(N);
   b.K = static_cast<int>(K);
@@ -96,11 +101,19 @@ hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
                                             const float* gate_scale, const uint8_t* w_up,
                                             const float* up_scale, hyena_act_t act, uint8_t* q,
                                             float* q_scale, int64_t T, int64_t I, int64_t K,
-                                            hipStream_t stream) {
+                                            void* workspace, size_t ws_bytes, hipStream_t stream) {
   if (act < HYENA_ACT_NONE || act > HYENA_ACT_SILU) return HYENA_ERR_INVALID_ARG;
   hyena::LinearArgs a{x, x_stride, x_scale, x_scale_stride, 0, w_gate, gate_scale, w_up, up_scale, nullptr,
-                      static_cast<int>(act), q, I, q_scale, hyena::OUT_FP8, T, 0, 0, stream};
-  return linear_impl(a, I, K, x_group, true);
+                      static_cast<int>(act), q, I, q_scale, hyena::OUT_FP8, T, 0, 0, stream,
+                      static_cast<float*>(workspace)};
+  return linear_impl(a, I, K, x_group, true, ws_bytes);
+}
+
+size_t hyena_gated_linear_fp8_workspace_size(int64_t T, int64_t I, int64_t K) {
+  if (T < 1 || I < 1 || K < 0 || I > HYENA_MAX_PROJ_DIM || K > HYENA_MAX_PROJ_DIM || T > kMaxInt ||
+      !hyena::linear_fits(T, I))
+    return 0;
+  return hyena::linear_workspace(T, I);
 }
 
 hyena_status_t hyena_quantize_fp8(const void* x, int64_t x_stride, uint8_t* q, float* q_scale,

@@ -12,6 +12,7 @@ per block of 128 x 128, as quantize_weight_fp8 gives them.
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -19,8 +20,8 @@ import torch
 from . import _ACT_DTYPES, BF16, F32, _check, _io, _stream, lib
 from .serving import _FP8, NORM_GROUP, _heads, _like, _rows, _vec
 
-__all__ = ["linear_fp8", "gated_linear_fp8", "quantize_fp8", "quantize_weight_fp8", "rotary_inv_freq",
-           "qk_norm_rope", "ACTS"]
+__all__ = ["linear_fp8", "gated_linear_fp8", "gated_linear_fp8_workspace_size", "quantize_fp8",
+           "quantize_weight_fp8", "rotary_inv_freq", "qk_norm_rope", "ACTS"]
 
 ACTS = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 
@@ -97,14 +98,21 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, out=None, dtype=torch.bfloat16
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def gated_linear_fp8_workspace_size(T: int, I: int, K: int) -> int:
+    """Bytes of workspace of gated_linear_fp8 with an e4m3 output."""
+    return int(lib().hyena_gated_linear_fp8_workspace_size(T, I, K))
+
+
 def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = "gelu", out=None, scale=None,
-                     dtype=torch.bfloat16):
+                     dtype=torch.bfloat16, workspace=None):
     """h = act(x w_gate^T) * (x w_up^T), operands as in linear_fp8; act "gelu", "gelu_tanh",
     "silu" or "none".
 
     dtype bfloat16 or float32: returns h (..., I) (out: written instead, in its type).
     dtype float8_e4m3fn: returns (q (..., I), scale (..., ceil(I / 128))), the operand of
-    the next linear_fp8, written to out and scale if given."""
+    the next linear_fp8, written to out and scale if given; workspace: gated_linear_fp8_workspace_size
+    bytes, made here if not given."""
     if act not in ACTS:
         raise ValueError(f"act must be one of {', '.join(ACTS)}")
     head, T, K, rows = _operand(x, x_scale)
@@ -123,8 +131,14 @@ def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = 
             sp = scale.data_ptr()
         else:
             sp = _vec("scale", scale, torch.float32, sshape, dev)
+        if workspace is None:
+            need = gated_linear_fp8_workspace_size(T, N, K)
+            if need:
+                workspace = x.new_empty(need, dtype=torch.uint8)
+        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                      workspace.numel() * workspace.element_size())
         _check("hyena_gated_linear_fp8_quant", lib().hyena_gated_linear_fp8_quant(
-            *head, *gp, *up, ACTS[act], qp, sp, T, N, K, _stream(x)))
+            *head, *gp, *up, ACTS[act], qp, sp, T, N, K, wp, wn, _stream(x)))
         return out, scale
     if scale is not None:
         raise ValueError("scale goes with dtype float8_e4m3fn")

@@ -657,6 +657,9 @@ hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const 
  * 128 columns, the operand of the MLP's last projection; scales and codes by the
  * rules of hyena_add_rmsnorm_fp8.
  *   q : (T, I) e4m3, contiguous;  q_scale : (T, ceil(I / 128)) fp32
+ * Workspace (device, 16-byte aligned, no initial contents) of
+ * hyena_gated_linear_fp8_workspace_size bytes (0 for many rows); NULL, short or
+ * misaligned when one is needed -> HYENA_ERR_WORKSPACE.
  */
 hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
                                             const float* x_scale, int64_t x_scale_stride,
@@ -664,7 +667,8 @@ hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
                                             const float* gate_scale, const uint8_t* w_up,
                                             const float* up_scale, hyena_act_t act, uint8_t* q,
                                             float* q_scale, int64_t T, int64_t I, int64_t K,
-                                            hipStream_t stream);
+                                            void* workspace, size_t ws_bytes, hipStream_t stream);
+size_t hyena_gated_linear_fp8_workspace_size(int64_t T, int64_t I, int64_t K);
 
 /*
  * hyena_quantize_fp8 -- activations to e4m3 with scales (a mixer's output in front

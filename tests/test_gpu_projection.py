@@ -111,7 +111,8 @@ def test_linear(T, K, N, group, dtype, bias):
 
 @pytest.mark.parametrize("T,K,N", [
     (2100, 128, 3700), (2100, 272, 3700), (2100, 400, 3800), (2060, 112, 3800),    # the largest tiles, one to four runs
-    (2100, 272, 2100), (700, 1040, 2000), (700, 1024, 2000), (130, 1168, 520), (40, 528, 640)])  # shared K
+    (2100, 272, 2100), (700, 1040, 2000), (700, 1024, 2000), (130, 1168, 520), (40, 528, 640),          # shared K
+    (1500, 272, 100), (500, 528, 250), (300, 145, 100)])                             # many rows of few outputs
 @pytest.mark.parametrize("group,dtype", [(128, BF), (0, F32)])
 def test_linear_tiles(T, K, N, group, dtype):
     rng = np.random.default_rng(T + K + N)
@@ -168,8 +169,8 @@ def test_gated(T, K, N, act, dtype, group):
 
 
 @pytest.mark.parametrize("T,K,N,act,dtype", [
-    (2100, 400, 1900, "none", BF), (2100, 272, 1900, "silu", F32), (5200, 144, 2500, "gelu", None),
-    (700, 1040, 1000, "gelu", BF), (700, 1040, 1000, "gelu", None), (2000, 128, 1100, "silu", BF)])
+    (2100, 400, 1900, "none", BF), (2100, 272, 1900, "silu", F32), (5200, 144, 2500, "gelu", None), (5200, 145, 2500, "silu", None),
+    (1500, 272, 100, "silu", BF), (300, 145, 100, "gelu", None), (700, 1040, 1000, "gelu", BF), (700, 1040, 1000, "gelu", None), (2000, 128, 1100, "silu", BF)])
 def test_gated_tiles(T, K, N, act, dtype):
     rng = np.random.default_rng(T + K + N)
     x, xs, ws = operands(rng, T, K, N, 128, 2)
@@ -177,20 +178,43 @@ def test_gated_tiles(T, K, N, act, dtype):
     check_gated(x, xs, ws, act, G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=dtype or F8), dtype)
 
 
-@pytest.mark.parametrize("T", [3, 40, 600])
-def test_strided_operands(T):
+@pytest.mark.parametrize("T,K,N", [(1, 256, 200), (70, 301, 130), (600, 144, 300)])
+def test_gated_codes_by_way_of_a_workspace(T, K, N):
+    """Whatever the workspace holds, and nothing behind the bytes that the size function names."""
+    rng = np.random.default_rng(T)
+    x, xs, ws = operands(rng, T, K, N, 128, 2)
+    args = to_gpu(x, xs / f32(60 * math.sqrt(K)), ws)
+    need = G.gated_linear_fp8_workspace_size(T, N, K)
+    assert need == 4 * T * N
+    want = G.gated_linear_fp8(*args, dtype=F8)
+    for fill in (0x00, 0xFF, 0x7F):
+        buf = torch.full((need + 64,), fill, dtype=U8, device=dev())
+        got = G.gated_linear_fp8(*args, dtype=F8, workspace=buf[:need])
+        assert bits_equal(got[0], want[0]) and bits_equal(got[1], want[1])
+        assert (buf[need:] == fill).all()
+    with pytest.raises(RuntimeError):
+        G.gated_linear_fp8(*args, dtype=F8, workspace=buf[:need - 4])
+    # the codes of the fp32 product, as quantize_fp8 makes them
+    h = G.gated_linear_fp8(*args, dtype=F32)
+    q, scale = G.quantize_fp8(h, 128)
+    assert bits_equal(q, want[0]) and bits_equal(scale, want[1])
+
+
+@pytest.mark.parametrize("T,K,at", [(3, 300, 5), (40, 300, 5), (600, 300, 5), (40, 304, 16), (200, 304, 16),
+                                    (1300, 304, 16)])
+def test_strided_operands(T, K, at):
     """Rows of x, of its scales and of y at strides of their own; a single token of a batch."""
     rng = np.random.default_rng(T)
-    K, N = 300, 200
+    N = 200
     x, xs, ws = operands(rng, T, K, N, 128)
     gx, gxs, gw, gws = to_gpu(x, xs, ws)
     want = G.linear_fp8(gx, gxs, gw, gws)
-    wide = torch.zeros((T, K + 13), dtype=U8, device=dev())
-    wide[:, 5:5 + K] = gx
+    wide = torch.zeros((T, K + (13 if at == 5 else 32)), dtype=U8, device=dev())
+    wide[:, at:at + K] = gx
     scales = torch.zeros((T, 7), device=dev())
     scales[:, 2:5] = gxs
     buf = torch.full((T, N + 9), 7.0, dtype=BF, device=dev())
-    G.linear_fp8(wide[:, 5:5 + K], scales[:, 2:5], gw, gws, out=buf[:, 3:3 + N])
+    G.linear_fp8(wide[:, at:at + K], scales[:, 2:5], gw, gws, out=buf[:, 3:3 + N])
     assert bits_equal(buf[:, 3:3 + N], want)
     assert (buf[:, :3] == 7).all() and (buf[:, 3 + N:] == 7).all()
     # one token of each sequence, one scale per row

@@ -46,10 +46,14 @@ def test_gated_refusals():
         ({5: None}, BAD), ({6: None}, BAD), ({7: None}, BAD), ({8: None}, BAD), ({8: ODD}, BAD), ({10: None}, BAD),
         ({9: 4}, BAD), ({9: -1}, BAD), ({10: P(0x10002)}, BAD), ({11: 100}, BAD), ({15: 2}, BAD), ({4: 1}, BAD),
         ({13: 1 << 21, 11: 1 << 21}, UNS), ({12: 0, 10: None}, OK)])
-    # x xs scale ss group wg gs wu us act q qs T I K stream
-    good = [FAKE, 256, FAKE, 1, 0, FAKE, FAKE, FAKE, FAKE, 1, ODD, FAKE, 5, 384, 256, None]
+    # x xs scale ss group wg gs wu us act q qs T I K ws bytes stream
+    size = G.lib().hyena_gated_linear_fp8_workspace_size
+    need = size(5, 384, 256)
+    assert need == 5 * 384 * 4 and size(8192, 11008, 4096) == 0 and size(0, 384, 256) == 0
+    good = [FAKE, 256, FAKE, 1, 0, FAKE, FAKE, FAKE, FAKE, 1, ODD, FAKE, 5, 384, 256, FAKE, need, None]
     refusals(G.lib().hyena_gated_linear_fp8_quant, good, [
         ({10: None}, BAD), ({11: None}, BAD), ({11: ODD}, BAD), ({9: 4}, BAD), ({7: None}, BAD), ({13: -2}, BAD),
+        ({15: None}, G.ERR_WORKSPACE), ({16: need - 1}, G.ERR_WORKSPACE), ({15: P(0x10008)}, G.ERR_WORKSPACE),
         ({14: 1 << 21}, UNS), ({13: 0, 10: None}, OK)])
 
 
