@@ -78,8 +78,9 @@ __device__ __forceinline__ i32x4 codes16(const uint8_t* p, int n) {
 // a relative 2.4e-8 (least squares at Chebyshev points, reweighted towards the largest error).  About
 // 20 instructions; the device library's erfc, ten times that, took a fifth of the time of a gated
 // product of 8192 x 4096 to 11008.
-__device__ __forceinline__ float gate(float g, float u, int act) {
-  if (act == ACT_GELU) {
+template <int ACT>
+__device__ __forceinline__ float gate(float g, float u) {
+  if constexpr (ACT == ACT_GELU) {
     const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.24748737341529164f, 1.0f));
     float q = 0.007330488879233599f;
     q = fmaf(q, t, 0.005140664987266064f);
@@ -94,12 +95,20 @@ __device__ __forceinline__ float gate(float g, float u, int act) {
     q = fmaf(q, t, 0.19746634364128113f);
     const float h = 0.5f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f) * (q * t);
     g *= g < 0.0f ? h : 1.0f - h;
-  } else if (act == ACT_GELU_TANH) {           // g / (1 + exp(-2 z)); 2 sqrt(2 / pi) log2 e
+  } else if constexpr (ACT == ACT_GELU_TANH) {           // g / (1 + exp(-2 z)); 2 sqrt(2 / pi) log2 e
     g *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-2.3022081982148305f * fmaf(0.044715f * g * g, g, g)));
-  } else if (act == ACT_SILU) {
+  } else if constexpr (ACT == ACT_SILU) {
     g *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
   }
   return g * u;
+}
+// f(act as a constant)
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+  else if (act == ACT_GELU_TANH) f(std::integral_constant<int, ACT_GELU_TANH>{});
+  else if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
+  else f(std::integral_constant<int, ACT_NONE>{});
 }
 
 // The scale of a run whose largest magnitude has the bits `top`, and codes of

@@ -2,6 +2,9 @@
 // 16-byte aligned: LDS tiles filled straight from memory.
 #include "linear_tile.hpp"
 
+#ifndef SPLITMAX
+#define SPLITMAX 0
+#endif
 namespace hyena {
 
 // All but N of this wave's loads have arrived, and its LDS reads; then every wave is here.
@@ -340,9 +343,27 @@ bool linear_dma_takes(const LinearArgs& a) {
 // groups, 41 by one, 37 by 64 x 64; 256 x 4096 (64) 28, 64 x 64 by four groups 26.
 template <bool GATED, int OUT>
 static void dma_pick(const LinearArgs& a) {
-  const int64_t n256 = tiles<256, GATED ? 128 : 256>(a), n128 = tiles<128, GATED ? 64 : 128>(a);
+  constexpr int CN = GATED ? 128 : 256;                  // columns of a tile of 256 rows
+  const int64_t n256 = tiles<256, CN>(a), n128 = tiles<128, CN / 2>(a);
+  const int64_t tt = (a.T + 255) / 256, whole = n256 / 256 * 256 / tt, rest = n256 - whole * tt;
   if constexpr (OUT == OUT_FP8) {
     dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
+  } else if (whole > 0 && rest > 0 && rest <= SPLITMAX) {
+    const int at = static_cast<int>(whole) * CN;
+    LinearArgs b = a, c = a;
+    b.N = at;
+    dma_pick<GATED, OUT>(b);
+    const int64_t block = static_cast<int64_t>(at / RUN) * ((a.K + RUN - 1) / RUN);
+    c.N = a.N - at;
+    c.w0 += static_cast<int64_t>(at) * a.K;
+    c.s0 += block;
+    if (GATED) {
+      c.w1 += static_cast<int64_t>(at) * a.K;
+      c.s1 += block;
+    }
+    if (a.bias) c.bias += at;
+    c.y = static_cast<uint8_t*>(a.y) + at * (OUT == OUT_BF16 ? 2 : 4);
+    dma_pick<GATED, OUT>(c);
   } else if (n128 > 256 && 100 * ((n256 + 255) / 256) <= 68 * ((n128 + 511) / 512) &&
              (OUT != OUT_BF16 || a.K >= RUN)) {
     if constexpr (OUT == OUT_BF16)

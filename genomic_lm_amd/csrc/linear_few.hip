@@ -29,10 +29,15 @@ __device__ __forceinline__ void few_join(const LinearArgs& a, const f32x4 (&acc)
     if (row >= a.T) continue;
     O* const yr = static_cast<O*>(a.y) + row * a.y_stride;
     const int n = n0 + i * 16 + 4 * (lane >> 4);
+    if constexpr (GATED)
+      with_act(a.act, [&](auto act) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s0[e] = gate<decltype(act)::value>(s0[e], s1[e]);
+      });
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (n + e >= a.N) continue;
-      if constexpr (GATED) Io<O>::st(yr, n + e, gate(s0[e], s1[e], a.act));
+      if constexpr (GATED) Io<O>::st(yr, n + e, s0[e]);
       else Io<O>::st(yr, n + e, s0[e] + (a.bias ? a.bias[n + e] : 0.0f));
     }
   }

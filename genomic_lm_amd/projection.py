@@ -131,12 +131,12 @@ def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = 
             sp = scale.data_ptr()
         else:
             sp = _vec("scale", scale, torch.float32, sshape, dev)
-        if workspace is None:
-            need = gated_linear_fp8_workspace_size(T, N, K)
-            if need:
-                workspace = x.new_empty(need, dtype=torch.uint8)
-        wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                      workspace.numel() * workspace.element_size())
+        wp, wn = None, 0
+        if workspace is not None:
+            wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif need := gated_linear_fp8_workspace_size(T, N, K):
+            workspace = x.new_empty(need, dtype=torch.uint8)
+            wp, wn = workspace.data_ptr(), need
         _check("hyena_gated_linear_fp8_quant", lib().hyena_gated_linear_fp8_quant(
             *head, *gp, *up, ACTS[act], qp, sp, T, N, K, wp, wn, _stream(x)))
         return out, scale
