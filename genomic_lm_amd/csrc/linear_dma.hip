@@ -2,9 +2,6 @@
 // 16-byte aligned: LDS tiles filled straight from memory.
 #include "linear_tile.hpp"
 
-#ifndef SPLITMAX
-#define SPLITMAX 0
-#endif
 namespace hyena {
 
 // All but N of this wave's loads have arrived, and its LDS reads; then every wave is here.
@@ -336,11 +333,13 @@ bool linear_dma_takes(const LinearArgs& a) {
 }
 
 // Tiles by the rounds of workgroups that they make on 256 CUs: one of 256 x 256 to a CU, two of 128 x
-// 128, whose round takes 0.68 of the time of one of the former.  Where there is less than a round,
-// two or four groups of waves share the K of a tile.  Measured (us, bf16 outputs, the tile that
-// is taken against the next): 8192 x 12288 x 4096 256 x 256 384, 128 x 128 486; 1024 x 12288 (192 and
-// 768 tiles) 72, 91; 512 x 12288 (96, 384) 128 x 128 54, 59; 512 x 4096 (128 of 128 x 128) 32 by two
-// groups, 41 by one, 37 by 64 x 64; 256 x 4096 (64) 28, 64 x 64 by four groups 26.
+// 128, whose round takes 0.7 to 0.8 of the time of one of the former.  Where there is less than a
+// round, two or four groups of waves share the K of a tile.  Measured (us, bf16 outputs, the tile
+// that is taken, then the next): 8192 x 4096 to 12288 256 x 256 376, 128 x 128 486; 512 to 12288 (96 tiles
+// of 256 x 256, 384 of 128 x 128) 128 x 128 37, 51; 512 to 16384 (128, 512) 42, 53; 512 to 4096 (128 of
+// 128 x 128) by two groups 22, by one 31.  Up to 100 tiles that whole rounds leave go into a launch
+// of smaller ones: 4096 to 4352 (272 tiles) 83, in one launch 117; 1500 to 12288 (288) 86, 107;
+// gated 1000 to 10928 (344) 118, 123; but 3000 x 2048 to 8192 (384) 67, 66.
 template <bool GATED, int OUT>
 static void dma_pick(const LinearArgs& a) {
   constexpr int CN = GATED ? 128 : 256;                  // columns of a tile of 256 rows
@@ -348,7 +347,8 @@ static void dma_pick(const LinearArgs& a) {
   const int64_t tt = (a.T + 255) / 256, whole = n256 / 256 * 256 / tt, rest = n256 - whole * tt;
   if constexpr (OUT == OUT_FP8) {
     dma_go<4, 2, 4, 8, 1, GATED, OUT>(a);
-  } else if (whole > 0 && rest > 0 && rest <= SPLITMAX) {
+  } else if (whole > 0 && rest > 0 && rest <= 100) {
+    // the columns that would be little of a last round, in a launch of smaller tiles
     const int at = static_cast<int>(whole) * CN;
     LinearArgs b = a, c = a;
     b.N = at;

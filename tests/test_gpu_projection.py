@@ -178,6 +178,24 @@ def test_gated_tiles(T, K, N, act, dtype):
     check_gated(x, xs, ws, act, G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=dtype or F8), dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_columns_of_two_launches(dtype):
+    """A little more than a round of the largest tiles: the last columns take a launch of their own."""
+    rng = np.random.default_rng(17)
+    x, xs, ws = operands(rng, 4200, 144, 4100, 128)
+    b = f32(rng.normal(size=4100) * 100)
+    y = torch.full((4200, 4104), 7.0, dtype=dtype, device=dev())
+    G.linear_fp8(*to_gpu(x, xs, ws), bias=put(b), out=y[:, :4100])
+    assert (y[:, 4100:] == 7).all()
+    want, size = ref.product(x, xs, *ws[0])
+    want, tol = want + b.astype(np.float64), sum_error(144, size + np.abs(b), dtype)
+    e = np.abs(to_f64(y[:, :4100]) - want)
+    assert (e <= tol + half(dtype) * (np.abs(want) + tol)).all(), (e - tol).max()
+    x, xs, ws = operands(rng, 2100, 144, 3700, 128, 2)
+    xs = xs / f32(60 * 12)
+    check_gated(x, xs, ws, "gelu", G.gated_linear_fp8(*to_gpu(x, xs, ws), dtype=dtype), dtype)
+
+
 @pytest.mark.parametrize("T,K,N", [(1, 256, 200), (70, 301, 130), (600, 144, 300)])
 def test_gated_codes_by_way_of_a_workspace(T, K, N):
     """Whatever the workspace holds, and nothing behind the bytes that the size function names."""
