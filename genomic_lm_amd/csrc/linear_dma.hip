@@ -1,5 +1,10 @@
 // linear_dma.hip -- block-scaled e4m3 products of many rows whose rows are
 // 16-byte aligned: LDS tiles filled straight from memory.
+//
+// Bound by the matrix cores, at the power limit (1.9 GHz): 8192 x 4096 to 12288, bf16 outputs, 376 to
+// 381 us, 2.2 PFLOP/s; gated to 11008 with e4m3 outputs, on the bf16 instructions, 1169 us, 1.26
+// PFLOP/s.  A load to LDS moves 1 KB in 16 cycles and needs no registers, which hold the sums (256 x
+// 256 fp32 in eight waves); a tile staged through registers spilled 210 of them.
 #include "linear_tile.hpp"
 
 namespace hyena {

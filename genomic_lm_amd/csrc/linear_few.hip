@@ -1,5 +1,8 @@
 // linear_few.hip -- block-scaled e4m3 products of few rows (decode steps) or few outputs, and the
 // choice among the products.
+//
+// Bound by reading the weights: 16 x 11008 to 4096 10.5 us, 4.3 TB/s; 1 x 4096 to 12288 9.0 us, 5.6
+// TB/s from the last-level cache; gated 4 x 4096 to 11008 16.4 us, 5.5 TB/s.
 #include "linear_common.hpp"
 
 namespace hyena {

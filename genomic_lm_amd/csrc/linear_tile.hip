@@ -1,5 +1,8 @@
 // linear_tile.hip -- block-scaled e4m3 products of many rows at any alignment, on LDS
 // tiles that pass through registers.
+//
+// K that is no multiple of 16 puts rows at odd addresses, which loads straight into LDS do
+// not take.  333 x 1001 to 1000, fp32: 12.5 us, a chain of four runs per group and the launch.
 #include "linear_tile.hpp"
 
 namespace hyena {

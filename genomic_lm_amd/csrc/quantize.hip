@@ -5,6 +5,10 @@
 // front of out_proj (evo2_flash README, layer_names table), and the weights.
 // Over a run or block,
 //     scale = max(max|x| / 448, 2^-140) (1 where x is 0),   q = e4m3(x / scale).
+//
+// One pass over memory, which bounds all of them: a run, row or block stays in registers between
+// its maximum and its codes.  Measured: 32768 x 4096 bf16 per 128 columns 75 us, 5.4 TB/s;
+// weights of 11008 x 4096 fp32 41.5 us, 5.4 TB/s; 16 x 4096 2.6 us in a graph, the launch.
 #include "linear_common.hpp"
 
 namespace hyena {

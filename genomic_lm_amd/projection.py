@@ -133,6 +133,8 @@ def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = 
             sp = _vec("scale", scale, torch.float32, sshape, dev)
         wp, wn = None, 0
         if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous, on the device of x")
             wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         elif need := gated_linear_fp8_workspace_size(T, N, K):
             workspace = x.new_empty(need, dtype=torch.uint8)

@@ -659,7 +659,8 @@ hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const 
  *   q : (T, I) e4m3, contiguous;  q_scale : (T, ceil(I / 128)) fp32
  * Workspace (device, 16-byte aligned, no initial contents) of
  * hyena_gated_linear_fp8_workspace_size bytes (0 for many rows); NULL, short or
- * misaligned when one is needed -> HYENA_ERR_WORKSPACE.
+ * misaligned when one is needed -> HYENA_ERR_WORKSPACE.  Calls sharing one
+ * workspace must be ordered.
  */
 hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
                                             const float* x_scale, int64_t x_scale_stride,

@@ -212,6 +212,10 @@ def test_gated_codes_by_way_of_a_workspace(T, K, N):
         assert (buf[need:] == fill).all()
     with pytest.raises(RuntimeError):
         G.gated_linear_fp8(*args, dtype=F8, workspace=buf[:need - 4])
+    with pytest.raises(ValueError):
+        G.gated_linear_fp8(*args, dtype=F8, workspace=buf[:need].cpu())
+    with pytest.raises(ValueError):
+        G.gated_linear_fp8(*args, dtype=F8, workspace=torch.empty(2 * need, dtype=U8, device=dev())[::2])
     # the codes of the fp32 product, as quantize_fp8 makes them
     h = G.gated_linear_fp8(*args, dtype=F32)
     q, scale = G.quantize_fp8(h, 128)
