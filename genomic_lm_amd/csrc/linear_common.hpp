@@ -158,16 +158,20 @@ __device__ __forceinline__ uint64_t scalar(const void* p) {
 // base and dst are the wave's.  Written as assembly so that the compiler, which cannot tell
 // the halves of the LDS buffer apart, does not make every LDS read of one half wait for the
 // loads into the other; the kernels wait for them themselves.  They write no vector
-// registers; m0 is the compiler's only where it sets it itself, just before the use.
+// registers.  A load that reads m0 needs one wait state after its write, one whose base a
+// v_readfirstlane (or a restored spill's v_readlane) wrote needs five; the compiler adds none
+// in front of assembly: the move and the s_nop are five.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(dst)),
                "v"(off), "s"(scalar(base))
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(dst)),
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(dst)),
                "v"(off), "s"(scalar(base))
-               : "memory");
+               : "memory", "m0");
 }
 // All but N of this wave's loads have arrived.
 template <int N>
