@@ -387,7 +387,8 @@ static void dma_pick(const LinearArgs& a) {
 }
 
 hipError_t launch_linear_dma(const LinearArgs& a) {
-  if (a.w1) {
+  if (a.out == OUT_FP8 && !a.gated) return hipErrorInvalidValue;
+  if (a.gated) {
     if (a.out == OUT_BF16) dma_pick<true, OUT_BF16>(a);
     else if (a.out == OUT_F32) dma_pick<true, OUT_F32>(a);
     else dma_pick<true, OUT_FP8>(a);

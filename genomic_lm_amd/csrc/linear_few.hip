@@ -269,7 +269,7 @@ static void few_pick(const LinearArgs& a) {
 }
 
 hipError_t launch_linear_few(const LinearArgs& a) {
-  if (a.w1) {
+  if (a.gated) {
     if (a.out == OUT_BF16) few_pick<true, OUT_BF16>(a);
     else few_pick<true, OUT_F32>(a);
   } else {

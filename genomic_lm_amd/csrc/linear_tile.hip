@@ -176,9 +176,10 @@ static void tile_go(const LinearArgs& a) {
 // (us, fp32 and bf16 outputs, by one group, two, four): 30 x 9662 to 384 59, 48, 45; 333 x 1001 to 1000
 // 15, 13, 14; 500 x 1001 to 4000 -, 28, 37; 700 x 301 to 2000 -, 24, 31.
 hipError_t launch_linear_tile(const LinearArgs& a) {
-  const int64_t n128 = (a.T + 127) / 128 * ((a.N + 127) / 128) * (a.w1 ? 2 : 1);
+  const int64_t n128 = (a.T + 127) / 128 * ((a.N + 127) / 128) * (a.gated ? 2 : 1);
+  if (a.out == OUT_FP8 && !a.gated) return hipErrorInvalidValue;
   if (a.out == OUT_FP8) tile_go<4, 2, 2, 8, 1, true>(a);
-  else if (a.w1) {
+  else if (a.gated) {
     if (n128 >= 256) tile_go<2, 2, 4, 4, 1, true>(a);
     else tile_go<2, 2, 2, 4, 2, true>(a);
   } else {

@@ -13,7 +13,8 @@ namespace hyena {
 enum Act { ACT_NONE = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_SILU = 3 };
 enum OutKind { OUT_F32 = 0, OUT_BF16 = 1, OUT_FP8 = 2 };
 
-// y = x w0^T + bias, or (w1 set) act(x w0^T) * (x w1^T); strides in elements.
+// y = x w0^T + bias, or (gated) act(x w0^T) * (x w1^T); strides in elements.  Weights of no
+// columns may be null, the second one of a gated product too.
 struct LinearArgs {
   const uint8_t* x;
   int64_t x_stride;
@@ -25,8 +26,9 @@ struct LinearArgs {
   const uint8_t* w1;
   const float* s1;
   const float* bias;
+  bool gated;
   int act;
-  void* y;                    // rows of fp32, bf16 or e4m3
+  void* y;                    // rows of fp32, bf16, or (gated) e4m3
   int64_t y_stride;
   float* q_scale;             // (T, ceil(N / 128)), OUT_FP8 only
   OutKind out;

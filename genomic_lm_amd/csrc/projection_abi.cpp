@@ -23,15 +23,15 @@ hyena_status_t from_hip(hipError_t e) { return e == hipSuccess ? HYENA_OK : HYEN
 bool valid_io(hyena_dtype_t io) { return io == HYENA_F32 || io == HYENA_BF16; }
 size_t io_size(hyena_dtype_t io) { return io == HYENA_BF16 ? 2 : 4; }
 
-// Sizes, pointers and strides of a product; two: a second weight.
-hyena_status_t linear_impl(const hyena::LinearArgs& a, int64_t N, int64_t K, int64_t x_group, bool two,
+// Sizes, pointers and strides of a product.
+hyena_status_t linear_impl(const hyena::LinearArgs& a, int64_t N, int64_t K, int64_t x_group,
                            size_t ws_bytes = 0) {
   if (a.T < 0 || N < 0 || K < 0 || a.x_stride < 0 || a.xs_row < 0 || a.y_stride < 0 ||
       (x_group != 0 && x_group != HYENA_NORM_GROUP))
     return HYENA_ERR_INVALID_ARG;
   if (a.T == 0 || N == 0) return HYENA_OK;
   if (!a.y || (a.out == hyena::OUT_FP8 && !a.q_scale) ||
-      (K > 0 && (!a.x || !a.x_scale || !a.w0 || !a.s0 || (two && (!a.w1 || !a.s1)))))
+      (K > 0 && (!a.x || !a.x_scale || !a.w0 || !a.s0 || (a.gated && (!a.w1 || !a.s1)))))
     return HYENA_ERR_INVALID_ARG;
   if (a.T > 1 && a.y_stride < N) return HYENA_ERR_INVALID_ARG;
   const size_t align = a.out == hyena::OUT_FP8 ? 1 : a.out == hyena::OUT_BF16 ? 2 : 4;
@@ -77,9 +77,9 @@ hyena_status_t hyena_linear_fp8(const uint8_t* x, int64_t x_stride, const float*
                                 hipStream_t stream) {
   if (!valid_io(io)) return HYENA_ERR_INVALID_ARG;
   hyena::LinearArgs a{x, x_stride, x_scale, x_scale_stride, 0, w, w_scale, nullptr, nullptr, bias,
-                      hyena::ACT_NONE, y, y_stride, nullptr,
+                      false, hyena::ACT_NONE, y, y_stride, nullptr,
                       io == HYENA_BF16 ? hyena::OUT_BF16 : hyena::OUT_F32, T, 0, 0, stream};
-  return linear_impl(a, N, K, x_group, false);
+  return linear_impl(a, N, K, x_group);
 }
 
 hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const float* x_scale,
@@ -90,9 +90,9 @@ hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const 
                                       hyena_dtype_t io, hipStream_t stream) {
   if (!valid_io(io) || act < HYENA_ACT_NONE || act > HYENA_ACT_SILU) return HYENA_ERR_INVALID_ARG;
   hyena::LinearArgs a{x, x_stride, x_scale, x_scale_stride, 0, w_gate, gate_scale, w_up, up_scale, nullptr,
-                      static_cast<int>(act), h, h_stride, nullptr,
+                      true, static_cast<int>(act), h, h_stride, nullptr,
                       io == HYENA_BF16 ? hyena::OUT_BF16 : hyena::OUT_F32, T, 0, 0, stream};
-  return linear_impl(a, I, K, x_group, true);
+  return linear_impl(a, I, K, x_group);
 }
 
 hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
@@ -104,9 +104,9 @@ hyena_status_t hyena_gated_linear_fp8_quant(const uint8_t* x, int64_t x_stride,
                                             void* workspace, size_t ws_bytes, hipStream_t stream) {
   if (act < HYENA_ACT_NONE || act > HYENA_ACT_SILU) return HYENA_ERR_INVALID_ARG;
   hyena::LinearArgs a{x, x_stride, x_scale, x_scale_stride, 0, w_gate, gate_scale, w_up, up_scale, nullptr,
-                      static_cast<int>(act), q, I, q_scale, hyena::OUT_FP8, T, 0, 0, stream,
+                      true, static_cast<int>(act), q, I, q_scale, hyena::OUT_FP8, T, 0, 0, stream,
                       static_cast<float*>(workspace)};
-  return linear_impl(a, I, K, x_group, true, ws_bytes);
+  return linear_impl(a, I, K, x_group, ws_bytes);
 }
 
 size_t hyena_gated_linear_fp8_workspace_size(int64_t T, int64_t I, int64_t K) {
