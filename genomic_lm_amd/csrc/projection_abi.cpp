@@ -66,6 +66,21 @@ hyena_status_t quantize_impl(const void* x, int64_t x_stride, uint8_t* q, float*
   return from_hip(hyena::launch_quantize(a));
 }
 
+// Whether the rows of DH at t tok + h head (t < T, h < H) do not overlap: they are written by
+// different waves.  The strides times T and H fit 64 bits.
+bool rows_apart(int64_t tok, int64_t head, int64_t T, int64_t H, int64_t DH) {
+  if (H == 0 || (T == 1 && H == 1)) return true;
+  if ((T > 1 && tok < DH) || (H > 1 && head < DH)) return false;
+  if (T == 1 || H == 1 || tok >= (H - 1) * head + DH || head >= (T - 1) * tok + DH) return true;
+  // neither axis lies within a step of the other: h heads on from some row, the rows of the tokens
+  // to either side of that place
+  for (int64_t h = 1; h < H; ++h) {
+    const int64_t t = h * head / tok, past = h * head - t * tok;
+    if ((t >= 1 && t < T && past < DH) || (t + 1 < T && tok - past < DH)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -149,18 +164,14 @@ hyena_status_t hyena_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q
   if (!aligned_to(q, s) || !aligned_to(k, s) || !aligned_to(q_out, s) || !aligned_to(k_out, s) ||
       !aligned_to(positions, 4) || !aligned_to(inv_freq, 4) || !aligned_to(q_weight, 4) || !aligned_to(k_weight, 4))
     return HYENA_ERR_INVALID_ARG;
-  // rows that are written must not overlap
-  const auto apart = [&](int64_t tok, int64_t head, int64_t H) {
-    return H == 0 || ((H == 1 || head >= DH) && (T == 1 || tok >= DH));
-  };
-  if (!apart(qo_tok_stride, qo_head_stride, Hq) || !apart(ko_tok_stride, ko_head_stride, Hk))
-    return HYENA_ERR_INVALID_ARG;
   if (DH > HYENA_MAX_ROPE_DIM || Hq > HYENA_MAX_HEADS || Hk > HYENA_MAX_HEADS || T > (int64_t(1) << 25))
     return HYENA_ERR_UNSUPPORTED;
   for (const int64_t st : {q_tok_stride, k_tok_stride, qo_tok_stride, ko_tok_stride})
     if (st > kMost / T) return HYENA_ERR_UNSUPPORTED;
   for (const int64_t st : {q_head_stride, k_head_stride, qo_head_stride, ko_head_stride})
     if (st > kMost / HYENA_MAX_HEADS) return HYENA_ERR_UNSUPPORTED;
+  if (!rows_apart(qo_tok_stride, qo_head_stride, T, Hq, DH) || !rows_apart(ko_tok_stride, ko_head_stride, T, Hk, DH))
+    return HYENA_ERR_INVALID_ARG;
   hyena::RopeArgs a{{q, k}, {q_tok_stride, k_tok_stride}, {q_head_stride, k_head_stride}, {q_out, k_out},
                     {qo_tok_stride, ko_tok_stride}, {qo_head_stride, ko_head_stride}, {q_weight, k_weight},
                     {static_cast<int>(Hq), static_cast<int>(Hk)}, positions, inv_freq,

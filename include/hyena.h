@@ -703,7 +703,8 @@ hyena_status_t hyena_quantize_weight_fp8(const void* w, int64_t w_stride, uint8_
  * positions keep their angle; outputs are rounded once.
  *   q (T, Hq, DH), k (T, Hk, DH) `io`, token and head strides >= 0
  *   q_out, k_out : written, with strides of their own; may be q and k (equal
- *                  strides), and must not overlap them otherwise
+ *                  strides), and must not overlap them or each other
+ *                  otherwise; two rows of one output that overlap -> invalid
  *   positions : (T) int32; rows with a negative position (hyena_page_map gives
  *               them to tokens past the last) are neither read nor written.
  *               NULL with rotary_dim = 0 only.

@@ -43,3 +43,35 @@ def test_gated_products_take_gated_kernels():
             assert found[-1][0] == "quantize_runs_kernel", (case, found)
         for name, args, _, _ in products:
             assert is_gated(name, args) == (True, OUT[F32 if two else out]), (case, name, args)
+
+
+def rope(qo, ko, T=3, Hq=4, Hk=2, DH=128):
+    """Strides (token, head) of the outputs."""
+    at = 1 << 40
+    return ("hyena_qk_norm_rope", [at, 768, 128, 2 * at, 768, 128, at, at, DH, 0, 0, 0.0, None, None, 3 * at, *qo, 4 * at,
+                                   *ko, T, Hq, Hk, DH, G.BF16, None])
+
+
+def test_rotated_rows_that_meet_are_refused():
+    """Two (token, head) of an output in one place: written by different waves, in no order."""
+    fine = [((512, 128), (256, 128)), ((128, 384), (128, 384)), ((1000, 130), (300, 150)),
+            ((512, 128), (384, 256)), ((512, 128), (383, 255)),        # rows of one token in the gaps of another
+            ((1 << 40, 128), (256, 128))]
+    for case, (status, found) in zip(fine, launches([rope(*c) for c in fine])):
+        assert status == G.OK and len(found) == 1, case
+    meet = [((128, 128), (256, 128)), ((512, 128), (128, 128)), ((256, 128), (256, 128)), ((128, 256), (256, 128)),
+            ((511, 128), (256, 128)), ((128, 383), (256, 128)), ((385, 257), (255, 128)), ((0, 128), (256, 128)),
+            ((512, 128), (382, 255))]
+    for case, (status, found) in zip(meet, launches([rope(*c) for c in meet])):
+        assert status == G.ERR_INVALID_ARG and not found, case
+    # one token, or one head: the other stride has no say
+    alone = [rope((0, 128), (0, 128), T=1), rope((128, 0), (128, 0), Hq=1, Hk=1)]
+    assert all(status == G.OK and found for status, found in launches(alone))
+    # every pair of strides against every pair of rows
+    cases = [(a, b, T, H) for a in (3, 4, 5, 6, 8, 9, 12, 13, 20, 21) for b in (4, 5, 6, 8, 10, 12, 15, 16, 24)
+             for T, H in ((2, 2), (3, 5), (6, 3))]
+    got = launches([rope((a, b), (H * b + 4, b), T, H, 1, 4) for a, b, T, H in cases])
+    for (a, b, T, H), (status, _) in zip(cases, got):
+        at = sorted(t * a + h * b for t in range(T) for h in range(H))
+        apart = all(y - x >= 4 for x, y in zip(at, at[1:]))
+        assert (status == G.OK) == apart, (a, b, T, H)
