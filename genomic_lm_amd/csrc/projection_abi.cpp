@@ -56,10 +56,10 @@ hyena_status_t quantize_impl(const void* x, int64_t x_stride, uint8_t* q, float*
                              int block, int64_t T, int64_t D, hyena_dtype_t io, hipStream_t stream) {
   if (!valid_io(io) || T < 0 || D < 0 || x_stride < 0 || (group != 0 && group != HYENA_NORM_GROUP))
     return HYENA_ERR_INVALID_ARG;
-  if (T == 0 || D == 0) return HYENA_OK;
-  if (!x || !q || !q_scale || !aligned_to(x, io_size(io)) || !aligned_to(q_scale, 4))
+  if (T == 0 || (D == 0 && group)) return HYENA_OK;      // rows of no columns have a scale, but no runs
+  if ((D > 0 && (!x || !q)) || !q_scale || !aligned_to(x, io_size(io)) || !aligned_to(q_scale, 4))
     return HYENA_ERR_INVALID_ARG;
-  if (D > (group ? HYENA_MAX_PROJ_DIM : HYENA_MAX_NORM_DIM) || T > kMost / D || x_stride > kMost / T)
+  if (D > (group ? HYENA_MAX_PROJ_DIM : HYENA_MAX_NORM_DIM) || T > kMost / (D + 1) || x_stride > kMost / T)
     return HYENA_ERR_UNSUPPORTED;
   hyena::QuantArgs a{x, x_stride, q, q_scale, static_cast<int>(group), block, T, static_cast<int>(D),
                      io == HYENA_BF16, stream};

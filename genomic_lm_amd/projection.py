@@ -171,7 +171,7 @@ def quantize_fp8(x, group: int = 0, q=None, scale=None):
         sp = scale.data_ptr()
     else:
         sp = _vec("scale", scale, torch.float32, sshape, dev)
-    T = x.numel() // D if D else 0
+    T = x.numel() // D if D else math.prod(shape[:-1])
     _check("hyena_quantize_fp8", lib().hyena_quantize_fp8(xp, xs, qp, sp, group, T, D, _io(x), _stream(x)))
     return q, scale
 

@@ -679,7 +679,7 @@ size_t hyena_gated_linear_fp8_workspace_size(int64_t T, int64_t I, int64_t K);
  *   0 or NaN),  q = e4m3(x / scale),  x ~ q * scale.
  * An infinity makes its run's scale infinite: its own code NaN, the others 0.
  *   x : T rows of D `io`, row stride x_stride >= 0;  q : (T, D), contiguous
- *   group = 0: q_scale (T), D <= HYENA_MAX_NORM_DIM;  group = HYENA_NORM_GROUP:
+ *   group = 0: q_scale (T) (D = 0: all 1), D <= HYENA_MAX_NORM_DIM;  group = HYENA_NORM_GROUP:
  *   q_scale (T, ceil(D / 128))
  *   w : N rows of K `io`;  scale : (ceil(N / 128), ceil(K / 128))
  */

@@ -34,3 +34,14 @@ def test_gated_without_columns(T, I):
     q, s = G.gated_linear_fp8(*args, dtype=U8, out=buf[:T * I].view(T, I), scale=scale)
     assert (q & 0x7F == 0).all() and (s == 1).all()
     assert (buf[T * I:] == 0x38).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantize_without_columns(dtype):
+    """An empty row has no magnitude: scale 1, as a row of zeros."""
+    for shape in ((5, 0), (2, 3, 0)):
+        scale = torch.full(shape[:-1], 7.0, device=dev())
+        q, s = G.quantize_fp8(torch.empty(shape, dtype=dtype, device=dev()), scale=scale)
+        assert q.shape == shape and s is scale and (s == 1).all()
+        q, s = G.quantize_fp8(torch.empty(shape, dtype=dtype, device=dev()), group=128)
+        assert s.shape == shape

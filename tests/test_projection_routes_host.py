@@ -75,3 +75,18 @@ def test_rotated_rows_that_meet_are_refused():
         at = sorted(t * a + h * b for t in range(T) for h in range(H))
         apart = all(y - x >= 4 for x, y in zip(at, at[1:]))
         assert (status == G.OK) == apart, (a, b, T, H)
+
+
+def test_rows_of_no_columns_are_given_a_scale():
+    at = 1 << 40
+    none = [("hyena_quantize_fp8", [None, 0, None, at, 0, 5, 0, io, None]) for io in (G.BF16, G.F32)]
+    for status, found in launches(none):
+        assert status == G.OK and [k[0] for k in found] == ["quantize_rows_kernel"]
+    # nothing to write: no rows, or no runs
+    for status, found in launches([("hyena_quantize_fp8", [None, 0, None, None, 128, 5, 0, G.BF16, None]),
+                                   ("hyena_quantize_fp8", [None, 0, None, None, 0, 0, 0, G.BF16, None]),
+                                   ("hyena_quantize_weight_fp8", [None, 0, None, None, 5, 0, G.BF16, None])]):
+        assert status == G.OK and not found
+    for bad in ([None, 0, None, None, 0, 5, 0, G.BF16, None], [None, 4, at, at, 0, 5, 4, G.BF16, None],
+                [at, 4, None, at, 0, 5, 4, G.BF16, None]):
+        assert launches([("hyena_quantize_fp8", bad)]) == [(G.ERR_INVALID_ARG, [])]
