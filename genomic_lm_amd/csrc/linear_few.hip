@@ -256,9 +256,9 @@ static void few_pick(const LinearArgs& a) {
     const dim3 grid(static_cast<unsigned>((a.N + 15) / 16), static_cast<unsigned>((a.T + 15) / 16));
     linear_few_kernel<8, 1, 4, GATED, OUT><<<grid, 512, 0, a.stream>>>(a);
   } else if (a.T <= 16) {
-    if (!GATED && many) few_dma_go<4, 1, 2, false, OUT>(a);
-    else if (many) few_dma_go<4, 1, 1, GATED, OUT>(a);
-    else few_dma_go<8, 1, 1, GATED, OUT>(a);
+    if (!many) few_dma_go<8, 1, 1, GATED, OUT>(a);
+    else if constexpr (GATED) few_dma_go<4, 1, 1, true, OUT>(a);
+    else few_dma_go<4, 1, 2, false, OUT>(a);
   } else if (a.T <= 32) {
     if (!GATED && many) few_dma_go<4, 2, 2, false, OUT>(a);
     else few_dma_go<4, 2, 1, GATED, OUT>(a);

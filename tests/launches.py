@@ -28,6 +28,7 @@ static dim3_t grid, block;
 static size_t shared;
 static void* stream;
 const char* recorded(void) { return text; }
+const char* name_of(int i) { return i < n_known ? known[i].name : 0; }
 void forget(void) { text[0] = 0; }
 void** __hipRegisterFatBinary(const void* data) { static void* h[1]; (void)data; return h; }
 void __hipUnregisterFatBinary(void** m) { (void)m; }
@@ -63,19 +64,30 @@ int hipGetSymbolAddress(void** p, const void* s) { (void)s; *p = 0; return 1; }
 CHILD = """
 import ctypes, json, sys
 recorder = ctypes.CDLL(sys.argv[1], ctypes.RTLD_GLOBAL)     # found before the library's own runtime
-recorder.recorded.restype = ctypes.c_char_p
+recorder.recorded.restype = recorder.name_of.restype = ctypes.c_char_p
 import genomic_lm_amd as G
+G.lib()
+names, i = [], 0
+while (name := recorder.name_of(i)) is not None:
+    names.append(name.decode())
+    i += 1
 out = []
 for name, args in json.load(sys.stdin):
     recorder.forget()
     status = getattr(G.lib(), name)(*args)
     out.append([status, recorder.recorded().decode().split("\\n")[:-1]])
-json.dump(out, sys.stdout)
+json.dump([out, [n for n in names if n.startswith("_ZN5hyena")]], sys.stdout)
 """
 
 
-def launches(calls):
-    """[(entry point, arguments)] -> [(status, [(kernel, template arguments, grid, threads)])]."""
+def _kernel(name):
+    """(kernel, template arguments) of a mangled name."""
+    m = re.match(r"_ZN5hyenaL?(?:12_GLOBAL__N_1)?\d+([a-z_0-9]+?)(?:I(.*?)EEv|E)", name)
+    assert m, name
+    return m.group(1), tuple(int(v) for v in re.findall(r"L[ib](\d+)E", (m.group(2) or "") + "E"))
+
+
+def _record(calls):
     with tempfile.TemporaryDirectory() as d:
         src, lib = os.path.join(d, "recorder.c"), os.path.join(d, "recorder.so")
         with open(src, "w") as f:
@@ -84,17 +96,24 @@ def launches(calls):
         r = subprocess.run([sys.executable, "-c", CHILD, lib], input=json.dumps(calls), capture_output=True, text=True,
                            cwd=ROOT, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+    return json.loads(r.stdout)
+
+
+def launches(calls):
+    """[(entry point, arguments)] -> [(status, [(kernel, template arguments, grid, threads)])]."""
     out = []
-    for status, lines in json.loads(r.stdout):
+    for status, lines in _record(calls)[0]:
         found = []
         for line in lines:
             name, x, y, z, threads = line.split()
-            m = re.match(r"_ZN5hyenaL?(?:12_GLOBAL__N_1)?\d+([a-z_0-9]+?)(?:I(.*?)EEv|E)", name)
-            assert m, name
-            found.append((m.group(1), tuple(int(v) for v in re.findall(r"L[ib](\d+)E", (m.group(2) or "") + "E")),
-                          (int(x), int(y), int(z)), int(threads)))
+            found.append((*_kernel(name), (int(x), int(y), int(z)), int(threads)))
         out.append((status, found))
     return out
+
+
+def library_kernels():
+    """(kernel, template arguments) of every kernel of the library's namespace."""
+    return [_kernel(name) for name in _record([])[1]]
 
 
 FAR = 1 << 40                # an aligned place that is never followed

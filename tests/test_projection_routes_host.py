@@ -4,7 +4,8 @@ import os
 import pytest
 
 import genomic_lm_amd as G
-from tests.launches import BF, F8, F32, gated, launches
+from tests import projection_sizes as sizes
+from tests.launches import BF, F8, F32, gated, launches, library_kernels, linear
 
 OUT = {F32: 0, BF: 1, F8: 2}
 
@@ -57,21 +58,22 @@ def test_rotated_rows_that_meet_are_refused():
     fine = [((512, 128), (256, 128)), ((128, 384), (128, 384)), ((1000, 130), (300, 150)),
             ((512, 128), (384, 256)), ((512, 128), (383, 255)),        # rows of one token in the gaps of another
             ((1 << 40, 128), (256, 128))]
-    for case, (status, found) in zip(fine, launches([rope(*c) for c in fine])):
-        assert status == G.OK and len(found) == 1, case
     meet = [((128, 128), (256, 128)), ((512, 128), (128, 128)), ((256, 128), (256, 128)), ((128, 256), (256, 128)),
             ((511, 128), (256, 128)), ((128, 383), (256, 128)), ((385, 257), (255, 128)), ((0, 128), (256, 128)),
             ((512, 128), (382, 255))]
-    for case, (status, found) in zip(meet, launches([rope(*c) for c in meet])):
-        assert status == G.ERR_INVALID_ARG and not found, case
     # one token, or one head: the other stride has no say
     alone = [rope((0, 128), (0, 128), T=1), rope((128, 0), (128, 0), Hq=1, Hk=1)]
-    assert all(status == G.OK and found for status, found in launches(alone))
     # every pair of strides against every pair of rows
     cases = [(a, b, T, H) for a in (3, 4, 5, 6, 8, 9, 12, 13, 20, 21) for b in (4, 5, 6, 8, 10, 12, 15, 16, 24)
              for T, H in ((2, 2), (3, 5), (6, 3))]
-    got = launches([rope((a, b), (H * b + 4, b), T, H, 1, 4) for a, b, T, H in cases])
-    for (a, b, T, H), (status, _) in zip(cases, got):
+    got = launches([rope(*c) for c in fine] + alone + [rope(*c) for c in meet]
+                   + [rope((a, b), (H * b + 4, b), T, H, 1, 4) for a, b, T, H in cases])
+    n = len(fine) + len(alone)
+    for i, (status, found) in enumerate(got[:n]):
+        assert status == G.OK and len(found) == 1, i
+    for case, (status, found) in zip(meet, got[n:]):
+        assert status == G.ERR_INVALID_ARG and not found, case
+    for (a, b, T, H), (status, _) in zip(cases, got[n + len(meet):]):
         at = sorted(t * a + h * b for t in range(T) for h in range(H))
         apart = all(y - x >= 4 for x, y in zip(at, at[1:]))
         assert (status == G.OK) == apart, (a, b, T, H)
@@ -79,14 +81,35 @@ def test_rotated_rows_that_meet_are_refused():
 
 def test_rows_of_no_columns_are_given_a_scale():
     at = 1 << 40
-    none = [("hyena_quantize_fp8", [None, 0, None, at, 0, 5, 0, io, None]) for io in (G.BF16, G.F32)]
-    for status, found in launches(none):
-        assert status == G.OK and [k[0] for k in found] == ["quantize_rows_kernel"]
-    # nothing to write: no rows, or no runs
-    for status, found in launches([("hyena_quantize_fp8", [None, 0, None, None, 128, 5, 0, G.BF16, None]),
-                                   ("hyena_quantize_fp8", [None, 0, None, None, 0, 0, 0, G.BF16, None]),
-                                   ("hyena_quantize_weight_fp8", [None, 0, None, None, 5, 0, G.BF16, None])]):
-        assert status == G.OK and not found
-    for bad in ([None, 0, None, None, 0, 5, 0, G.BF16, None], [None, 4, at, at, 0, 5, 4, G.BF16, None],
-                [at, 4, None, at, 0, 5, 4, G.BF16, None]):
-        assert launches([("hyena_quantize_fp8", bad)]) == [(G.ERR_INVALID_ARG, [])]
+    f, w = "hyena_quantize_fp8", "hyena_quantize_weight_fp8"
+    calls = [(f, [None, 0, None, at, 0, 5, 0, G.BF16, None]), (f, [None, 0, None, at, 0, 5, 0, G.F32, None]),
+             # nothing to write: no runs, no rows
+             (f, [None, 0, None, None, 128, 5, 0, G.BF16, None]), (f, [None, 0, None, None, 0, 0, 0, G.BF16, None]),
+             (w, [None, 0, None, None, 5, 0, G.BF16, None]),
+             # what is needed and missing
+             (f, [None, 0, None, None, 0, 5, 0, G.BF16, None]), (f, [None, 4, at, at, 0, 5, 4, G.BF16, None]),
+             (f, [at, 4, None, at, 0, 5, 4, G.BF16, None])]
+    got = [(status, [k[0] for k in found]) for status, found in launches(calls)]
+    assert got[:2] == [(G.OK, ["quantize_rows_kernel"])] * 2
+    assert got[2:5] == [(G.OK, [])] * 3
+    assert got[5:] == [(G.ERR_INVALID_ARG, [])] * 3
+
+
+def test_the_tests_sizes_take_every_kernel():
+    """Each size of projection_sizes.py takes the kernel that it names, and together they take all that there are."""
+    calls, want = [], []
+    for make, table, outs in ((linear, sizes.PLAIN, (BF, F32)), (gated, sizes.GATED, (BF, F32)), (gated, sizes.CODES, (F8,))):
+        for T, N, ks, kernel in table:
+            for K in ks:
+                for out in outs:
+                    calls.append(make(T, K, N, out))
+                    name, *tile = kernel[out] if isinstance(kernel, dict) else kernel
+                    want.append((T, K, N, out, name, tuple(tile)))
+    taken = set()
+    for case, (status, found) in zip(want, launches(calls)):
+        assert status == G.OK and len(found) == 1, (case, found)
+        name, args, _, _ = found[0]
+        assert (name, args[:len(case[-1])]) == case[-2:], (case, name, args)
+        taken.add((name, args))
+    there = {k for k in library_kernels() if k[0].startswith("linear_")}
+    assert taken == there, (there - taken, taken - there)
