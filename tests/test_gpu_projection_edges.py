@@ -1,10 +1,25 @@
-"""The 8-bit projections where they can go wrong."""
+"""The 8-bit projections where they can go wrong, and every kernel of the products at sizes that take it
+(projection_sizes.py).
+
+Tolerances, stated before any run: those of test_gpu_projection.py for single elements.  For the norm of a bf16
+output's error against that of the output, where the signs of the products are random: the rounding of a value in [2^e, 2^(e+1))
+is spread evenly over 2^(e-8) to either side, at most 2^-8 / sqrt 3 of the value in the mean square; a product cut below
+2^-13 of the largest of its eight loses up to that much, 2^-13 / sqrt 3 of it in the mean square, the largest squared is at
+most the eight squares' sum, so the cuts of a sum of K products of mean square p2 come to at most
+sqrt(K 8 p2 / 3) 2^-13 against sqrt(K p2): 2^-13 sqrt(8 / 3).  Together 2.27e-3, allowed 2.3e-3; a column of
+K = 1040 left out is 3e-2.
+
+Small whole numbers (and scales that are powers of two) have exact sums in any order, and no product below 2^-13 of
+another: those outputs are compared for equality."""
 import numpy as np
 import pytest
 import torch
 
 import genomic_lm_amd as G
-from tests.gpu_util import dev
+from tests import projection_ref as ref
+from tests import projection_sizes as sizes
+from tests.gpu_util import dev, to_f64
+from tests.test_gpu_projection import bits_equal, check_gated, f32, half, operands, put, sum_error, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +60,85 @@ def test_quantize_without_columns(dtype):
         assert q.shape == shape and s is scale and (s == 1).all()
         q, s = G.quantize_fp8(torch.empty(shape, dtype=dtype, device=dev()), group=128)
         assert s.shape == shape
+
+
+# ------------------------------------------------------------------ every kernel
+def whole(rng, most, T, K, N, group, weights=1):
+    """Operands of whole numbers up to `most` with scales 1/2, 1 and 2, and what they stand for."""
+    runs = -(-K // 128)
+    x = rng.integers(-most, most + 1, (T, K))
+    xs = 2.0 ** rng.integers(-1, 2, (T, runs) if group else (T,))
+    out, wide = [put(x).to(F8), put(xs)], []
+    each = np.repeat(xs, 128, 1)[:, :K] if group else xs[:, None]
+    xw = x * each
+    for _ in range(weights):
+        w = rng.integers(-most, most + 1, (N, K))
+        ws = 2.0 ** rng.integers(-1, 2, (-(-N // 128), runs))
+        out += [put(w).to(F8), put(ws)]
+        wide.append(xw @ (w * np.repeat(np.repeat(ws, 128, 0)[:N], 128, 1)[:, :K]).T)
+    return out, wide
+
+
+def rounded(a, dtype):
+    """Values of at most 24 bits in a type: one rounding."""
+    assert (a == f32(a)).all()
+    return put(a).to(dtype)
+
+
+@pytest.mark.parametrize("T,K,N", sizes.cases(sizes.PLAIN))
+def test_exact_sums(T, K, N):
+    rng = np.random.default_rng(T + K + N)
+    for group in (128, 0):
+        args, (want,) = whole(rng, 4, T, K, N, group)
+        b = rng.integers(-100, 101, N)
+        for dtype in (BF, F32):
+            assert bits_equal(G.linear_fp8(*args, dtype=dtype), rounded(want, dtype)), (group, dtype)
+            assert bits_equal(G.linear_fp8(*args, bias=put(b), dtype=dtype), rounded(want + b, dtype)), (group, dtype)
+
+
+@pytest.mark.parametrize("T,K,N", sizes.cases(sizes.GATED) + sizes.cases(sizes.CODES))
+def test_exact_gated(T, K, N):
+    rng = np.random.default_rng(T + K + N)
+    args, (g, u) = whole(rng, 1, T, K, N, 128, 2)
+    h = g * u
+    for dtype in (BF, F32):
+        assert bits_equal(G.gated_linear_fp8(*args, act="none", dtype=dtype) + 0, rounded(h, dtype) + 0), dtype
+    q, scale = G.gated_linear_fp8(*args, act="none", dtype=F8)
+    want, wscale = G.quantize_fp8(rounded(h, F32), 128)
+    assert bits_equal(scale, wscale) and torch.equal(q.float(), want.float())
+
+
+@pytest.mark.parametrize("T,K,N", [c for c in sizes.cases(sizes.PLAIN) if c[0] == 2100])
+@pytest.mark.parametrize("group", [0, 128])
+def test_large_tiles(T, K, N, group):
+    rng = np.random.default_rng(T + K + N + group)
+    x, xs, ws = operands(rng, T, K, N, group)
+    b = f32(rng.normal(size=N))
+    args = to_gpu(x, xs, ws)
+    want, size = ref.product(x, xs, *ws[0])
+    want, size = want + b.astype(np.float64), size + np.abs(b)
+    for dtype in (BF, F32):
+        e = np.abs(to_f64(G.linear_fp8(*args, bias=put(b), dtype=dtype)) - want)
+        tol = sum_error(K, size, dtype)
+        assert (e <= tol + half(dtype) * (np.abs(want) + tol)).all(), (dtype, (e - tol).max())
+        far = np.linalg.norm(e) / np.linalg.norm(want)
+        assert dtype == F32 or far <= 2.3e-3, far
+
+
+@pytest.mark.parametrize("T,K,N,act", [(*c, act) for (c, act) in zip(
+    [c for c in sizes.cases(sizes.GATED) if c[0] == 2100], 4 * ("gelu", "silu", "gelu_tanh"))])
+def test_large_gated_tiles(T, K, N, act):
+    rng = np.random.default_rng(T + K + N)
+    x, xs, ws = operands(rng, T, K, N, 128, 2)
+    xs = xs / f32(60 * K ** 0.5)
+    args = to_gpu(x, xs, ws)
+    for dtype in (BF, F32):
+        check_gated(x, xs, ws, act, G.gated_linear_fp8(*args, act=act, dtype=dtype), dtype)
+
+
+@pytest.mark.parametrize("T,K,N,act", [(*c, act) for (c, act) in zip(sizes.cases(sizes.CODES), 4 * ("gelu", "silu"))])
+def test_large_code_tiles(T, K, N, act):
+    rng = np.random.default_rng(T + K + N)
+    x, xs, ws = operands(rng, T, K, N, 128, 2)
+    xs = xs / f32(60 * K ** 0.5)
+    check_gated(x, xs, ws, act, G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=F8), None)
