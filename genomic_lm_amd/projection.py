@@ -88,7 +88,9 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, out=None, dtype=torch.bfloat16
     """y = x w^T + bias of 8-bit operands: x (..., K) with x_scale (...) or (..., ceil(K / 128)),
     w (N, K) with w_scale (ceil(N / 128), ceil(K / 128)), bias (N) fp32 or None.
 
-    Returns y (..., N) in `dtype` (bfloat16 or float32), or in out and its type."""
+    Returns y (..., N) in `dtype` (bfloat16 or float32), or in out and its type.  float32: exact products,
+    fp32 sums; bfloat16 in calls of more than 16 rows: products of eight columns may be cut below 2^-13 of their
+    largest, up to 2^-10 of sum |x| |w|."""
     head, T, K, rows = _operand(x, x_scale)
     dev = x.get_device()
     wp, N = _weight("w", w, w_scale, K, dev)
@@ -109,7 +111,7 @@ def gated_linear_fp8(x, x_scale, w_gate, gate_scale, w_up, up_scale, act: str = 
     """h = act(x w_gate^T) * (x w_up^T), operands as in linear_fp8; act "gelu", "gelu_tanh",
     "silu" or "none".
 
-    dtype bfloat16 or float32: returns h (..., I) (out: written instead, in its type).
+    dtype bfloat16 or float32: returns h (..., I) (out: written instead, in its type); sums as in linear_fp8.
     dtype float8_e4m3fn: returns (q (..., I), scale (..., ceil(I / 128))), the operand of
     the next linear_fp8, written to out and scale if given; workspace: gated_linear_fp8_workspace_size
     bytes, made here if not given."""

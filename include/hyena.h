@@ -494,7 +494,8 @@ hyena_status_t hyena_add_rmsnorm(const void* x, int64_t x_stride, const void* re
  * 8-bit in_proj takes (evo2_flash README, layer_names table:
  * 'blocks.N.projections').
  *   scale = max|y| / 448 over the run, at least 2^-140 (1 where max|y| is 0 or NaN),
- *   q = e4m3(y / scale),  y ~ q * scale.
+ *   q = e4m3(y * (1 / scale)),  y ~ q * scale;  each step rounded to fp32 (scales
+ *   below 2^-100: y / scale).
  *   q       : (T, D) e4m3, contiguous
  *   q_scale : fp32; group = 0: one run per row, (T); group = HYENA_NORM_GROUP:
  *             runs of 128 columns (the last one shorter), (T, ceil(D / 128))
@@ -627,8 +628,13 @@ size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int6
 /*
  * hyena_linear_fp8 -- y = x w^T + bias.
  *   y[t, n] = sum_b (x_scale[t, b] * w_scale[n / 128, b]) * sum_{k in run b} x[t, k] w[n, k] + bias[n]
- * Products and sums are fp32, the two scales are multiplied first; y is rounded
- * once.  K = 0 gives the bias.
+ * The two scales are multiplied first; y is rounded once.  K = 0 gives the bias.
+ * With an fp32 output, and in calls of up to 16 rows, products are exact and their
+ * sums fp32.  In larger calls with a bf16 output the matrix unit may add the products
+ * of eight columns at a time, each cut below 2^-13 of the largest of its eight: an
+ * error of up to 2^-10 of sum |x| |w| (scales included), 1.5e-5 of y's norm on
+ * normally distributed codes.  So a row may differ between a prompt and a decode
+ * step; ask for fp32 where large products cancel.
  *   bias : (N) fp32, or NULL (0);  y : T rows of N `io`, row stride y_stride >= N
  * The order of the sums is fixed for a T: a call repeated gives the same bits.
  */
@@ -641,7 +647,8 @@ hyena_status_t hyena_linear_fp8(const uint8_t* x, int64_t x_stride, const float*
 /*
  * hyena_gated_linear_fp8 -- the first half of the gated MLP in one pass:
  *   h = act(x w_gate^T) * (x w_up^T)
- * with both products as hyena_linear_fp8 has them, unrounded; h is rounded once.
+ * with both products as hyena_linear_fp8 has them for this output, unrounded; h is
+ * rounded once.
  *   w_gate, w_up : (I, K) with their scales;  act : hyena_act_t
  *   h : T rows of I `io`, row stride h_stride >= I
  */
@@ -654,8 +661,8 @@ hyena_status_t hyena_gated_linear_fp8(const uint8_t* x, int64_t x_stride, const 
 
 /*
  * hyena_gated_linear_fp8_quant -- the same with h in e4m3 and a scale per row and
- * 128 columns, the operand of the MLP's last projection; scales and codes by the
- * rules of hyena_add_rmsnorm_fp8.
+ * 128 columns, the operand of the MLP's last projection; products exact and sums
+ * fp32 at any size, scales and codes by the rules of hyena_quantize_fp8.
  *   q : (T, I) e4m3, contiguous;  q_scale : (T, ceil(I / 128)) fp32
  * Workspace (device, 16-byte aligned, no initial contents) of
  * hyena_gated_linear_fp8_workspace_size bytes (0 for many rows); NULL, short or
@@ -676,7 +683,8 @@ size_t hyena_gated_linear_fp8_workspace_size(int64_t T, int64_t I, int64_t K);
  * of out_proj); hyena_quantize_weight_fp8 -- a weight, with a scale per block of
  * 128 rows by 128 columns.
  *   scale = max|x| / 448 over the run or block, at least 2^-140 (1 where max|x| is
- *   0 or NaN),  q = e4m3(x / scale),  x ~ q * scale.
+ *   0 or NaN),  q = e4m3(x * (1 / scale)),  x ~ q * scale;
+ *   each step rounded to fp32 (scales below 2^-100: x / scale).
  * An infinity makes its run's scale infinite: its own code NaN, the others 0.
  *   x : T rows of D `io`, row stride x_stride >= 0;  q : (T, D), contiguous
  *   group = 0: q_scale (T) (D = 0: all 1), D <= HYENA_MAX_NORM_DIM;  group = HYENA_NORM_GROUP:

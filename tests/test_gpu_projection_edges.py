@@ -142,3 +142,48 @@ def test_large_code_tiles(T, K, N, act):
     x, xs, ws = operands(rng, T, K, N, 128, 2)
     xs = xs / f32(60 * K ** 0.5)
     check_gated(x, xs, ws, act, G.gated_linear_fp8(*to_gpu(x, xs, ws), act=act, dtype=F8), None)
+
+
+@pytest.mark.parametrize("T,N", [(4, 400), (40, 400), (700, 1500), (1100, 1500), (2100, 2100), (2100, 4000)])
+@pytest.mark.parametrize("K,apart", [(1040, 1), (1040, 500), (1041, 1)])
+def test_large_products_that_cancel(T, N, K, apart):
+    """Two products of 448 * 448 that cancel, side by side or in different groups of eight columns, among whole
+    numbers up to 4: fp32 outputs and calls of few rows keep every bit; bf16 outputs of many rows may lose what lies
+    below 2^-13 of the largest product of eight columns, at most 2^-10 of the magnitudes."""
+    rng = np.random.default_rng(T + N + K + apart)
+    runs = -(-K // 128)
+    x, w = rng.integers(-4, 5, (T, K)).astype(np.float64), rng.integers(-4, 5, (N, K)).astype(np.float64)
+    a = 7 if apart == 1 else 130
+    x[:, [a, a + apart]] = 448
+    w[:, a], w[:, a + apart] = 448, -448
+    want, size = x @ w.T, np.abs(x) @ np.abs(w).T
+    assert np.abs(want).max() < 2 ** 20
+    args = (put(x).to(F8), torch.ones((T, runs), device=dev()), put(w).to(F8),
+            torch.ones((-(-N // 128), runs), device=dev()))
+    assert bits_equal(G.linear_fp8(*args, dtype=F32), rounded(want, F32))
+    y = G.linear_fp8(*args)
+    if T <= (64 if K % 16 == 0 else 16):
+        assert bits_equal(y, rounded(want, BF))
+    cut = 2.0 ** -10 * size
+    e = np.abs(to_f64(y) - want)
+    assert (e <= cut + half(BF) * (np.abs(want) + cut)).all()
+    h = G.gated_linear_fp8(*args, *args[2:], act="none", dtype=F32)
+    q, scale = G.gated_linear_fp8(*args, *args[2:], act="none", dtype=F8)
+    want = rounded(f32(want) * f32(want), F32)           # one rounding, of the product
+    qw, sw = G.quantize_fp8(want, 128)
+    assert bits_equal(h, want) and bits_equal(scale, sw) and torch.equal(q.float(), qw.float())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 128])
+def test_codes_by_the_stated_steps(dtype, rows):
+    """scale = max|x| / 448 and the code of x * (1 / scale), each step rounded to fp32."""
+    rng = np.random.default_rng(rows)
+    x = put(rng.normal(size=(256, 384)) * np.exp(2 * rng.normal(size=(256, 1))), dtype)
+    q, s = G.quantize_weight_fp8(x) if rows > 1 else G.quantize_fp8(x, 128)
+    v = x.float().cpu().numpy()
+    top = np.abs(v).reshape(256 // rows, rows, 3, 128).max((1, 3))
+    scale = top / f32(448)
+    z = v * np.repeat(np.repeat(f32(1) / scale, rows, 0), 128, 1)
+    assert scale.dtype == z.dtype == np.float32
+    assert bits_equal(s, put(scale)) and bits_equal(q, torch.from_numpy(z).to(F8).to(dev()))
