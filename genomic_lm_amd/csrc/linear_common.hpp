@@ -74,9 +74,10 @@ __device__ __forceinline__ i32x4 codes16(const uint8_t* p, int n) {
 // act(g) * u, in forms without a difference of near equals.
 //
 // The gelu is g Phi(g), Phi(-|g|) = exp(-g^2 / 2) erfcx(|g| / sqrt 2) / 2, where erfcx(z) =
-// exp(z^2) erfc(z) = t q(t), t = 1 / (1 + 0.35 z), with a polynomial q fitted over all z >= 0 to
-// a relative 2.4e-8 (least squares at Chebyshev points, reweighted towards the largest error).  About
-// 20 instructions; the device library's erfc, ten times that, took a fifth of the time of a gated
+// exp(z^2) erfc(z) = t q(t), t = 1 / (1 + 0.35 z), with a polynomial q fitted over all z >= 0
+// (least squares at Chebyshev points, reweighted towards the largest error): with the coefficients as
+// they stand here, in fp32, within a relative 3.5e-8 of it, taken in 64 bits.  About 20
+// instructions; the device library's erfc, ten times that, took a fifth of the time of a gated
 // product of 8192 x 4096 to 11008.
 template <int ACT>
 __device__ __forceinline__ float gate(float g, float u) {
