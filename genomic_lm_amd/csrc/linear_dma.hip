@@ -1,9 +1,10 @@
 // linear_dma.hip -- block-scaled e4m3 products of many rows whose rows are
 // 16-byte aligned: LDS tiles filled straight from memory.
 //
-// Bound by the matrix cores, at the power limit (1.9 GHz): 8192 x 4096 to 12288, bf16 outputs, 376 to
-// 381 us, 2.2 PFLOP/s; gated to 11008 with e4m3 outputs, on the bf16 instructions, 1169 us, 1.26
-// PFLOP/s.  A load to LDS moves 1 KB in 16 cycles and needs no registers, which hold the sums (256 x
+// Bound by the matrix cores and the scales' FMAs beside them, at 1.9 to 2.05 GHz: 8192 x 4096 to 12288,
+// bf16 outputs, 368 to 388 us by card, 2.1 to 2.2 PFLOP/s, fp32 ones, on the bf16 instructions, 690, 1.2;
+// gated to 11008 with e4m3 outputs 1197 to 1235, 1.20 to 1.23 PFLOP/s; the matrix pipes are busy half of the
+// cycles.  A load to LDS moves 1 KB in 16 cycles and needs no registers, which hold the sums (256 x
 // 256 fp32 in eight waves); a tile staged through registers spilled 210 of them.
 #include "linear_tile.hpp"
 
@@ -340,11 +341,11 @@ bool linear_dma_takes(const LinearArgs& a) {
 // Tiles by the rounds of workgroups that they make on 256 CUs: one of 256 x 256 to a CU, two of 128 x
 // 128, whose round takes 0.7 to 0.8 of the time of one of the former.  Where there is less than a
 // round, two or four groups of waves share the K of a tile.  Measured (us, bf16 outputs, the tile
-// that is taken, then the next): 8192 x 4096 to 12288 256 x 256 376, 128 x 128 486; 512 to 12288 (96 tiles
-// of 256 x 256, 384 of 128 x 128) 128 x 128 37, 51; 512 to 16384 (128, 512) 42, 53; 512 to 4096 (128 of
-// 128 x 128) by two groups 22, by one 31.  Up to 100 tiles that whole rounds leave go into a launch
-// of smaller ones: 4096 to 4352 (272 tiles) 83, in one launch 117; 1500 to 12288 (288) 86, 107;
-// gated 1000 to 10928 (344) 118, 123; but 3000 x 2048 to 8192 (384) 67, 66.
+// that is taken, then the next): 8192 x 4096 to 12288 256 x 256 368, 128 x 128 471; 512 to 12288 (96 tiles
+// of 256 x 256, 384 of 128 x 128) 128 x 128 38, 52; 512 to 16384 (128, 512) 41, 54; 512 to 4096 (128 of
+// 128 x 128) by two groups 23, by one 33.  Up to 100 tiles that whole rounds leave go into a launch
+// of smaller ones: 4096 to 4352 (272 tiles) 74, in one launch 108; 1500 to 12288 (288) 84, 108;
+// gated 1000 to 10928 (344) 100, 114; but 3000 x 2048 to 8192 (384) 67, 66.
 template <bool GATED, int OUT>
 static void dma_pick(const LinearArgs& a) {
   constexpr int CN = GATED ? 128 : 256;                  // columns of a tile of 256 rows

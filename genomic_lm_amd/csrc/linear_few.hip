@@ -1,8 +1,10 @@
 // linear_few.hip -- block-scaled e4m3 products of few rows (decode steps) or few outputs, and the
 // choice among the products.
 //
-// Bound by reading the weights: 16 x 11008 to 4096 10.5 us, 4.3 TB/s; 1 x 4096 to 12288 9.0 us, 5.6
-// TB/s from the last-level cache; gated 4 x 4096 to 11008 16.4 us, 5.5 TB/s.
+// Bound by reading the weights up to about 32 rows: 16 x 11008 to 4096 10.5 to 11.5 us by card, 4.0 to 4.3
+// TB/s; 1 x 4096 to 12288 9.6 us, 5.2 TB/s from the last-level cache; gated 4 x 4096 to 11008 18 us,
+// 5.0 TB/s.  Beyond, by the tokens that every workgroup loads for its 16 or 32 columns: 64 x 4096
+// to 4096 9.0 to 9.6 us, 1.9 TB/s.
 #include "linear_common.hpp"
 
 namespace hyena {
@@ -60,7 +62,7 @@ __device__ __forceinline__ void few_rows(LinearArgs& a) {
 // 16 MT tokens, and takes every WK-th run of K, through a ring of two runs in LDS of its own,
 // filled straight from memory: loads of operands to registers, 16 rows in one instruction, pass
 // the address unit at a quarter of its 64 bytes per cycle (16 x 11008 to 4096 14.0 us that way,
-// 10.1 this).  No wave waits for another before the end, where their sums are added.
+// 11 this).  No wave waits for another before the end, where their sums are added.
 template <int WK, int MT, int NI, bool GATED, int OUT>
 __global__ __launch_bounds__(WK * 64) void linear_few_dma_kernel(LinearArgs a) {
   constexpr int M = GATED ? 2 * NI : NI, W = GATED ? 2 : 1;
@@ -246,9 +248,10 @@ static void few_dma_go(const LinearArgs& a) {
 // Eight waves to a workgroup where there are few; four, with more workgroups to a CU, and two
 // tiles of columns for each reading of the tokens, where there are many.  Measured (us, weights
 // from the last-level cache unless said): 16 x 11008 to 4096 (256 workgroups)
-// 10.0 with eight waves, 11.1 with four; 1 x 4096 to 12288 from HBM 12.9 with two tiles, 13.9 with one,
-// 14.0 with eight waves; 32 x 4096 to 12288 13.5 with one tile of columns, 12.0 with two, to 4096
-// 6.5, 7.4; 64 x 4096 to 12288 22.6, 20.4, to 4096 8.6, 10.5.
+// 11.5 with eight waves, 12.8 with four; 1 x 4096 to 12288 9.6 with two tiles, 9.9 with one, 11.2
+// with eight waves (from HBM 12.9, 13.0, 14.0); gated 4 x 4096 to 11008 19.9 with eight waves, 18.0 with
+// four; 32 x 4096 to 12288 14.0 with one tile of columns, 13.6 with two, to 4096 7.7, 8.8; 64 x 4096 to
+// 12288 23.3, 21.9, to 4096 9.6, 12.0.
 template <bool GATED, int OUT>
 static void few_pick(const LinearArgs& a) {
   const bool many = a.N > 16 * 512;
@@ -282,11 +285,14 @@ hipError_t launch_linear_few(const LinearArgs& a) {
 // less than 2^32 threads in a grid of the smallest tiles (64 x 64, 256 threads)
 bool linear_fits(int64_t T, int64_t N) { return (T + 63) / 64 * ((N + 63) / 64) < (int64_t(1) << 24); }
 
-// Up to 64 rows (16 without the loads straight to LDS), and more of them as further workgroups while
-// two of those go to a CU, one without those loads: their waves split K finer than the tiles' do.  Measured
-// (us, few-row kernel, then tiles; bf16 outputs): 128 x 4096 to 512 7.4, 12.0; to 4096 (512 workgroups) 14.8,
-// 18.8; 192 x 4096 to 4096 (768) 21, 23; 256 28, 25; 512 x 11008 to 1024 (512) 30, 36; K = 4097: 48
-// rows to 1024 (192) 17, 21; 128 to 512 (256) 17, 21; 65 to 1024 (320) 24, 21.
+// Up to 64 rows (16 without the loads straight to LDS), and more of them as further workgroups up to
+// 512, 256 without those loads: their waves split K finer than the tiles' do.  The rings of 33 rows or
+// more take 84 to 102 KB, so one workgroup goes to a CU and more than 256 make a second round.  Measured
+// (us, few-row kernel, then tiles; bf16 outputs): 128 x 4096 to 512 (64 workgroups) 9.1, 10.4; to 2048
+// (256) 9.3, 10.4; 192 x 4096 to 4096 (768) 23, 11; 256 30, 12; K = 4097: 48 rows to 1024 (192) 18.0, 19.1; 128 to
+// 512 (256) 18.2, 19.7; 65 to 1024 (320) 25, 19.  Between 256 and 512 the rule is older than the tiles'
+// present ends, with which they are the faster: 128 x 4096 to 4096 (512) 16.9, 10.8 (fp32 16.9, 15.6); 512 x
+// 11008 to 1024 (512) 34, 29.
 static bool few_takes(const LinearArgs& a, bool dma) {
   const int64_t parts = dma ? (a.T + 63) / 64 : (a.T + 15) / 16;
   return parts == 1 || parts * ((a.N + 15) / 16) <= (dma ? 512 : 256);
@@ -294,8 +300,9 @@ static bool few_takes(const LinearArgs& a, bool dma) {
 
 // A workgroup that makes e4m3 codes has runs of 128 columns whole.  Where that leaves CUs idle, less
 // than 300 tiles of 256 x 128, h goes through memory in fp32 and its codes are made in a second
-// launch.  Measured (us, one launch, then two): 4 x 4096 to 11008 25, 19; 128 72, 43; 400 144, 111; 600
-// (258 tiles) 147, 134; 1000 (344) 209, 217; 1000 x 2048 to 5504 (172) 86, 66.
+// launch.  Measured (us, one launch, then two): 4 x 4096 to 11008 109, 21; 128 109, 43; 400 115, 112; 600
+// (258 tiles) 213, 141; 1000 x 2048 to 5504 (172) 70, 66.  A little above 300, where one launch is a round and a
+// part, two are the faster as well (1000 x 4096 to 11008, 344 tiles: 221, 184), for a workspace of 4 T N bytes.
 size_t linear_workspace(int64_t T, int64_t N) {
   return (T + 255) / 256 * ((N + 127) / 128) < 300 ? static_cast<size_t>(T) * static_cast<size_t>(N) * 4 : 0;
 }

@@ -2,7 +2,8 @@
 // tiles that pass through registers.
 //
 // K that is no multiple of 16 puts rows at odd addresses, which loads straight into LDS do
-// not take.  333 x 1001 to 1000, fp32: 12.5 us, a chain of four runs per group and the launch.
+// not take.  333 x 1001 to 1000, fp32: 12.5 to 13.1 us, a chain of four runs per group, one of them on its way
+// at a time, and the launch; 8192 x 4097 to 12288, bf16: 830 us, 1.0 PFLOP/s.
 #include "linear_tile.hpp"
 
 namespace hyena {
@@ -173,8 +174,10 @@ static void tile_go(const LinearArgs& a) {
 }
 
 // Smaller tiles, whose K two groups of waves share, where those of 128 x 128 leave CUs idle.  Measured
-// (us, fp32 and bf16 outputs, by one group, two, four): 30 x 9662 to 384 59, 48, 45; 333 x 1001 to 1000
-// 15, 13, 14; 500 x 1001 to 4000 -, 28, 37; 700 x 301 to 2000 -, 24, 31.
+// (us, tiles of 64 x 64 by one group, two, four): fp32 30 x 9662 to 384 60, 49, 45; 333 x 1001 to 1000
+// 14.2, 13.5, 14.1; 500 x 1001 to 4000 20, 25, 27; 700 x 301 to 2000 15, 21, 22; bf16 47, 40, 40; 12.8,
+// 12.8, 13.2; 18.1, 18.4, 24; 13.7, 14.2, 20: two gain where K is long for the number of tiles, one where
+// several tiles share a CU.
 hipError_t launch_linear_tile(const LinearArgs& a) {
   const int64_t n128 = (a.T + 127) / 128 * ((a.N + 127) / 128) * (a.gated ? 2 : 1);
   if (a.out == OUT_FP8 && !a.gated) return hipErrorInvalidValue;

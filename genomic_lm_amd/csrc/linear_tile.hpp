@@ -72,8 +72,8 @@ __device__ __forceinline__ void tile_epilogue(const LinearArgs& a, f32x4 (&acc)[
   const int N = a.N;
   const int cg = 4 * (lane >> 4);
   // One decision for all elements where there is one to make: the code of a tile's end is read once
-  // by each CU, and from memory, as the products go through the L2s (8192 x 4096 to 4096, K = 128,
-  // bf16: 27 us with branches at every element, 13 so).
+  // by each CU, and from memory, as the products go through the L2s (4096 x 128 to 4096,
+  // bf16: 27 us with branches at every element, 14 so).
   if constexpr (GATED)
     with_act(a.act, [&](auto act) {
 #pragma unroll

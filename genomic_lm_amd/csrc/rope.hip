@@ -9,8 +9,9 @@
 //     a' = a cos f - b sin f,  b' = b cos f + a sin f,   f = position * inv_freq[i],
 // for the pairs (a, b) = columns (i, i + R / 2) or (2i, 2i + 1) of the first R.
 //
-// Bound by memory: 32768 tokens of 32 + 32 heads of 128 201 to 211 us, 5.1 to 5.3 TB/s; 16 tokens of
-// 32 + 4 heads 6 us in a graph, the chain of a position, its angle and its sine.  The angle of
+// Bound by memory: 32768 tokens of 32 + 32 heads of 128 201 to 216 us by card, 5.0 to 5.3 TB/s (heads of 80, 40
+// turning, whose half is no multiple of 8 and goes element by element, 418, 1.6 TB/s); 16 tokens of
+// 32 + 4 heads 6.7 us in a graph, the chain of a position, its angle and its sine.  The angle of
 // a position up to 2^31 needs 64 bits, once for all heads of a token.  One copy of the loop
 // for queries and keys was slower (251 us).
 #include "fp8.hpp"

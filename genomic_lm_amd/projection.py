@@ -211,7 +211,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=No
     """Queries (T, Hq, DH) and keys (T, Hk, DH), normed per head (eps given) and turned by
     position, in one pass; k may be None.
 
-    positions (T) int32 (negative: the row is left as it is in the output); inv_freq (R / 2) fp32 turns the
+    positions (T) int32 (negative: the row is not written; q_out and k_out keep theirs, in tensors
+    made here it holds no value); inv_freq (R / 2) fp32 turns the
     first R columns, pairs (i, i + R / 2), or (2i, 2i + 1) if interleaved; None: no rotation.
     q_weight, k_weight (DH) fp32 or None (1).  q_out may be q, k_out may be k.  Returns (q_out, k_out)."""
     qp = _heads("q", q)

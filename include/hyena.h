@@ -622,7 +622,7 @@ size_t hyena_attn_paged_workspace_size(int64_t R, int64_t T, int64_t max_q, int6
  *     a scale per block of 128 x 128 (the last ones smaller), the form that
  *     hyena_quantize_weight_fp8 writes.
  * Codes need no alignment; rows of 16-byte alignment load fastest.  N and K up to
- * HYENA_MAX_PROJ_DIM.
+ * HYENA_MAX_PROJ_DIM, ceil(T / 64) ceil(N / 64) below 2^24.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -714,7 +714,8 @@ hyena_status_t hyena_quantize_weight_fp8(const void* w, int64_t w_stride, uint8_
  *                  strides), and must not overlap them or each other
  *                  otherwise; two rows of one output that overlap -> invalid
  *   positions : (T) int32; rows with a negative position (hyena_page_map gives
- *               them to tokens past the last) are neither read nor written.
+ *               them to tokens past the last) are neither read nor written:
+ *               those of q_out and k_out keep what they hold.
  *               NULL with rotary_dim = 0 only.
  *   inv_freq  : (rotary_dim / 2) fp32; scaled positions have it divided
  *   q_weight, k_weight : (DH) fp32, or NULL (1);  eps : finite, >= 0
